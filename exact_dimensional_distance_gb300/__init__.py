@@ -42,6 +42,11 @@ HISS_OPT_REFINE = 2
 HISS_REFINE_CUDA_CORES = 0
 HISS_REFINE_TENSOR_CORES = 1
 HISS_MAX_DIM = 256
+HISS_F32 = 0
+HISS_F16 = 1
+HISS_BF16 = 2
+HISS_MAX_WIDTH = 65536
+HISS_NO_PAD = -(1 << 63)
 
 _i64, _i32, _f32, _p = ctypes.c_int64, ctypes.c_int32, ctypes.c_float, ctypes.c_void_p
 
@@ -77,6 +82,10 @@ class hiss_stats(ctypes.Structure):
                 ("candidates_refined", _i64)]
 
 
+class hiss_tensor(ctypes.Structure):
+    _fields_ = [("in_", _p), ("out", _p), ("n", _i64), ("dtype", _i32), ("reserved", _i32)]
+
+
 def _sig(name, res, args):
     f = getattr(_lib, name)
     f.restype = res
@@ -108,12 +117,23 @@ hiss_gram_tf32 = _sig("hiss_gram_tf32", ctypes.c_int, [_p, _p, _p, _i32, _p])
 hiss_knn = _sig("hiss_knn", ctypes.c_int, [_p, _i32, _f32, _p, _p])
 hiss_join_shard = _sig("hiss_join_shard", ctypes.c_int,
                        [_p, _f32, ctypes.c_size_t, ctypes.POINTER(hiss_out), _i32, _i32])
+hiss_embed = _sig("hiss_embed", ctypes.c_int,
+                  [_p, _p, _i32, _i64, _i32, _i64, _p, _i32, _i64, _i64, _f32, _p, _i32, _i64])
+hiss_embed_grad = _sig("hiss_embed_grad", ctypes.c_int,
+                       [_p, _p, _i32, _i64, _p, _i32, _i64, _i64, _f32, _i64, _i32, _i32, _p, _i32, _i64])
+hiss_layer_norm = _sig("hiss_layer_norm", ctypes.c_int,
+                       [_p, _p, _i32, _i64, _i64, _i32, _p, _p, _i32, _f32, _p, _i32, _i64, _p, _p])
+hiss_layer_norm_grad = _sig("hiss_layer_norm_grad", ctypes.c_int,
+                            [_p, _p, _i32, _i64, _p, _i32, _i64, _p, _p, _p, _i32, _i64, _i32, _p, _i64, _p, _p])
+hiss_clip_grads = _sig("hiss_clip_grads", ctypes.c_int, [_p, ctypes.POINTER(hiss_tensor), _i64, _f32, _p])
+hiss_finish = _sig("hiss_finish", ctypes.c_int, [_p])
 
 EXPORTED = ["hiss_create", "hiss_destroy", "hiss_build", "hiss_build_host", "hiss_count", "hiss_join",
             "hiss_index", "hiss_last_stats", "hiss_launch_count", "hiss_strerror", "hiss_last_cuda_error",
             "hiss_set_option", "hiss_sort_pairs", "hiss_exclusive_scan", "hiss_mask_positions",
             "hiss_exclusive_scan_noalloc", "hiss_work_profile", "hiss_join_queries", "hiss_count_queries",
-            "hiss_gram_tf32", "hiss_knn", "hiss_join_shard"]
+            "hiss_gram_tf32", "hiss_knn", "hiss_join_shard", "hiss_embed", "hiss_embed_grad", "hiss_layer_norm",
+            "hiss_layer_norm_grad", "hiss_clip_grads", "hiss_finish"]
 
 
 class HissError(RuntimeError):
@@ -152,6 +172,81 @@ def _device_tensor(ptr, n, typestr):
         return torch.zeros(0, dtype={"<i8": torch.int64, "<i4": torch.int32, "<u4": torch.int32}[typestr],
                            device="cuda")
     return torch.as_tensor(DeviceArray(ptr, (n,), typestr), device="cuda")
+
+
+def _dtype(t):
+    """The hiss_dtype of a torch dtype."""
+    import torch
+    code = {torch.float32: HISS_F32, torch.float16: HISS_F16, torch.bfloat16: HISS_BF16}.get(t)
+    if code is None:
+        raise ValueError("float32, float16 or bfloat16 expected, not %s" % t)
+    return code
+
+
+def _matrix(t, name):
+    """t as rows of unit column stride, a copy only where its strides need one."""
+    if t.dim() < 1:
+        raise ValueError("%s: at least one dimension expected" % name)
+    m = t if t.dim() == 2 else t.reshape(-1, t.shape[-1])
+    if m.shape[1] < 1 or m.shape[1] > HISS_MAX_WIDTH:
+        raise ValueError("%s: width %d is outside 1..%d" % (name, m.shape[1], HISS_MAX_WIDTH))
+    return m if m.stride(1) == 1 else m.contiguous()
+
+
+def _stride(m):
+    """Row stride of a matrix (the width where a single row's stride says nothing)."""
+    return m.stride(0) if m.shape[0] > 1 else m.shape[1]
+
+
+def _ptr(t):
+    return t.data_ptr() if t is not None else None
+
+
+class Gradients:
+    """Tensors to be clipped together: grads (float32, float16 or bfloat16 CUDA
+    tensors) and optionally the tensors of the same shapes and types that receive the
+    clipped values (default: in place).  Keeps the list that
+    ``Join.clip_grads`` hands to the library, so a step that reuses its gradient
+    tensors builds it once.  Tensors must be dense (contiguous in some
+    order of their dimensions) and must not overlap."""
+
+    def __init__(self, grads, out=None):
+        grads = list(grads)
+        out = grads if out is None else list(out)
+        if len(out) != len(grads):
+            raise ValueError("as many outputs as gradients expected")
+        spans = []
+        self.array = (hiss_tensor * max(1, len(grads)))()
+        for i, (g, o) in enumerate(zip(grads, out)):
+            if not (g.is_cuda and o.is_cuda and g.device == o.device == grads[0].device):
+                raise ValueError("gradient %d: CUDA tensors of one device expected" % i)
+            if g.dtype != o.dtype or g.shape != o.shape or g.stride() != o.stride():
+                raise ValueError("gradient %d: the output's type, shape and strides must be the gradient's" % i)
+            if not self._dense(g):
+                raise ValueError("gradient %d is not dense" % i)
+            n = g.numel()
+            self.array[i] = hiss_tensor(g.data_ptr(), o.data_ptr(), n, _dtype(g.dtype), 0)
+            if n:
+                spans.append((g.data_ptr(), g.data_ptr() + n * g.element_size()))
+                if o.data_ptr() != g.data_ptr():
+                    spans.append((o.data_ptr(), o.data_ptr() + n * o.element_size()))
+        spans.sort()
+        for a, b in zip(spans, spans[1:]):
+            if b[0] < a[1]:
+                raise ValueError("the tensors overlap")
+        self.grads, self.out = grads, out
+
+    @staticmethod
+    def _dense(t):
+        want = 1
+        for size, stride in sorted(((n, s) for n, s in zip(t.shape, t.stride()) if n != 1), key=lambda p: p[1]):
+            if stride != want:
+                return t.numel() == 0
+            want *= size
+        return True
+
+    def __len__(self):
+        return len(self.grads)
 
 
 class Join:
@@ -396,3 +491,158 @@ class Join:
         _check(hiss_mask_positions(self._h, words.data_ptr(), int(nbits), pos.data_ptr(), ctypes.byref(cnt)),
                self._h, "hiss_mask_positions")
         return int(cnt.value)
+
+    # operators between a model's parameters and the points: asynchronous on
+    # the context's stream (``finish`` waits).  Called with another current
+    # stream, that stream's earlier work is waited for on the device first and
+    # its later work waits for the call.
+
+    def _enqueue(self, call, what, tensors):
+        import torch
+        for t in tensors:
+            if t is not None and (not t.is_cuda or t.device != self.stream.device):
+                raise ValueError("%s: CUDA tensors on the context's device expected" % what)
+        cur = torch.cuda.current_stream(self.stream.device)
+        if cur.cuda_stream == self.stream.cuda_stream:
+            _check(call(), self._h, what)
+            return
+        self.stream.wait_stream(cur)
+        _check(call(), self._h, what)
+        for t in tensors:  # keep the allocator from reusing them before the context's stream is done
+            if t is not None:
+                t.record_stream(self.stream)
+        cur.wait_stream(self.stream)
+
+    @staticmethod
+    def _tokens(tokens):
+        import torch
+        if tokens.dtype not in (torch.int32, torch.int64):
+            raise ValueError("int32 or int64 tokens expected, not %s" % tokens.dtype)
+        return tokens.contiguous()
+
+    def embed(self, tokens, table, scale=1.0, pad=None, dtype=None, out=None):
+        """scale * table[tokens] (hiss_embed): tokens int32 or int64 of any
+        shape, table (vocab, width); zeros where tokens == pad.  dtype: the result's
+        type (default: the table's); out: a tensor of shape
+        (*tokens.shape, width) that receives it."""
+        import torch
+        t, w = self._tokens(tokens), _matrix(table, "table")
+        if table.dim() != 2:
+            raise ValueError("table: (vocab, width) expected")
+        if out is None:
+            out = torch.empty((*tokens.shape, w.shape[1]), dtype=dtype or table.dtype, device=table.device)
+        elif out.shape != (*tokens.shape, w.shape[1]) or (dtype is not None and out.dtype != dtype):
+            raise ValueError("out: shape or type differs from the result's")
+        o = self._out_matrix(out, "out")
+        self._enqueue(lambda: hiss_embed(
+            self._h, w.data_ptr(), _dtype(w.dtype), w.shape[0], w.shape[1], _stride(w), t.data_ptr(),
+            8 * t.element_size(), t.numel(), HISS_NO_PAD if pad is None else int(pad), float(scale), o.data_ptr(),
+            _dtype(o.dtype), _stride(o)), "hiss_embed", (t, w, o))
+        return out
+
+    def embed_grad(self, tokens, dy, vocab, scale=1.0, pad=None, dtype=None, out=None, accumulate=False):
+        """Gradient of ``embed`` with respect to its table (hiss_embed_grad):
+        dy (*tokens.shape, width); returns (vocab, width) of the given dtype
+        (default: dy's), or out, to which it is added with accumulate."""
+        import torch
+        t, g = self._tokens(tokens), _matrix(dy, "dy")
+        if dy.shape[:-1] != tokens.shape:
+            raise ValueError("dy: shape (*tokens.shape, width) expected")
+        if out is None:
+            if accumulate:
+                raise ValueError("accumulate needs out")
+            out = torch.empty((int(vocab), g.shape[1]), dtype=dtype or dy.dtype, device=dy.device)
+        elif out.shape != (int(vocab), g.shape[1]) or (dtype is not None and out.dtype != dtype):
+            raise ValueError("out: shape or type differs from the result's")
+        o = self._out_matrix(out, "out")
+        self._enqueue(lambda: hiss_embed_grad(
+            self._h, g.data_ptr(), _dtype(g.dtype), _stride(g), t.data_ptr(), 8 * t.element_size(), t.numel(),
+            HISS_NO_PAD if pad is None else int(pad), float(scale), o.shape[0], g.shape[1], 1 if accumulate else 0,
+            o.data_ptr(), _dtype(o.dtype), _stride(o)), "hiss_embed_grad", (t, g, o))
+        return out
+
+    def layer_norm(self, x, weight=None, bias=None, eps=1e-5, dtype=None, out=None):
+        """Layer norm over the last dimension (hiss_layer_norm): (y, mean,
+        rstd), the statistics float32 of shape x.shape[:-1].  dtype: y's type, x's
+        (default) or float32."""
+        import torch
+        m = _matrix(x, "x")
+        p = self._params(m.shape[1], weight, bias)
+        if out is None:
+            out = torch.empty(x.shape, dtype=dtype or x.dtype, device=x.device)
+        elif out.shape != x.shape or (dtype is not None and out.dtype != dtype):
+            raise ValueError("out: shape or type differs from the result's")
+        o = self._out_matrix(out, "out")
+        mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+        rstd = torch.empty_like(mean)
+        self._enqueue(lambda: hiss_layer_norm(
+            self._h, m.data_ptr(), _dtype(m.dtype), _stride(m), m.shape[0], m.shape[1], _ptr(weight), _ptr(bias), p,
+            float(eps), o.data_ptr(), _dtype(o.dtype), _stride(o), mean.data_ptr(), rstd.data_ptr()),
+            "hiss_layer_norm", (m, weight, bias, o, mean, rstd))
+        return out, mean, rstd
+
+    def layer_norm_grad(self, dy, x, mean, rstd, weight=None, param_dtype=None):
+        """Gradient of ``layer_norm`` (hiss_layer_norm_grad): (dx, dweight,
+        dbias).  dweight and dbias have the weight's type, or param_dtype
+        (default: float32) without a weight."""
+        import torch
+        g, m = _matrix(dy, "dy"), _matrix(x, "x")
+        if dy.shape != x.shape or mean.shape != x.shape[:-1] or rstd.shape != x.shape[:-1]:
+            raise ValueError("dy, mean and rstd do not match x")
+        if mean.dtype != torch.float32 or rstd.dtype != torch.float32:
+            raise ValueError("mean and rstd: float32 expected")
+        p = self._params(m.shape[1], weight, None)
+        pt = weight.dtype if weight is not None else param_dtype or torch.float32
+        if weight is None:
+            p = _dtype(pt)
+        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        dw = torch.empty(m.shape[1], dtype=pt, device=x.device)
+        db = torch.empty_like(dw)
+        mean, rstd = mean.contiguous(), rstd.contiguous()
+        self._enqueue(lambda: hiss_layer_norm_grad(
+            self._h, g.data_ptr(), _dtype(g.dtype), _stride(g), m.data_ptr(), _dtype(m.dtype), _stride(m),
+            mean.data_ptr(), rstd.data_ptr(), _ptr(weight), p, m.shape[0], m.shape[1], dx.data_ptr(), m.shape[1],
+            dw.data_ptr(), db.data_ptr()), "hiss_layer_norm_grad", (g, m, mean, rstd, weight, dx, dw, db))
+        return dx, dw, db
+
+    def clip_grads(self, grads, max_norm):
+        """Clip by the global norm (hiss_clip_grads): grads is a ``Gradients``
+        or a sequence of tensors, clipped in place.  Returns the norm before
+        clipping (float32 CUDA scalar)."""
+        import torch
+        g = grads if isinstance(grads, Gradients) else Gradients(grads)
+        norm = torch.empty((), dtype=torch.float32, device=self.stream.device)
+        self._enqueue(lambda: hiss_clip_grads(self._h, g.array, len(g), float(max_norm), norm.data_ptr()),
+                      "hiss_clip_grads", (norm, *g.grads[:1]) if self._on_stream() else (norm, *g.grads, *g.out))
+        return norm
+
+    def finish(self):
+        """Wait for the context's stream (hiss_finish); raises if a token since
+        the last call was neither padding nor in the table."""
+        _check(hiss_finish(self._h), self._h, "hiss_finish")
+
+    def _on_stream(self):
+        import torch
+        return torch.cuda.current_stream(self.stream.device).cuda_stream == self.stream.cuda_stream
+
+    @staticmethod
+    def _params(width, weight, bias):
+        """The hiss_dtype of weight and bias."""
+        kinds = {t.dtype for t in (weight, bias) if t is not None}
+        if len(kinds) > 1:
+            raise ValueError("weight and bias of one type expected")
+        for t in (weight, bias):
+            if t is not None and (t.shape != (width,) or (width > 1 and t.stride(0) != 1)):
+                raise ValueError("weight and bias: contiguous vectors of %d entries expected" % width)
+        return _dtype(kinds.pop()) if kinds else HISS_F32
+
+    @staticmethod
+    def _out_matrix(t, name):
+        """t as rows without a copy (it is written)."""
+        try:
+            m = t if t.dim() == 2 else t.view(-1, t.shape[-1])
+        except RuntimeError:
+            m = None
+        if m is None or (m.shape[1] > 1 and m.stride(1) != 1):
+            raise ValueError("%s: rows of unit stride expected" % name)
+        return m

@@ -90,6 +90,10 @@ struct hiss_ctx {
     // exact kNN: per-batch pair scratch, done flags, active query ids
     DBuf k_keys, k_vals, k_keys_alt, k_vals_alt, k_sort_tmp, k_d2, k_prow, k_done, k_active;
 
+    // operators on parameters and activations: workspace, and a device int
+    // that records an out-of-range token until hiss_finish reads it
+    DBuf op_tmp, op_flags;
+
     hiss_stats st{};
     cudaEvent_t ev[8] = {};
 };
@@ -1203,6 +1207,62 @@ int do_knn(hiss_ctx *ctx, int32_t k, float eps0, int64_t *out_ids, float *out_d2
     return HISS_E_OVERFLOW;
 }
 
+// ---- operators on parameters and activations ---------------------------------
+
+size_t dtype_size(int dtype) { return dtype == HISS_F32 ? 4 : 2; }
+
+bool dtype_ok(int dtype) { return dtype == HISS_F32 || dtype == HISS_F16 || dtype == HISS_BF16; }
+
+// A range of device memory that a call reads or writes.
+struct Span {
+    uintptr_t lo, hi;
+};
+
+Span span(const void *p, size_t bytes) { return {(uintptr_t)p, (uintptr_t)p + (p ? bytes : 0)}; }
+
+// n rows of width elements, stride elements apart.
+Span span_rows(const void *p, int64_t n, int64_t width, int64_t stride, int dtype)
+{
+    return span(p, n > 0 ? dtype_size(dtype) * (size_t)((n - 1) * stride + width) : 0);
+}
+
+bool overlap(const Span &a, const Span &b) { return a.lo < b.hi && b.lo < a.hi; }
+
+bool aligned(const void *p, size_t bytes) { return (uintptr_t)p % bytes == 0; }
+
+constexpr int64_t kOpMaxRows = int64_t(1) << 30;
+constexpr int64_t kOpMaxStride = int64_t(1) << 30;  // rows (< 2^31) * stride * 4 bytes stays within a size_t
+
+bool rows_ok(const void *p, int dtype, int64_t n, int64_t width, int64_t stride, bool written)
+{
+    if (!dtype_ok(dtype) || !aligned(p, dtype_size(dtype))) return false;
+    if (stride < (written ? width : 0) || stride > kOpMaxStride) return false;
+    return n == 0 || p != nullptr;
+}
+
+int embed_args_ok(const EmbedArgs &a, int64_t rows_n, int64_t out_n)
+{
+    if (a.n < 0 || a.n >= kOpMaxRows || a.vocab < 1 || a.vocab >= (int64_t(1) << 31)) return HISS_E_ARG;
+    if (a.width < 1 || a.width > HISS_MAX_WIDTH || !std::isfinite(a.scale)) return HISS_E_ARG;
+    if (a.token_bits != 32 && a.token_bits != 64) return HISS_E_ARG;
+    if (!aligned(a.tokens, a.token_bits / 8) || (a.n > 0 && !a.tokens)) return HISS_E_ARG;
+    if (!rows_ok(a.rows, a.rows_dtype, rows_n, a.width, a.rows_stride, false)) return HISS_E_ARG;
+    if (!rows_ok(a.out, a.out_dtype, out_n, a.width, a.out_stride, true)) return HISS_E_ARG;
+    const Span o = span_rows(a.out, out_n, a.width, a.out_stride, a.out_dtype);
+    if (overlap(o, span_rows(a.rows, rows_n, a.width, a.rows_stride, a.rows_dtype)) ||
+        overlap(o, span(a.tokens, (size_t)a.n * a.token_bits / 8)))
+        return HISS_E_ARG;
+    return HISS_OK;
+}
+
+int ensure_op_flags(hiss_ctx *ctx)
+{
+    if (ctx->op_flags.p) return HISS_OK;
+    ST(ensure(ctx, ctx->op_flags, sizeof(int) * (kNumFlags + 1)));
+    CK(cudaMemsetAsync(ctx->op_flags.p, 0, sizeof(int) * (kNumFlags + 1), ctx->stream));
+    return HISS_OK;
+}
+
 }  // namespace
 
 // ============================================================================
@@ -1253,7 +1313,7 @@ void hiss_destroy(hiss_ctx *ctx)
                    &ctx->q_bound, &ctx->q_work_key, &ctx->q_cell_idx, &ctx->q_work, &ctx->k_keys,
                    &ctx->k_vals, &ctx->k_keys_alt, &ctx->k_vals_alt, &ctx->k_sort_tmp, &ctx->k_d2, &ctx->k_prow,
                    &ctx->k_done, &ctx->k_active, &ctx->row_ptr2, &ctx->cols2, &ctx->row_ptr_sub, &ctx->unit_tile, &ctx->unit_chunk,
-                   &ctx->query_ids2, &ctx->query_rows2};
+                   &ctx->query_ids2, &ctx->query_rows2, &ctx->op_tmp, &ctx->op_flags};
     if (ctx->copy_stream) cudaStreamSynchronize(ctx->copy_stream);
     for (DBuf *b : all) release(ctx, *b);
     cudaStreamSynchronize(ctx->stream);
@@ -1510,6 +1570,160 @@ int hiss_knn(hiss_ctx *ctx, int32_t k, float eps0, int64_t *d_ids, float *d_dist
     const int rc = do_knn(ctx, k, eps0, d_ids, d_dist2);
     ctx->st.kernel_launches = ctx->launches - launches0;
     return rc;
+}
+
+int hiss_embed(hiss_ctx *ctx, const void *d_table, int32_t table_dtype, int64_t vocab, int32_t width,
+               int64_t table_stride, const void *d_tokens, int32_t token_bits, int64_t n, int64_t pad, float scale,
+               void *d_out, int32_t out_dtype, int64_t out_stride)
+{
+    ST(enter(ctx));
+    EmbedArgs a{d_table, table_dtype, table_stride, d_tokens, token_bits, n, pad, vocab, width, scale,
+                d_out, out_dtype, out_stride, 0, nullptr};
+    ST(embed_args_ok(a, vocab, n));
+    if (n == 0) return HISS_OK;
+    ST(ensure_op_flags(ctx));
+    a.bad = as<int>(ctx->op_flags) + kNumFlags;
+    CK(embed(a, ctx->stream, &ctx->launches));
+    return HISS_OK;
+}
+
+int hiss_embed_grad(hiss_ctx *ctx, const void *d_dy, int32_t dy_dtype, int64_t dy_stride, const void *d_tokens,
+                    int32_t token_bits, int64_t n, int64_t pad, float scale, int64_t vocab, int32_t width,
+                    int32_t accumulate, void *d_grad, int32_t grad_dtype, int64_t grad_stride)
+{
+    ST(enter(ctx));
+    EmbedArgs a{d_dy, dy_dtype, dy_stride, d_tokens, token_bits, n, pad, vocab, width, scale,
+                d_grad, grad_dtype, grad_stride, accumulate, nullptr};
+    if (accumulate != 0 && accumulate != 1) return HISS_E_ARG;
+    ST(embed_args_ok(a, n, vocab));
+    ST(ensure_op_flags(ctx));
+    ST(ensure(ctx, ctx->op_tmp, embed_grad_tmp_bytes(a)));
+    a.bad = as<int>(ctx->op_flags) + kNumFlags;
+    CK(embed_grad(a, ctx->op_tmp.p, as<int>(ctx->op_flags), ctx->stream, &ctx->launches));
+    return HISS_OK;
+}
+
+int hiss_layer_norm(hiss_ctx *ctx, const void *d_x, int32_t x_dtype, int64_t x_stride, int64_t n, int32_t width,
+                    const void *d_weight, const void *d_bias, int32_t param_dtype, float eps, void *d_y,
+                    int32_t y_dtype, int64_t y_stride, float *d_mean, float *d_rstd)
+{
+    ST(enter(ctx));
+    if (n < 0 || n >= kOpMaxRows || width < 1 || width > HISS_MAX_WIDTH) return HISS_E_ARG;
+    if (!(eps >= 0.0f) || std::isinf(eps)) return HISS_E_ARG;
+    if (!rows_ok(d_x, x_dtype, n, width, x_stride, false) || !rows_ok(d_y, y_dtype, n, width, y_stride, true))
+        return HISS_E_ARG;
+    if ((y_dtype != x_dtype && y_dtype != HISS_F32) || !dtype_ok(param_dtype)) return HISS_E_ARG;
+    const size_t ps = dtype_size(param_dtype);
+    if (!aligned(d_weight, ps) || !aligned(d_bias, ps) || !aligned(d_mean, 4) || !aligned(d_rstd, 4)) return HISS_E_ARG;
+    const Span in[] = {span_rows(d_x, n, width, x_stride, x_dtype), span(d_weight, ps * width), span(d_bias, ps * width)};
+    const Span out[] = {span_rows(d_y, n, width, y_stride, y_dtype), span(d_mean, 4 * (size_t)n), span(d_rstd, 4 * (size_t)n)};
+    for (int i = 0; i < 3; ++i)
+        for (int k = 0; k < 3; ++k)
+            if (overlap(out[i], in[k]) || (k < i && overlap(out[i], out[k]))) return HISS_E_ARG;
+    if (n == 0) return HISS_OK;
+    NormArgs a{};
+    a.x = d_x;
+    a.x_dtype = x_dtype;
+    a.y_dtype = y_dtype;
+    a.p_dtype = param_dtype;
+    a.x_stride = x_stride;
+    a.y_stride = y_stride;
+    a.n = n;
+    a.width = width;
+    a.weight = d_weight;
+    a.bias = d_bias;
+    a.eps = eps;
+    a.y = d_y;
+    a.mean = d_mean;
+    a.rstd = d_rstd;
+    CK(layer_norm(a, ctx->stream, &ctx->launches));
+    return HISS_OK;
+}
+
+int hiss_layer_norm_grad(hiss_ctx *ctx, const void *d_dy, int32_t dy_dtype, int64_t dy_stride, const void *d_x,
+                         int32_t x_dtype, int64_t x_stride, const float *d_mean, const float *d_rstd,
+                         const void *d_weight, int32_t param_dtype, int64_t n, int32_t width, void *d_dx,
+                         int64_t dx_stride, void *d_dweight, void *d_dbias)
+{
+    ST(enter(ctx));
+    if (n < 0 || n >= kOpMaxRows || width < 1 || width > HISS_MAX_WIDTH) return HISS_E_ARG;
+    if (!rows_ok(d_x, x_dtype, n, width, x_stride, false) || !rows_ok(d_dy, dy_dtype, n, width, dy_stride, false))
+        return HISS_E_ARG;
+    if (d_dx && !rows_ok(d_dx, x_dtype, n, width, dx_stride, true)) return HISS_E_ARG;
+    if ((dy_dtype != x_dtype && dy_dtype != HISS_F32) || !dtype_ok(param_dtype)) return HISS_E_ARG;
+    const size_t ps = dtype_size(param_dtype);
+    if (!aligned(d_weight, ps) || !aligned(d_dweight, ps) || !aligned(d_dbias, ps) || !aligned(d_mean, 4) ||
+        !aligned(d_rstd, 4) || (n > 0 && (!d_mean || !d_rstd)))
+        return HISS_E_ARG;
+    const Span in[] = {span_rows(d_x, n, width, x_stride, x_dtype), span_rows(d_dy, n, width, dy_stride, dy_dtype),
+                       span(d_weight, ps * width), span(d_mean, 4 * (size_t)n), span(d_rstd, 4 * (size_t)n)};
+    const Span out[] = {d_dx ? span_rows(d_dx, n, width, dx_stride, x_dtype) : span(nullptr, 0),
+                        span(d_dweight, ps * width), span(d_dbias, ps * width)};
+    for (int i = 0; i < 3; ++i) {
+        for (int k = 0; k < 5; ++k)
+            if (overlap(out[i], in[k])) return HISS_E_ARG;
+        for (int k = 0; k < i; ++k)
+            if (overlap(out[i], out[k])) return HISS_E_ARG;
+    }
+    if (!d_dx && !d_dweight && !d_dbias) return HISS_OK;
+    NormArgs a{};
+    a.x = d_x;
+    a.dy = d_dy;
+    a.x_dtype = x_dtype;
+    a.y_dtype = dy_dtype;
+    a.p_dtype = param_dtype;
+    a.x_stride = x_stride;
+    a.y_stride = dy_stride;
+    a.dx_stride = dx_stride;
+    a.n = n;
+    a.width = width;
+    a.weight = d_weight;
+    a.mean = const_cast<float *>(d_mean);
+    a.rstd = const_cast<float *>(d_rstd);
+    a.dx = d_dx;
+    a.dweight = d_dweight;
+    a.dbias = d_dbias;
+    ST(ensure(ctx, ctx->op_tmp, layer_norm_grad_tmp_bytes(a)));
+    CK(layer_norm_grad(a, ctx->op_tmp.p, ctx->stream, &ctx->launches));
+    return HISS_OK;
+}
+
+int hiss_clip_grads(hiss_ctx *ctx, const hiss_tensor *tensors, int64_t count, float max_norm, float *d_norm)
+{
+    ST(enter(ctx));
+    if (count < 0 || (count > 0 && !tensors) || !d_norm || !aligned(d_norm, 4) || !(max_norm >= 0.0f)) return HISS_E_ARG;
+    const Span norm = span(d_norm, 4);
+    int64_t total = 0;
+    for (int64_t i = 0; i < count; ++i) {
+        const hiss_tensor &t = tensors[i];
+        if (t.n < 0 || t.reserved != 0 || !dtype_ok(t.dtype)) return HISS_E_ARG;
+        if (t.n == 0) continue;
+        const size_t es = dtype_size(t.dtype);
+        if (t.n > (int64_t(1) << 50) - total) return HISS_E_ARG;
+        total += t.n;
+        if (!t.in || !aligned(t.in, es) || !aligned(t.out, es)) return HISS_E_ARG;
+        const Span in = span(t.in, es * (size_t)t.n), out = span(t.out, es * (size_t)t.n);
+        if ((t.out && t.out != t.in && overlap(in, out)) || overlap(norm, in) || overlap(norm, out)) return HISS_E_ARG;
+    }
+    ST(ensure(ctx, ctx->op_tmp, clip_tmp_bytes(tensors, count)));
+    CK(clip_grads(tensors, count, max_norm, d_norm, ctx->op_tmp.p, ctx->stream, &ctx->launches));
+    return HISS_OK;
+}
+
+int hiss_finish(hiss_ctx *ctx)
+{
+    ST(enter(ctx));
+    if (!ctx->op_flags.p) return sync(ctx);
+    int h[kNumFlags + 1];
+    CK(cudaMemcpyAsync(h, ctx->op_flags.p, sizeof(h), cudaMemcpyDeviceToHost, ctx->stream));
+    CK(cudaMemsetAsync(ctx->op_flags.p, 0, sizeof(h), ctx->stream));
+    ST(sync(ctx));
+    if (h[kFlagSortTimeout]) {
+        snprintf(ctx->cuda_err, sizeof(ctx->cuda_err), "token sort look-back exceeded its wait limit");
+        ctx->sticky = HISS_E_CUDA;
+        return HISS_E_CUDA;
+    }
+    return h[kNumFlags] ? HISS_E_ARG : HISS_OK;
 }
 
 }  // extern "C"

@@ -229,4 +229,46 @@ cudaError_t refine_tc(const RefineArgs &a, float eps, cudaStream_t s, int64_t *l
 cudaError_t gram_tf32(const float *a, const float *b, int k, float *out, int *flags, cudaStream_t s,
                       int64_t *launches);
 
+// ---- operators on parameters and activations (embed.cu, norm.cu, clip.cu) -------
+// dtypes are hiss_dtype values; strides in elements.
+struct EmbedArgs {
+    const void *rows;      // forward: table; backward: dy
+    int rows_dtype;
+    int64_t rows_stride;
+    const void *tokens;
+    int token_bits;
+    int64_t n, pad, vocab;
+    int width;
+    float scale;
+    void *out;             // forward: [n][width]; backward: [vocab][width]
+    int out_dtype;
+    int64_t out_stride;
+    int accumulate;        // backward: add to out
+    int *bad;              // device int, set to 1 when a token is out of range
+};
+cudaError_t embed(const EmbedArgs &a, cudaStream_t s, int64_t *launches);
+// Workspace of embed_grad in bytes.
+size_t embed_grad_tmp_bytes(const EmbedArgs &a);
+cudaError_t embed_grad(const EmbedArgs &a, void *tmp, int *flags, cudaStream_t s, int64_t *launches);
+
+struct NormArgs {
+    const void *x, *dy;    // dy: backward only
+    int x_dtype, y_dtype, p_dtype;
+    int64_t x_stride, y_stride, dx_stride;
+    int64_t n;
+    int width;
+    const void *weight, *bias;
+    float eps;
+    void *y;               // forward output
+    float *mean, *rstd;    // written by the forward pass, read by the backward pass
+    void *dx, *dweight, *dbias;
+};
+cudaError_t layer_norm(const NormArgs &a, cudaStream_t s, int64_t *launches);
+size_t layer_norm_grad_tmp_bytes(const NormArgs &a);
+cudaError_t layer_norm_grad(const NormArgs &a, void *tmp, cudaStream_t s, int64_t *launches);
+
+size_t clip_tmp_bytes(const hiss_tensor *t, int64_t count);
+cudaError_t clip_grads(const hiss_tensor *t, int64_t count, float max_norm, float *norm, void *tmp, cudaStream_t s,
+                       int64_t *launches);
+
 }  // namespace hiss

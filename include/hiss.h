@@ -65,7 +65,7 @@ typedef struct hiss_ctx hiss_ctx;
 
 /* Create a context on the current CUDA device.  cuda_stream is a
  * cudaStream_t (NULL = the legacy default stream).  The context owns every
- * internal device buffer; none is allocated before the first build. */
+ * internal device buffer; none is allocated before the first call that uses it. */
 int hiss_create(hiss_ctx **out, void *cuda_stream);
 
 /* Free every resource of the context.  NULL is ignored. */
@@ -332,6 +332,106 @@ int hiss_mask_positions(hiss_ctx *ctx, const uint32_t *d_words, int64_t nbits, i
  * tensor-core refinement evaluates (see HISS_OPT_REFINE); exposed to test the
  * tensor-core operand layout. */
 int hiss_gram_tf32(hiss_ctx *ctx, const float *d_a, const float *d_b, int32_t k, float *d_out);
+
+/* ---- operators between a model's parameters and the points ------------------
+ * The points that the join searches are often what a model learns: rows of an
+ * embedding table, normalised; and the pairs the join returns are what it
+ * trains on next.  These calls take token ids to points and a gradient at the
+ * points back to the table.  The paper has no counterpart to them.
+ *
+ * Common to all five
+ *   - They need no dataset (no hiss_build) and leave the context's dataset and
+ *     index alone.
+ *   - They are asynchronous: the work is ordered on the context's stream and
+ *     the call returns without waiting for it.  hiss_finish waits.  Workspace
+ *     belongs to the context, grows on the first call that needs more, and
+ *     counts towards HISS_OPT_ALLOC_LIMIT; a call that allocates nothing new
+ *     can be captured in a CUDA graph.
+ *   - A matrix of n rows has unit column stride and a row stride given in
+ *     elements, at most 2^30: at least the width for what is written, any value
+ *     >= 0 for what is only read (0 repeats one row).  Pointers are aligned to
+ *     their element.  Any alignment and width is accepted; 16-byte aligned
+ *     rows are read and written with 16-byte accesses.
+ *   - What is written must not overlap anything else of the same call
+ *     (HISS_E_ARG), unless a call says otherwise.
+ *   - Sums, means and norms are held in float32 or wider whatever the types,
+ *     and each result is rounded once, to nearest even, when it is stored.
+ *     Results do not depend on scheduling: equal inputs give equal bits. */
+typedef enum { HISS_F32 = 0, HISS_F16 = 1, HISS_BF16 = 2 } hiss_dtype;
+
+#define HISS_MAX_WIDTH 65536
+#define HISS_NO_PAD INT64_MIN /* pad value that no token equals */
+
+/* Embedding lookup: out[i][:] = scale * table[token[i]][:] for n tokens (int32
+ * or int64: token_bits 32 or 64; 0 <= n < 2^30) and a vocab x width table
+ * (1 <= vocab < 2^31, 1 <= width <= HISS_MAX_WIDTH).  A position whose token
+ * equals pad gets a row of zeros (HISS_NO_PAD: none does); so does one whose
+ * token is outside [0, vocab), which the next hiss_finish reports.  scale
+ * must be finite.  The product is rounded from float32 to out_dtype. */
+int hiss_embed(hiss_ctx *ctx, const void *d_table, int32_t table_dtype, int64_t vocab, int32_t width,
+               int64_t table_stride, const void *d_tokens, int32_t token_bits, int64_t n, int64_t pad, float scale,
+               void *d_out, int32_t out_dtype, int64_t out_stride);
+
+/* Gradient of hiss_embed with respect to the table:
+ *   grad[v][:] = scale * sum of dy[i][:] over the positions i with token[i] = v
+ * in float32 and in an order that depends on the positions alone
+ * (the positions are sorted by token; no floating-point atomics).  Padding and
+ * out-of-range tokens contribute nothing (the latter are reported by
+ * hiss_finish).  Every row of grad is written, with zeros for a row without positions;
+ * with accumulate = 1 the sum is added to grad and such rows are left alone. */
+int hiss_embed_grad(hiss_ctx *ctx, const void *d_dy, int32_t dy_dtype, int64_t dy_stride, const void *d_tokens,
+                    int32_t token_bits, int64_t n, int64_t pad, float scale, int64_t vocab, int32_t width,
+                    int32_t accumulate, void *d_grad, int32_t grad_dtype, int64_t grad_stride);
+
+/* Layer norm of n rows (0 <= n < 2^30, 1 <= width <= HISS_MAX_WIDTH):
+ *   mean = sum(x) / width,  rstd = 1 / sqrt(sum((x - mean)^2) / width + eps),
+ *   y = (x - mean) * rstd * weight + bias.
+ * weight and bias (param_dtype, width entries) may be NULL: 1 and 0.  y has
+ * x's type or float32.  d_mean and d_rstd (float32[n], either may be NULL)
+ * receive the statistics that hiss_layer_norm_grad takes.  eps must be finite
+ * and >= 0; a constant row with eps = 0 gives rstd = +inf and NaN, as the
+ * formula does. */
+int hiss_layer_norm(hiss_ctx *ctx, const void *d_x, int32_t x_dtype, int64_t x_stride, int64_t n, int32_t width,
+                    const void *d_weight, const void *d_bias, int32_t param_dtype, float eps, void *d_y,
+                    int32_t y_dtype, int64_t y_stride, float *d_mean, float *d_rstd);
+
+/* Gradient of hiss_layer_norm: with h = (x - mean) * rstd and g = dy * weight,
+ *   dx = rstd * (g - mean(g) - h * mean(g * h)),
+ *   dweight = sum over rows of dy * h,  dbias = sum over rows of dy.
+ * dy has the type y had (dy_dtype: x's type or float32), dx has x's type,
+ * dweight and dbias have param_dtype; any of the three outputs may be NULL
+ * (not computed).  n = 0 gives dweight = dbias = 0. */
+int hiss_layer_norm_grad(hiss_ctx *ctx, const void *d_dy, int32_t dy_dtype, int64_t dy_stride, const void *d_x,
+                         int32_t x_dtype, int64_t x_stride, const float *d_mean, const float *d_rstd,
+                         const void *d_weight, int32_t param_dtype, int64_t n, int32_t width, void *d_dx,
+                         int64_t dx_stride, void *d_dweight, void *d_dbias);
+
+/* One tensor of hiss_clip_grads: n contiguous elements read at in, written at
+ * out (NULL or equal to in: in place). */
+typedef struct {
+    const void *in;
+    void *out;
+    int64_t n;     /* >= 0; 0 is skipped and its pointers are not looked at */
+    int32_t dtype; /* hiss_dtype of in and out */
+    int32_t reserved; /* 0 */
+} hiss_tensor;
+
+/* Clipping by the global gradient norm: N = sqrt(sum of g^2 over every element
+ * of every tensor); *d_norm (device float32) receives N, and each tensor is
+ * multiplied by max_norm / N if N is finite and greater than max_norm, and
+ * by 1 otherwise (nothing is written in place then; an out of its own receives a copy).
+ * Squares that overflow or underflow float32 are summed in float64, so N is
+ * right whenever it is representable (+inf above that, with the factor still
+ * right); an infinity or NaN among the elements gives N = inf or NaN and leaves the
+ * gradients as they are.  max_norm >= 0, +inf allowed (the norm alone).
+ * tensors is a host array, read during the call only; the tensors must not
+ * overlap one another (not checked). */
+int hiss_clip_grads(hiss_ctx *ctx, const hiss_tensor *tensors, int64_t count, float max_norm, float *d_norm);
+
+/* Wait for everything this context has put on its stream.  HISS_E_ARG if an
+ * embedding call since the last hiss_finish met a token that was neither pad nor
+ * in [0, vocab) (the context stays usable). */
+int hiss_finish(hiss_ctx *ctx);
 
 /* ---- allocation-free variant ---------------------------------------------
  * The paper has no counterpart to this entry point; it exists for callers
