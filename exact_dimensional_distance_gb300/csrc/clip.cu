@@ -1,4 +1,19 @@
 // Clipping by the global gradient norm over many tensors.
+//
+//   N = sqrt(sum g^2),  g <- g * max_norm / N  if N is finite and > max_norm.
+//
+// Two launches whatever the number of tensors (up to kMaxTensors; further
+// tensors go to further launches): k_sum_squares leaves one float64 partial sum per
+// block, and every block of k_clip adds all of them up in the same order (a few
+// KB from L2, cheaper than a launch for it), so every block has the same
+// factor.  The list of tensors travels in the kernels' parameters: no copy to
+// the device, nothing to keep alive after the call, and a captured graph holds its own.
+//
+// The work is cut into chunks of one tensor each, dealt out to the blocks in
+// turn.  The norm needs every element before the first write, so a set larger
+// than L2 is read twice: 2 reads and 1 write per element bound it, not 1 and
+// 1.  k_clip takes the chunks in reverse order, so that it starts with what
+// the first pass left in L2.
 #include <algorithm>
 
 #include "hiss_internal.cuh"
@@ -8,87 +23,269 @@ namespace hiss {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kBlocks = 64;  // per tensor
+constexpr int kWarps = kThreads / 32;
+constexpr int kBlocksPerSM = 4;
+constexpr int kMaxBlocks = kSMs * kBlocksPerSM;
+constexpr int kUnroll = 4;         // accesses in flight per thread
+constexpr int kMaxTensors = 1000;  // 29 KB of parameters per launch (the limit is 32,764 bytes)
+constexpr int kFewTensors = 64;
 
-// Partial sums of squares of one tensor, one per block, in float64.
-template <typename T>
-__global__ void __launch_bounds__(kThreads) k_sum_squares(const T *x, int64_t n, double *part)
+template <int CAP>
+struct TensorList {
+    const void *in[CAP];
+    void *out[CAP];
+    int64_t n[CAP];
+    int32_t first[CAP + 1];  // first chunk of each tensor; first[count] = number of chunks
+    uint8_t dtype[CAP];
+    int32_t count;
+    int32_t chunk;           // elements per chunk, a multiple of 2048
+};
+
+// Sum of the squares of a pack in float32.  A result that is not well inside
+// float32's range (some square overflowed or lost bits to underflow) is
+// computed again in float64 and added to *wide; 0 is returned for it.
+// A pack whose sum is at least 2^-80 loses at most 8 * 2^-126 to underflow.
+template <typename T, int E>
+__device__ __forceinline__ float pack_squares(const Pack<T, E> &p, double *wide)
 {
-    __shared__ double warp_sum[kThreads / 32];
-    double s = 0.0;
-    for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < n; i += (int64_t)gridDim.x * kThreads) {
-        const double v = to_f32(x[i]);
-        s += v * v;
+    float s = 0.0f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        const float v = to_f32(p.v[e]);
+        s = fmaf(v, v, s);
     }
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if ((threadIdx.x & 31) == 0) warp_sum[threadIdx.x >> 5] = s;
+    if (!(s >= 0x1p-80f && s <= 0x1p100f)) {
+        double w = 0.0;
+        for (int e = 0; e < E; ++e) {
+            const double v = to_f32(p.v[e]);
+            w += v * v;
+        }
+        *wide += w;
+        s = 0.0f;
+    }
+    return s;
+}
+
+// Sum of squares of x[0 .. n) over the block; each thread returns its share.
+// A float32 sum covers kUnroll packs; above that the sums are float64.
+template <typename T>
+__device__ double chunk_squares(const T *x, int64_t n)
+{
+    constexpr int E = 16 / sizeof(T);
+    double wide = 0.0;
+    float narrow = 0.0f;
+    const int head = (int)min((int64_t)((16 - (reinterpret_cast<uintptr_t>(x) & 15)) & 15) / (int)sizeof(T), n);
+    if ((int)threadIdx.x < head) narrow += pack_squares<T, 1>(load_pack<T, 1>(x + threadIdx.x), &wide);
+    const T *v = x + head;
+    const int packs = (int)((n - head) / E);
+    int i = threadIdx.x;
+    for (; i + (kUnroll - 1) * kThreads < packs; i += kUnroll * kThreads) {
+        Pack<T, E> p[kUnroll];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) p[u] = load_pack<T, E>(v + (int64_t)(i + u * kThreads) * E);
+        float s = 0.0f;
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) s += pack_squares<T, E>(p[u], &wide);
+        wide += (double)s;
+    }
+    for (; i < packs; i += kThreads) narrow += pack_squares<T, E>(load_pack<T, E>(v + (int64_t)i * E), &wide);
+    const int tail = (int)(n - head) - packs * E;
+    if ((int)threadIdx.x < tail)
+        narrow += pack_squares<T, 1>(load_pack<T, 1>(v + (int64_t)packs * E + threadIdx.x), &wide);
+    return wide + (double)narrow;
+}
+
+// The tensor that holds a chunk.
+template <int CAP>
+__device__ __forceinline__ int tensor_of(const TensorList<CAP> &l, int chunk)
+{
+    int lo = 0, hi = l.count;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (l.first[mid] <= chunk) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+
+// Sum of v over the block, the same bits in every thread.
+__device__ __forceinline__ double block_sum(double v)
+{
+    __shared__ double part[kWarps];
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
     __syncthreads();
-    if (threadIdx.x == 0) {
-        for (int w = 1; w < kThreads / 32; ++w) s += warp_sum[w];
-        part[blockIdx.x] = s;
+    double s = 0.0;
+    for (int w = 0; w < kWarps; ++w) s += part[w];
+    return s;
+}
+
+template <int CAP>
+__global__ void __launch_bounds__(kThreads) k_sum_squares(const __grid_constant__ TensorList<CAP> l, double *part)
+{
+    wait_for_previous();
+    double s = 0.0;
+    const int chunks = l.first[l.count];
+    for (int c = blockIdx.x; c < chunks; c += gridDim.x) {
+        const int t = tensor_of(l, c);
+        const int64_t at = (int64_t)(c - l.first[t]) * l.chunk, n = min((int64_t)l.chunk, l.n[t] - at);
+        if (l.dtype[t] == HISS_F32) s += chunk_squares(static_cast<const float *>(l.in[t]) + at, n);
+        else if (l.dtype[t] == HISS_F16) s += chunk_squares(static_cast<const __half *>(l.in[t]) + at, n);
+        else s += chunk_squares(static_cast<const __nv_bfloat16 *>(l.in[t]) + at, n);
+    }
+    s = block_sum(s);
+    if (threadIdx.x == 0) part[blockIdx.x] = s;
+    let_next_start();
+}
+
+template <typename T>
+__device__ void chunk_scale(const T *x, T *y, int64_t n, float f)
+{
+    constexpr int E = 16 / sizeof(T);
+    const int off = (int)(reinterpret_cast<uintptr_t>(x) & 15);
+    if (off != (int)(reinterpret_cast<uintptr_t>(y) & 15)) {  // no common 16-byte alignment
+        for (int64_t i = threadIdx.x; i < n; i += kThreads) y[i] = f == 1.0f ? x[i] : from_f32<T>(to_f32(x[i]) * f);
+        return;
+    }
+    const int head = (int)min((int64_t)((16 - off) & 15) / (int)sizeof(T), n);
+    if ((int)threadIdx.x < head)
+        y[threadIdx.x] = f == 1.0f ? x[threadIdx.x] : from_f32<T>(to_f32(x[threadIdx.x]) * f);
+    const T *v = x + head;
+    T *w = y + head;
+    const int packs = (int)((n - head) / E);
+    int i = threadIdx.x;
+    auto scaled = [f](Pack<T, E> p) {
+        if (f != 1.0f)  // a factor of 1 copies the bits, NaN and infinities included
+#pragma unroll
+            for (int e = 0; e < E; ++e) p.v[e] = from_f32<T>(to_f32(p.v[e]) * f);
+        return p;
+    };
+    for (; i + (kUnroll - 1) * kThreads < packs; i += kUnroll * kThreads) {
+        Pack<T, E> p[kUnroll];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) p[u] = load_pack<T, E>(v + (int64_t)(i + u * kThreads) * E);
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) store_pack<T, E>(w + (int64_t)(i + u * kThreads) * E, scaled(p[u]));
+    }
+    for (; i < packs; i += kThreads) store_pack<T, E>(w + (int64_t)i * E, scaled(load_pack<T, E>(v + (int64_t)i * E)));
+    const int tail = (int)(n - head) - packs * E;
+    if ((int)threadIdx.x < tail) {
+        const int64_t at = (int64_t)packs * E + threadIdx.x;
+        w[at] = f == 1.0f ? v[at] : from_f32<T>(to_f32(v[at]) * f);
     }
 }
 
-// The norm from the partial sums, and the factor of every gradient.
-__global__ void __launch_bounds__(kThreads) k_clip_factor(const double *part, int64_t n, float max_norm, float *norm,
-                                                          float *factor)
+template <int CAP>
+__global__ void __launch_bounds__(kThreads) k_clip(const __grid_constant__ TensorList<CAP> l, const double *part, int parts,
+                                                   float max_norm, float *norm)
 {
-    __shared__ double sum[kThreads];
+    wait_for_previous();
     double s = 0.0;
-    for (int64_t i = threadIdx.x; i < n; i += kThreads) s += part[i];
-    sum[threadIdx.x] = s;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        for (int i = 1; i < kThreads; ++i) s += sum[i];
-        const double v = sqrt(s);
-        *norm = (float)v;
-        *factor = isfinite(v) && v > (double)max_norm ? (float)((double)max_norm / v) : 1.0f;
+    for (int i = threadIdx.x; i < parts; i += kThreads) s += part[i];
+    const double total = sqrt(block_sum(s));
+    const float f = isfinite(total) && total > (double)max_norm ? (float)((double)max_norm / total) : 1.0f;
+    if (blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)total;
+    const int chunks = l.first[l.count];
+    for (int i = blockIdx.x; i < chunks; i += gridDim.x) {
+        const int c = chunks - 1 - i;
+        const int t = tensor_of(l, c);
+        if (f == 1.0f && l.in[t] == l.out[t]) continue;
+        const int64_t at = (int64_t)(c - l.first[t]) * l.chunk, n = min((int64_t)l.chunk, l.n[t] - at);
+        if (l.dtype[t] == HISS_F32)
+            chunk_scale(static_cast<const float *>(l.in[t]) + at, static_cast<float *>(l.out[t]) + at, n, f);
+        else if (l.dtype[t] == HISS_F16)
+            chunk_scale(static_cast<const __half *>(l.in[t]) + at, static_cast<__half *>(l.out[t]) + at, n, f);
+        else
+            chunk_scale(static_cast<const __nv_bfloat16 *>(l.in[t]) + at, static_cast<__nv_bfloat16 *>(l.out[t]) + at, n, f);
     }
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads) k_scale(const T *x, T *y, int64_t n, const float *factor)
+// The next up to CAP tensors of t from *i on; tensors without elements are
+// skipped, those behind the last one taken too.
+template <int CAP>
+void fill(TensorList<CAP> &l, const hiss_tensor *t, int64_t count, int64_t *i, int64_t chunk)
 {
-    const float f = *factor;
-    if (f == 1.0f && x == y) return;
-    for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < n; i += (int64_t)gridDim.x * kThreads)
-        y[i] = f == 1.0f ? x[i] : from_f32<T>(to_f32(x[i]) * f);
+    l.chunk = (int32_t)chunk;
+    l.count = 0;
+    l.first[0] = 0;
+    int64_t chunks = 0;
+    for (; *i < count && l.count < CAP; ++*i) {
+        const hiss_tensor &e = t[*i];
+        if (e.n == 0) continue;
+        const int k = l.count++;
+        l.in[k] = e.in;
+        l.out[k] = e.out ? e.out : const_cast<void *>(e.in);
+        l.n[k] = e.n;
+        l.dtype[k] = (uint8_t)e.dtype;
+        chunks += (e.n + chunk - 1) / chunk;
+        l.first[k + 1] = (int32_t)chunks;
+    }
+    while (*i < count && t[*i].n == 0) ++*i;
+}
+
+struct Plan {
+    int64_t used = 0;    // tensors with elements
+    int64_t lists = 0;   // launches of each kernel
+    int64_t chunk = 0;
+};
+
+// Chunks are 2^11 to 2^15 elements (above that only so that a tensor's chunk
+// count fits 32 bits): small enough that a small set reaches every block,
+// large enough that finding the chunk's tensor costs nothing.
+Plan plan(const hiss_tensor *t, int64_t count)
+{
+    Plan p;
+    int64_t total = 0;
+    for (int64_t i = 0; i < count; ++i) {
+        total += t[i].n;
+        p.used += t[i].n > 0;
+    }
+    p.lists = (p.used + kMaxTensors - 1) / kMaxTensors;
+    p.chunk = 1 << 11;
+    while (p.chunk < (1 << 15) && total > p.chunk * kMaxBlocks) p.chunk <<= 1;
+    while (total / p.chunk > (1 << 28)) p.chunk <<= 1;
+    return p;
+}
+
+template <int CAP>
+cudaError_t run(const hiss_tensor *t, int64_t count, const Plan &p, float max_norm, float *norm, double *part,
+                cudaStream_t s, int64_t *launches)
+{
+    TensorList<CAP> l;
+    int parts = 0;
+    int64_t i = 0;
+    do {
+        fill(l, t, count, &i, p.chunk);
+        const int blocks = std::max(1, std::min(kMaxBlocks, l.first[l.count]));
+        HISS_TRY(launch_after(k_sum_squares<CAP>, blocks, kThreads, 0, s, l, part + parts));
+        parts += blocks;
+        ++*launches;
+    } while (i < count);
+    i = 0;
+    do {
+        if (p.lists > 1) fill(l, t, count, &i, p.chunk);
+        else i = count;
+        const int blocks = std::max(1, std::min(kMaxBlocks, l.first[l.count]));
+        HISS_TRY(launch_after(k_clip<CAP>, blocks, kThreads, 0, s, l, part, parts, max_norm, norm));
+        ++*launches;
+    } while (i < count);
+    return cudaSuccess;
 }
 
 }  // namespace
 
-size_t clip_tmp_bytes(const hiss_tensor *, int64_t count) { return 8 * (size_t)(count * kBlocks) + 16; }
+size_t clip_tmp_bytes(const hiss_tensor *t, int64_t count)
+{
+    return 8 * (size_t)kMaxBlocks * (size_t)std::max<int64_t>(1, plan(t, count).lists);
+}
 
 cudaError_t clip_grads(const hiss_tensor *t, int64_t count, float max_norm, float *norm, void *tmp, cudaStream_t s,
                        int64_t *launches)
 {
-    double *part = static_cast<double *>(tmp) + 2;
-    float *factor = static_cast<float *>(tmp);
-    int64_t used = 0;
-    for (int64_t i = 0; i < count; ++i) {
-        if (t[i].n == 0) continue;
-        HISS_TRY(with_dtype(t[i].dtype, [&](auto e) {
-            using T = decltype(e);
-            k_sum_squares<T><<<kBlocks, kThreads, 0, s>>>(static_cast<const T *>(t[i].in), t[i].n, part + used * kBlocks);
-            return cudaGetLastError();
-        }));
-        ++used;
-    }
-    k_clip_factor<<<1, kThreads, 0, s>>>(part, used * kBlocks, max_norm, norm, factor);
-    *launches += used + 1;
-    for (int64_t i = 0; i < count; ++i) {
-        if (t[i].n == 0) continue;
-        HISS_TRY(with_dtype(t[i].dtype, [&](auto e) {
-            using T = decltype(e);
-            const T *in = static_cast<const T *>(t[i].in);
-            T *out = t[i].out ? static_cast<T *>(t[i].out) : const_cast<T *>(in);
-            k_scale<T><<<(unsigned)std::min<int64_t>(152 * 8, (t[i].n + kThreads - 1) / kThreads), kThreads, 0, s>>>(
-                in, out, t[i].n, factor);
-            return cudaGetLastError();
-        }));
-        ++*launches;
-    }
-    return cudaGetLastError();
+    const Plan p = plan(t, count);
+    double *part = static_cast<double *>(tmp);
+    if (p.used <= kFewTensors) return run<kFewTensors>(t, count, p, max_norm, norm, part, s, launches);
+    return run<kMaxTensors>(t, count, p, max_norm, norm, part, s, launches);
 }
 
 }  // namespace hiss

@@ -1,14 +1,19 @@
 // Element types of the operators on parameters and activations: conversions
-// between float32, float16 and bfloat16 (round to nearest even) and the
-// dispatch from hiss_dtype values to types.
+// between float32, float16 and bfloat16 (round to nearest even), the dispatch
+// from hiss_dtype values to types, and packs of elements that are read or
+// written with one access.
 #pragma once
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "hiss.h"
 
 namespace hiss {
+
+constexpr int kSMs = 152;  // GB300
 
 __device__ __forceinline__ float to_f32(float v) { return v; }
 __device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
@@ -32,12 +37,48 @@ cudaError_t with_dtype(int dtype, F &&f)
     return f(__nv_bfloat16{});
 }
 
-// Element i of an array of a type known at run time (parameters, read once per block).
+inline size_t dtype_bytes(int dtype) { return dtype == HISS_F32 ? 4 : 2; }
+
+// E elements in accesses of up to 16 bytes.
+template <typename T, int E>
+struct alignas(sizeof(T) * E < 16 ? sizeof(T) * E : 16) Pack {
+    T v[E];
+};
+
+template <typename T, int E>
+__device__ __forceinline__ Pack<T, E> load_pack(const T *p)
+{
+    return *reinterpret_cast<const Pack<T, E> *>(p);
+}
+template <typename T, int E>
+__device__ __forceinline__ void store_pack(T *p, const Pack<T, E> &v)
+{
+    *reinterpret_cast<Pack<T, E> *>(p) = v;
+}
+
+// E consecutive parameters of a type known at run time (read once per block).
+template <int E>
+__device__ __forceinline__ void load_params(const void *p, int dtype, int64_t i, float (&v)[E])
+{
+    if (dtype == HISS_F32) {
+        const auto k = load_pack<float, E>(static_cast<const float *>(p) + i);
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[e] = k.v[e];
+    } else if (dtype == HISS_F16) {
+        const auto k = load_pack<__half, E>(static_cast<const __half *>(p) + i);
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[e] = to_f32(k.v[e]);
+    } else {
+        const auto k = load_pack<__nv_bfloat16, E>(static_cast<const __nv_bfloat16 *>(p) + i);
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[e] = to_f32(k.v[e]);
+    }
+}
 __device__ __forceinline__ float load_any(const void *p, int dtype, int64_t i)
 {
-    if (dtype == HISS_F32) return static_cast<const float *>(p)[i];
-    if (dtype == HISS_F16) return to_f32(static_cast<const __half *>(p)[i]);
-    return to_f32(static_cast<const __nv_bfloat16 *>(p)[i]);
+    float v[1];
+    load_params<1>(p, dtype, i, v);
+    return v[0];
 }
 __device__ __forceinline__ void store_any(void *p, int dtype, int64_t i, float v)
 {
@@ -45,5 +86,36 @@ __device__ __forceinline__ void store_any(void *p, int dtype, int64_t i, float v
     else if (dtype == HISS_F16) static_cast<__half *>(p)[i] = from_f32<__half>(v);
     else static_cast<__nv_bfloat16 *>(p)[i] = from_f32<__nv_bfloat16>(v);
 }
+
+// Whether rows of a matrix can be accessed E elements at a time.
+inline bool rows_aligned(const void *p, int64_t stride, int dtype, int e)
+{
+    const size_t b = dtype_bytes(dtype) * e < 16 ? dtype_bytes(dtype) * e : 16;
+    return reinterpret_cast<uintptr_t>(p) % b == 0 && (stride * dtype_bytes(dtype)) % b == 0;
+}
+
+// ---- launches that overlap the kernel before them ---------------------------
+// A kernel launched with launch_after may start while the kernel before it on
+// the stream is finishing; it calls wait_for_previous before it touches
+// anything that kernel writes.
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*kernel)(P...), unsigned grid, unsigned block, size_t smem, cudaStream_t s, A... args)
+{
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+__device__ __forceinline__ void wait_for_previous() { cudaGridDependencySynchronize(); }
+// Lets the dependent kernel start launching (its wait still covers everything
+// this kernel writes).
+__device__ __forceinline__ void let_next_start() { cudaTriggerProgrammaticLaunchCompletion(); }
 
 }  // namespace hiss
