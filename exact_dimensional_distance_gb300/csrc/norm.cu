@@ -1,41 +1,579 @@
 // Layer norm, forward and backward.
+//
+//   forward    m = mean(x), r = 1 / sqrt(mean((x - m)^2) + eps), y = (x - m) r w + b
+//   backward   h = (x - m) r, g = dy w:  dx = r (g - mean(g) - h mean(g h)),
+//              dw = sum over rows of dy h,  db = sum over rows of dy
+//
+// Both are bound by memory: 2 (forward) and 3 (backward) elements moved per
+// element, a dozen float32 operations.  A group of lanes owns a row, NV packs of
+// E elements per lane, so that everything is read from memory once.  A group is
+// a power of two of lanes inside a warp (narrow rows, several per warp), or
+// whole warps that meet at a named barrier once per row.  Blocks are persistent:
+// the weights (and in the backward pass each lane's column sums of dw and
+// db) stay in registers from row to row.  Each thread copies its own packs
+// of the rows to come into its own slots of a shared-memory ring
+// (cp.async), so no barrier guards the ring and the loads in flight cost no
+// registers.  Rows too wide for a group of kMaxLanes go through the looping
+// kernels at the end of the file.
+#include <algorithm>
+#include <atomic>
+
 #include "hiss_internal.cuh"
 #include "numeric.cuh"
+#include "ptx.cuh"
 
 namespace hiss {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kMaxLanes = 512;  // of a group, and threads of a block
+constexpr int kMaxWarps = kMaxLanes / 32;
+constexpr int kRingBytes = 208 * 1024;  // shared memory that a ring of a full block may take
 
-// Sum of v over the block, returned to every thread.
-__device__ __forceinline__ float block_sum(float v)
+// ---- groups ---------------------------------------------------------------------
+
+struct Group {
+    int lanes, id, lane;   // lanes per group; this thread's group in the block and lane in the group
+    int warps, warp;       // warps per group and this thread's warp in the group (NARROW: 1 and 0)
+};
+
+template <bool NARROW>
+__device__ __forceinline__ Group group_of(int lanes)
 {
-    __shared__ float part[kThreads / 32];
+    Group g;
+    g.lanes = lanes;
+    g.id = threadIdx.x / lanes;
+    g.lane = threadIdx.x - g.id * lanes;
+    g.warps = NARROW ? 1 : lanes >> 5;
+    g.warp = NARROW ? 0 : g.lane >> 5;
+    return g;
+}
+
+// First column of a lane; its pack v is E * (NARROW ? lanes : 32) * v further on,
+// so that a warp of a wide group owns consecutive columns.
+template <bool NARROW, int E, int NV>
+__device__ __forceinline__ int column_of(const Group &g)
+{
+    return NARROW ? g.lane * E : (g.warp * 32 * NV + (g.lane & 31)) * E;
+}
+
+__device__ __forceinline__ void group_barrier(const Group &g)
+{
+    asm volatile("bar.sync %0, %1;" ::"r"(g.id + 1), "r"(g.lanes) : "memory");
+}
+
+// Sum over the group's lanes of this warp.
+template <bool NARROW>
+__device__ __forceinline__ float warp_sum(const Group &g, float v)
+{
+    if (NARROW) {
+        for (int o = g.lanes >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    } else {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    }
+    return v;
+}
+
+// One float2 per warp of a group, double-buffered by parity so that one
+// barrier per row is enough: a warp that writes a buffer again has passed the
+// barrier of the row between, which every reader of the buffer's old contents
+// had reached.
+struct Exchange {
+    float2 slot[2][kMaxWarps];
+};
+
+// ---- the rows to come -------------------------------------------------------------
+
+// S rows ahead of one operand in this thread's slots of shared memory.  Packs
+// below 4 bytes (16-bit elements of rows without 4-byte alignment) cannot be
+// copied asynchronously and are held in registers, one row ahead.
+template <typename T, int E, int NV, int S>
+struct Stream {
+    using P = Pack<T, E>;
+    static constexpr bool kAsync = sizeof(P) >= 4 && (sizeof(T) * E) % 4 == 0;
+    static constexpr size_t kThreadBytes = kAsync ? sizeof(P) * NV * S : 0;
+    P *slot;
+    P cur[kAsync ? 1 : NV], next[kAsync ? 1 : NV];
+
+    // base: the block's part of shared memory for this operand
+    __device__ __forceinline__ void open(char *base) { slot = reinterpret_cast<P *>(base) + threadIdx.x; }
+
+    // Start the copy of pack v of a row into stage st.
+    __device__ __forceinline__ void fetch(int st, int v, const T *p)
+    {
+        if constexpr (kAsync) {
+            char *d = reinterpret_cast<char *>(slot + (st * NV + v) * blockDim.x);
+            const char *q = reinterpret_cast<const char *>(p);
+            if constexpr (sizeof(T) * E >= 16) {
+#pragma unroll
+                for (size_t i = 0; i < sizeof(T) * E; i += 16) cp_async16(d + i, q + i);
+            } else if constexpr (sizeof(T) * E == 8) {
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(d)), "l"(q) : "memory");
+            } else {
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(d)), "l"(q) : "memory");
+            }
+        } else {
+            next[v] = load_pack<T, E>(p);
+        }
+    }
+    __device__ __forceinline__ P get(int st, int v) const
+    {
+        if constexpr (kAsync) return slot[(st * NV + v) * blockDim.x];
+        else return cur[v];
+    }
+    // Make the row fetched last the current one (register form).
+    __device__ __forceinline__ void turn()
+    {
+        if constexpr (!kAsync)
+#pragma unroll
+            for (int v = 0; v < NV; ++v) cur[v] = next[v];
+    }
+};
+
+// Rows in flight per thread: what fits kRingBytes, at most 4.
+constexpr int stages(size_t row_bytes)
+{
+    const int s = (int)(kRingBytes / (kMaxLanes * row_bytes));
+    return s > 4 ? 4 : s;
+}
+
+// ---- geometry -----------------------------------------------------------------
+
+struct Rows {
+    int e = 0, nv = 0;     // elements per pack, packs per lane; e = 0: looping kernels
+    int lanes = 0, groups = 0;
+    bool narrow = false;
+};
+
+// The widest pack that the width and every row's alignment allow; 16 elements
+// per lane, or 32 where that is too few and the caller has such a kernel; as
+// many groups per block as reach the given threads without leaving SMs idle.
+Rows plan_rows(const NormArgs &a, bool has32, int threads)
+{
+    const bool half = a.x_dtype != HISS_F32;
+    auto fits = [&](int e) {
+        if (a.width % e) return false;
+        bool ok = rows_aligned(a.x, a.x_stride, a.x_dtype, e) && rows_aligned(a.weight, 0, a.p_dtype, e) &&
+                  rows_aligned(a.bias, 0, a.p_dtype, e);
+        if (a.y) ok = ok && rows_aligned(a.y, a.y_stride, a.y_dtype, e);
+        if (a.dy) ok = ok && rows_aligned(a.dy, a.y_stride, a.y_dtype, e);
+        if (a.dx) ok = ok && rows_aligned(a.dx, a.dx_stride, a.x_dtype, e);
+        return ok;
+    };
+    const int wide = half ? 8 : 4;
+    Rows r;
+    const int e = fits(wide) ? wide : half && fits(2) ? 2 : 1;
+    int per = 16;
+    if (has32 && e == wide && a.width > per * kMaxLanes) per = 32;
+    const int lanes = (a.width + per - 1) / per;
+    if (lanes > kMaxLanes) return r;
+    r.e = e;
+    r.nv = per / e;
+    r.narrow = lanes <= 16;
+    if (r.narrow) {
+        r.lanes = 1;
+        while (r.lanes < lanes) r.lanes <<= 1;
+        r.groups = 32 / r.lanes;
+    } else {
+        r.lanes = (lanes + 31) & ~31;
+        r.groups = 1;
+    }
+    while (2 * r.groups * r.lanes <= threads && (int64_t)r.groups * kSMs < a.n) r.groups <<= 1;
+    return r;
+}
+
+// Resident blocks per SM of a kernel at a block size and its shared memory,
+// asked for once (and the kernel is allowed that much shared memory).
+struct Residency {
+    std::atomic<int> blocks[kMaxWarps + 1];
+};
+template <typename K>
+int resident(K kernel, int threads, size_t smem, Residency &cache)
+{
+    std::atomic<int> &c = cache.blocks[threads / 32];
+    int v = c.load(std::memory_order_acquire);
+    if (v == 0) {
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 220 * 1024) != cudaSuccess ||
+            cudaOccupancyMaxActiveBlocksPerMultiprocessor(&v, kernel, threads, smem) != cudaSuccess || v < 1)
+            v = 1;
+        c.store(v, std::memory_order_release);
+    }
+    return v;
+}
+
+// ---- forward --------------------------------------------------------------------
+
+template <typename TX, typename TY, int E, int NV, bool NARROW>
+struct Forward {
+    static constexpr int kStages = stages(sizeof(TX) * E * NV);
+    using X = Stream<TX, E, NV, kStages>;
+    static constexpr size_t kThreadBytes = X::kThreadBytes;
+};
+
+template <typename TX, typename TY, int E, int NV, bool NARROW>
+__global__ void __launch_bounds__(kMaxLanes) k_norm(NormArgs a, int lanes, int groups)
+{
+    using F = Forward<TX, TY, E, NV, NARROW>;
+    constexpr int S = F::kStages, C = NV * E;
+    extern __shared__ __align__(16) char ring[];
+    __shared__ Exchange ex[kMaxWarps];
+    const Group g = group_of<NARROW>(lanes);
+    const int col = column_of<NARROW, E, NV>(g);
+    const int vs = E * (NARROW ? lanes : 32);
+    float w[C], b[C];
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+        float t[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) w[v * E + e] = 1.0f, b[v * E + e] = 0.0f;
+        if (col + v * vs >= a.width) continue;
+        if (a.weight) {
+            load_params<E>(a.weight, a.p_dtype, col + v * vs, t);
+#pragma unroll
+            for (int e = 0; e < E; ++e) w[v * E + e] = t[e];
+        }
+        if (a.bias) {
+            load_params<E>(a.bias, a.p_dtype, col + v * vs, t);
+#pragma unroll
+            for (int e = 0; e < E; ++e) b[v * E + e] = t[e];
+        }
+    }
+    const float width = (float)a.width;
+    // columns of this thread's warp, and of warp (lane id) of the group
+    auto columns = [&](int i) { return (float)min(max(a.width - i * 32 * C, 0), 32 * C); };
+    const float my_n = NARROW ? width : columns(g.warp), lane_n = NARROW ? 0.0f : columns(threadIdx.x & 31);
+    const int64_t step = (int64_t)gridDim.x * groups;
+    int64_t row = (int64_t)blockIdx.x * groups + g.id;
+    // the loop runs for whole warps: as long as the warp's first row exists
+    int64_t first = row - (NARROW ? (threadIdx.x & 31) / lanes : 0);
+    typename F::X xs;
+    xs.open(ring);
+    auto fetch = [&](int st, int64_t r) {
+        if (r < a.n) {
+            const TX *p = static_cast<const TX *>(a.x) + r * a.x_stride + col;
+#pragma unroll
+            for (int v = 0; v < NV; ++v)
+                if (col + v * vs < a.width) xs.fetch(st, v, p + v * vs);
+        }
+        cp_async_commit();
+    };
+    if constexpr (F::X::kAsync) {
+#pragma unroll
+        for (int i = 0; i < S - 1; ++i) fetch(i, row + i * step);
+    } else {
+        fetch(0, row);
+    }
+    int st = 0;
+    for (int parity = 0; first < a.n; first += step, row += step, parity ^= 1) {
+        if constexpr (F::X::kAsync) {
+            fetch(st == 0 ? S - 1 : st - 1, row + (S - 1) * step);
+            cp_async_wait<S - 1>();
+        } else {
+            xs.turn();
+            fetch(0, row + step);
+        }
+        float x[C];
+        float s = 0.0f;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            const auto p = xs.get(st, v);
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                x[v * E + e] = to_f32(p.v[e]);
+                if (col + v * vs < a.width) s += x[v * E + e];
+            }
+        }
+        // mean and sum of squared differences of the warp's columns, then of the
+        // row from those of its warps: M2 = sum of (M2_w + n_w (m_w - m)^2)
+        float mean = my_n > 0.0f ? warp_sum<NARROW>(g, s) / my_n : 0.0f;
+        float q = 0.0f;
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const float d = x[v * E + e] - mean;
+                if (col + v * vs < a.width) q = fmaf(d, d, q);
+            }
+        q = warp_sum<NARROW>(g, q);
+        if (!NARROW && g.warps > 1) {
+            float2 *slot = ex[g.id].slot[parity];
+            if ((threadIdx.x & 31) == 0) slot[g.warp] = make_float2(mean, q);
+            group_barrier(g);
+            const float2 mine = (threadIdx.x & 31) < g.warps ? slot[threadIdx.x & 31] : make_float2(0.0f, 0.0f);
+            mean = warp_sum<NARROW>(g, lane_n * mine.x) / width;
+            const float d = mine.x - mean;
+            q = warp_sum<NARROW>(g, lane_n > 0.0f ? fmaf(lane_n * d, d, mine.y) : 0.0f);
+        }
+        const float rstd = 1.0f / sqrtf(q / width + a.eps);
+        if (row < a.n) {
+            TY *y = static_cast<TY *>(a.y) + row * a.y_stride + col;
+#pragma unroll
+            for (int v = 0; v < NV; ++v) {
+                if (col + v * vs >= a.width) continue;
+                Pack<TY, E> o;
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+                    o.v[e] = from_f32<TY>(fmaf((x[v * E + e] - mean) * rstd, w[v * E + e], b[v * E + e]));
+                store_pack<TY, E>(y + v * vs, o);
+            }
+            if (g.lane == 0) {
+                if (a.mean) a.mean[row] = mean;
+                if (a.rstd) a.rstd[row] = rstd;
+            }
+        }
+        st = st == S - 1 ? 0 : st + 1;
+    }
+}
+
+// ---- backward -------------------------------------------------------------------
+
+template <typename TX, typename TY, int E, int NV>
+struct Backward {
+    static constexpr int kStages = stages((sizeof(TX) + sizeof(TY)) * E * NV);
+    using X = Stream<TX, E, NV, kStages>;
+    using Y = Stream<TY, E, NV, kStages>;
+    static constexpr size_t kThreadBytes = X::kThreadBytes + Y::kThreadBytes;
+};
+
+// Each block leaves its column sums in part[block][0 .. width) (dw) and
+// [width .. 2 width) (db): k_norm_param adds the blocks up.
+template <typename TX, typename TY, int E, int NV, bool NARROW>
+__global__ void __launch_bounds__(kMaxLanes) k_norm_grad(NormArgs a, int lanes, int groups, float *part)
+{
+    using B = Backward<TX, TY, E, NV>;
+    constexpr int S = B::kStages, C = NV * E;
+    // with 32 elements per lane the weights are read again for each row (they
+    // stay in L1); 96 registers of them and the column sums would spill
+    constexpr bool kHeld = C <= 16;
+    extern __shared__ __align__(16) char ring[];
+    __shared__ Exchange ex[kMaxWarps];
+    const Group g = group_of<NARROW>(lanes);
+    const int col = column_of<NARROW, E, NV>(g);
+    const int vs = E * (NARROW ? lanes : 32);
+    float w[kHeld ? C : 1], dw[C], db[C];
+    auto weights = [&](int v, float(&t)[E]) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) t[e] = 1.0f;
+        if (a.weight && col + v * vs < a.width) load_params<E>(a.weight, a.p_dtype, col + v * vs, t);
+    };
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+        if constexpr (kHeld) {
+            float t[E];
+            weights(v, t);
+#pragma unroll
+            for (int e = 0; e < E; ++e) w[v * E + e] = t[e];
+        }
+#pragma unroll
+        for (int e = 0; e < E; ++e) dw[v * E + e] = 0.0f, db[v * E + e] = 0.0f;
+    }
+    const float width = (float)a.width;
+    const int64_t step = (int64_t)gridDim.x * groups;
+    int64_t row = (int64_t)blockIdx.x * groups + g.id;
+    int64_t first = row - (NARROW ? (threadIdx.x & 31) / lanes : 0);
+    typename B::X xs;
+    typename B::Y ys;
+    xs.open(ring);
+    ys.open(ring + B::X::kThreadBytes * blockDim.x);
+    auto fetch = [&](int st, int64_t r) {
+        if (r < a.n) {
+            const TX *p = static_cast<const TX *>(a.x) + r * a.x_stride + col;
+            const TY *q = static_cast<const TY *>(a.dy) + r * a.y_stride + col;
+#pragma unroll
+            for (int v = 0; v < NV; ++v)
+                if (col + v * vs < a.width) {
+                    xs.fetch(st, v, p + v * vs);
+                    ys.fetch(st, v, q + v * vs);
+                }
+        }
+        cp_async_commit();
+    };
+    // a pair of operands of which only one can be copied asynchronously
+    // (16-bit x, float32 dy, odd rows) moves in step: one row ahead
+    constexpr bool kAhead = B::X::kAsync && B::Y::kAsync;
+    constexpr int A = kAhead ? S - 1 : 1;  // rows fetched before the loop
+#pragma unroll
+    for (int i = 0; i < A; ++i) fetch(i, row + i * step);
+    float mean_n = row < a.n ? a.mean[row] : 0.0f, rstd_n = row < a.n ? a.rstd[row] : 0.0f;
+    int st = 0;
+    for (int parity = 0; first < a.n; first += step, row += step, parity ^= 1) {
+        if constexpr (kAhead) {
+            fetch(st == 0 ? S - 1 : st - 1, row + (S - 1) * step);
+            cp_async_wait<S - 1>();
+        } else {
+            xs.turn();
+            ys.turn();
+            fetch(st ^ 1, row + step);
+            cp_async_wait<1>();
+        }
+        const float mean = mean_n, rstd = rstd_n;
+        if (row + step < a.n) {
+            mean_n = a.mean[row + step];
+            rstd_n = a.rstd[row + step];
+        }
+        float sg = 0.0f, sgh = 0.0f;
+        if (row < a.n) {
+#pragma unroll
+            for (int v = 0; v < NV; ++v) {
+                if (col + v * vs >= a.width) continue;
+                const auto px = xs.get(st, v);
+                const auto py = ys.get(st, v);
+                float t[E];
+                if constexpr (!kHeld) weights(v, t);
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    const int k = v * E + e;
+                    const float d = to_f32(py.v[e]);
+                    const float h = (to_f32(px.v[e]) - mean) * rstd;
+                    const float gr = d * (kHeld ? w[kHeld ? k : 0] : t[e]);
+                    db[k] += d;
+                    dw[k] = fmaf(d, h, dw[k]);
+                    sg += gr;
+                    sgh = fmaf(gr, h, sgh);
+                }
+            }
+        }
+        if (a.dx) {
+            sg = warp_sum<NARROW>(g, sg);
+            sgh = warp_sum<NARROW>(g, sgh);
+            if (!NARROW && g.warps > 1) {
+                float2 *slot = ex[g.id].slot[parity];
+                if ((threadIdx.x & 31) == 0) slot[g.warp] = make_float2(sg, sgh);
+                group_barrier(g);
+                const float2 mine = (threadIdx.x & 31) < g.warps ? slot[threadIdx.x & 31] : make_float2(0.0f, 0.0f);
+                sg = warp_sum<NARROW>(g, mine.x);
+                sgh = warp_sum<NARROW>(g, mine.y);
+            }
+            const float mg = sg / width, mgh = sgh / width;
+            if (row < a.n) {
+                TX *dx = static_cast<TX *>(a.dx) + row * a.dx_stride + col;
+#pragma unroll
+                for (int v = 0; v < NV; ++v) {
+                    if (col + v * vs >= a.width) continue;
+                    // read and computed again: holding h and g from above would
+                    // take 2 registers per element
+                    const auto px = xs.get(st, v);
+                    const auto py = ys.get(st, v);
+                    float t[E];
+                    if constexpr (!kHeld) weights(v, t);
+                    Pack<TX, E> o;
+#pragma unroll
+                    for (int e = 0; e < E; ++e) {
+                        const float h = (to_f32(px.v[e]) - mean) * rstd;
+                        const float gr = to_f32(py.v[e]) * (kHeld ? w[kHeld ? v * E + e : 0] : t[e]);
+                        o.v[e] = from_f32<TX>(rstd * (gr - mg - h * mgh));
+                    }
+                    store_pack<TX, E>(dx + v * vs, o);
+                }
+            }
+        }
+        if constexpr (kAhead) st = st == S - 1 ? 0 : st + 1;
+        else st ^= 1;
+    }
+    if (!part) return;
+    // the block's column sums: over the groups of a warp, then over the warps (or
+    // groups of warps) in a fixed tree, through the ring's memory
+    cp_async_wait<0>();
+    float *sh = reinterpret_cast<float *>(ring);
+    if (NARROW)
+        for (int o = lanes; o < 32; o <<= 1)
+#pragma unroll
+            for (int k = 0; k < C; ++k) {
+                dw[k] += __shfl_xor_sync(0xffffffffu, dw[k], o);
+                db[k] += __shfl_xor_sync(0xffffffffu, db[k], o);
+            }
+    const int unit_lanes = NARROW ? 32 : lanes;
+    const int unit = threadIdx.x / unit_lanes, lane = threadIdx.x - unit * unit_lanes;
+    for (int half = blockDim.x / unit_lanes / 2; half > 0; half >>= 1) {
+        __syncthreads();
+        const int stride = half * unit_lanes;
+        if (unit >= half && unit < 2 * half)
+#pragma unroll
+            for (int k = 0; k < C; ++k) {
+                sh[(2 * k) * stride + (unit - half) * unit_lanes + lane] = dw[k];
+                sh[(2 * k + 1) * stride + (unit - half) * unit_lanes + lane] = db[k];
+            }
+        __syncthreads();
+        if (unit < half)
+#pragma unroll
+            for (int k = 0; k < C; ++k) {
+                dw[k] += sh[(2 * k) * stride + unit * unit_lanes + lane];
+                db[k] += sh[(2 * k + 1) * stride + unit * unit_lanes + lane];
+            }
+    }
+    if (unit == 0 && lane < lanes) {
+        float *p = part + (int64_t)blockIdx.x * 2 * a.width;
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+            if (col + v * vs < a.width)
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    p[col + v * vs + e] = dw[v * E + e];
+                    p[a.width + col + v * vs + e] = db[v * E + e];
+                }
+    }
+    let_next_start();
+}
+
+// dweight and dbias from the parts: 32 of the 2 width columns per block, 32
+// parts at a time.
+__global__ void __launch_bounds__(1024) k_norm_param(NormArgs a, const float *part, int parts)
+{
+    __shared__ float sh[32][33];
+    wait_for_previous();
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const int c = blockIdx.x * 32 + lane;
+    float s = 0.0f;
+    if (c < 2 * a.width)
+        for (int i = w; i < parts; i += 32) s += part[(int64_t)i * 2 * a.width + c];
+    sh[w][lane] = s;
+    __syncthreads();
+    s = sh[lane][w];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    const int k = blockIdx.x * 32 + w;  // this warp's column
+    if (lane == 0 && k < 2 * a.width) {
+        if (k < a.width) {
+            if (a.dweight) store_any(a.dweight, a.p_dtype, k, s);
+        } else if (a.dbias) {
+            store_any(a.dbias, a.p_dtype, k - a.width, s);
+        }
+    }
+}
+
+// ---- rows of any width and alignment, read again for each pass ---------------------
+
+constexpr int kLoopThreads = 512;
+constexpr int kLoopSplits = 64;  // row ranges of the column sums
+
+__device__ __forceinline__ float loop_sum(float v)
+{
+    __shared__ float part[kLoopThreads / 32];
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     __syncthreads();
     if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
     __syncthreads();
     float s = 0.0f;
-    for (int w = 0; w < kThreads / 32; ++w) s += part[w];
+    for (int w = 0; w < kLoopThreads / 32; ++w) s += part[w];
     return s;
 }
 
 template <typename TX, typename TY>
-__global__ void __launch_bounds__(kThreads) k_norm(NormArgs a)
+__global__ void __launch_bounds__(kLoopThreads) k_norm_loop(NormArgs a)
 {
     const int64_t r = blockIdx.x;
     const TX *x = static_cast<const TX *>(a.x) + r * a.x_stride;
     float s = 0.0f;
-    for (int c = threadIdx.x; c < a.width; c += kThreads) s += to_f32(x[c]);
-    const float mean = block_sum(s) / a.width;
+    for (int c = threadIdx.x; c < a.width; c += kLoopThreads) s += to_f32(x[c]);
+    const float mean = loop_sum(s) / a.width;
     s = 0.0f;
-    for (int c = threadIdx.x; c < a.width; c += kThreads) {
+    for (int c = threadIdx.x; c < a.width; c += kLoopThreads) {
         const float e = to_f32(x[c]) - mean;
         s += e * e;
     }
-    const float rstd = 1.0f / sqrtf(block_sum(s) / a.width + a.eps);
+    const float rstd = 1.0f / sqrtf(loop_sum(s) / a.width + a.eps);
     TY *y = static_cast<TY *>(a.y) + r * a.y_stride;
-    for (int c = threadIdx.x; c < a.width; c += kThreads) {
+    for (int c = threadIdx.x; c < a.width; c += kLoopThreads) {
         float v = (to_f32(x[c]) - mean) * rstd;
         if (a.weight) v *= load_any(a.weight, a.p_dtype, c);
         if (a.bias) v += load_any(a.bias, a.p_dtype, c);
@@ -48,52 +586,47 @@ __global__ void __launch_bounds__(kThreads) k_norm(NormArgs a)
 }
 
 template <typename TX, typename TY>
-__global__ void __launch_bounds__(kThreads) k_norm_dx(NormArgs a)
+__global__ void __launch_bounds__(kLoopThreads) k_norm_dx_loop(NormArgs a)
 {
     const int64_t r = blockIdx.x;
     const TX *x = static_cast<const TX *>(a.x) + r * a.x_stride;
     const TY *dy = static_cast<const TY *>(a.dy) + r * a.y_stride;
     const float mean = a.mean[r], rstd = a.rstd[r];
     float sg = 0.0f, sgh = 0.0f;
-    for (int c = threadIdx.x; c < a.width; c += kThreads) {
+    for (int c = threadIdx.x; c < a.width; c += kLoopThreads) {
         const float g = to_f32(dy[c]) * (a.weight ? load_any(a.weight, a.p_dtype, c) : 1.0f);
         sg += g;
         sgh += g * ((to_f32(x[c]) - mean) * rstd);
     }
-    const float mg = block_sum(sg) / a.width, mgh = block_sum(sgh) / a.width;
+    const float mg = loop_sum(sg) / a.width, mgh = loop_sum(sgh) / a.width;
     TX *dx = static_cast<TX *>(a.dx) + r * a.dx_stride;
-    for (int c = threadIdx.x; c < a.width; c += kThreads) {
+    for (int c = threadIdx.x; c < a.width; c += kLoopThreads) {
         const float g = to_f32(dy[c]) * (a.weight ? load_any(a.weight, a.p_dtype, c) : 1.0f);
         dx[c] = from_f32<TX>(rstd * (g - mg - (to_f32(x[c]) - mean) * rstd * mgh));
     }
 }
 
-// 32 columns per block, 8 rows at a time.
+// Column sums of one range of rows (blockIdx.y of gridDim.y), one column per thread.
 template <typename TX, typename TY>
-__global__ void __launch_bounds__(kThreads) k_norm_dparam(NormArgs a)
+__global__ void __launch_bounds__(kLoopThreads) k_norm_param_loop(NormArgs a, float *part)
 {
-    __shared__ float sw[8][33], sb[8][33];
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    const int c = blockIdx.x * 32 + lane;
-    float dw = 0.0f, db = 0.0f;
-    if (c < a.width)
-        for (int64_t r = w; r < a.n; r += 8) {
+    const int c = blockIdx.x * kLoopThreads + threadIdx.x;
+    if (c < a.width) {
+        const int64_t r0 = a.n * blockIdx.y / gridDim.y, r1 = a.n * (blockIdx.y + 1) / gridDim.y;
+        float dw = 0.0f, db = 0.0f;
+        for (int64_t r = r0; r < r1; ++r) {
             const float dy = to_f32(static_cast<const TY *>(a.dy)[r * a.y_stride + c]);
             db += dy;
             dw += dy * ((to_f32(static_cast<const TX *>(a.x)[r * a.x_stride + c]) - a.mean[r]) * a.rstd[r]);
         }
-    sw[w][lane] = dw;
-    sb[w][lane] = db;
-    __syncthreads();
-    if (w == 0 && c < a.width) {
-        for (int i = 1; i < 8; ++i) {
-            dw += sw[i][lane];
-            db += sb[i][lane];
-        }
-        if (a.dweight) store_any(a.dweight, a.p_dtype, c, dw);
-        if (a.dbias) store_any(a.dbias, a.p_dtype, c, db);
+        float *p = part + (int64_t)blockIdx.y * 2 * a.width;
+        p[c] = dw;
+        p[a.width + c] = db;
     }
+    let_next_start();
 }
+
+// ---- dispatch ------------------------------------------------------------------------
 
 // f(TX{}, TY{}): y has x's type or float32.
 template <typename F>
@@ -105,32 +638,117 @@ cudaError_t with_xy(const NormArgs &a, F &&f)
     });
 }
 
+template <int V>
+using Int = std::integral_constant<int, V>;
+
+// f(E, NV, NARROW) for the packs of r.
+template <typename TX, bool HAS32, typename F>
+cudaError_t with_packs(const Rows &r, F &&f)
+{
+    constexpr int W = 16 / (int)sizeof(TX);
+    auto with_width = [&](auto e) {
+        constexpr int E = decltype(e)::value;
+        if constexpr (HAS32 && E == W)
+            if (r.e * r.nv == 32) return f(e, Int<32 / E>{}, std::false_type{});
+        if (r.narrow) return f(e, Int<16 / E>{}, std::true_type{});
+        return f(e, Int<16 / E>{}, std::false_type{});
+    };
+    if (r.e == W) return with_width(Int<W>{});
+    if constexpr (W == 8)
+        if (r.e == 2) return with_width(Int<2>{});
+    return with_width(Int<1>{});
+}
+
+unsigned grid_for(const NormArgs &a, const Rows &r, int per_sm)
+{
+    const int64_t want = (a.n + r.groups - 1) / r.groups;
+    return (unsigned)(want < (int64_t)kSMs * per_sm ? want : (int64_t)kSMs * per_sm);
+}
+
+Rows plan_forward(const NormArgs &a) { return plan_rows(a, true, 256); }
+
+// 32 float32 elements per lane would not leave room for two rows in the ring.
+Rows plan_backward(const NormArgs &a) { return plan_rows(a, a.x_dtype != HISS_F32, kMaxLanes); }
+
+// Blocks (and parts) of the backward pass: one per SM, so that there are few
+// parts to add up.
+unsigned grad_grid(const NormArgs &a, const Rows &r) { return grid_for(a, r, 1); }
+
 }  // namespace
 
 cudaError_t layer_norm(const NormArgs &a, cudaStream_t s, int64_t *launches)
 {
+    const Rows r = plan_forward(a);
+    ++*launches;
     return with_xy(a, [&](auto tx, auto ty) {
-        k_norm<decltype(tx), decltype(ty)><<<(unsigned)a.n, kThreads, 0, s>>>(a);
-        ++*launches;
-        return cudaGetLastError();
+        using TX = decltype(tx);
+        using TY = decltype(ty);
+        if (!r.e) {
+            k_norm_loop<TX, TY><<<(unsigned)a.n, kLoopThreads, 0, s>>>(a);
+            return cudaGetLastError();
+        }
+        return with_packs<TX, true>(r, [&](auto e, auto nv, auto narrow) {
+            constexpr int E = decltype(e)::value, NV = decltype(nv)::value;
+            constexpr bool NARROW = decltype(narrow)::value;
+            static Residency cache;
+            auto kernel = k_norm<TX, TY, E, NV, NARROW>;
+            const int threads = r.lanes * r.groups;
+            const size_t smem = Forward<TX, TY, E, NV, NARROW>::kThreadBytes * threads;
+            const unsigned grid = grid_for(a, r, resident(kernel, threads, smem, cache));
+            kernel<<<grid, threads, smem, s>>>(a, r.lanes, r.groups);
+            return cudaGetLastError();
+        });
     });
 }
 
-size_t layer_norm_grad_tmp_bytes(const NormArgs &) { return 0; }
-
-cudaError_t layer_norm_grad(const NormArgs &a, void *, cudaStream_t s, int64_t *launches)
+size_t layer_norm_grad_tmp_bytes(const NormArgs &a)
 {
-    return with_xy(a, [&](auto tx, auto ty) {
-        if (a.dx && a.n > 0) {
-            k_norm_dx<decltype(tx), decltype(ty)><<<(unsigned)a.n, kThreads, 0, s>>>(a);
-            ++*launches;
-        }
-        if (a.dweight || a.dbias) {
-            k_norm_dparam<decltype(tx), decltype(ty)><<<(unsigned)((a.width + 31) / 32), kThreads, 0, s>>>(a);
-            ++*launches;
-        }
-        return cudaGetLastError();
-    });
+    const Rows r = plan_backward(a);
+    return 8 * (size_t)a.width * (r.e ? grad_grid(a, r) : kLoopSplits);
+}
+
+cudaError_t layer_norm_grad(const NormArgs &a, void *tmp, cudaStream_t s, int64_t *launches)
+{
+    const bool params = a.dweight || a.dbias;
+    float *part = params ? static_cast<float *>(tmp) : nullptr;
+    unsigned parts = 0;
+    if (a.n > 0) {
+        const Rows r = plan_backward(a);
+        HISS_TRY(with_xy(a, [&](auto tx, auto ty) {
+            using TX = decltype(tx);
+            using TY = decltype(ty);
+            if (!r.e) {
+                if (a.dx) {
+                    k_norm_dx_loop<TX, TY><<<(unsigned)a.n, kLoopThreads, 0, s>>>(a);
+                    ++*launches;
+                }
+                if (params) {
+                    parts = (unsigned)(a.n < kLoopSplits ? a.n : kLoopSplits);
+                    k_norm_param_loop<TX, TY><<<dim3((a.width + kLoopThreads - 1) / kLoopThreads, parts), kLoopThreads, 0, s>>>(
+                        a, part);
+                    ++*launches;
+                }
+                return cudaGetLastError();
+            }
+            return with_packs<TX, sizeof(TX) == 2>(r, [&](auto e, auto nv, auto narrow) {
+                constexpr int E = decltype(e)::value, NV = decltype(nv)::value;
+                static Residency cache;
+                auto kernel = k_norm_grad<TX, TY, E, NV, decltype(narrow)::value>;
+                const int threads = r.lanes * r.groups;
+                const bool many = threads > (r.narrow ? 32 : r.lanes);  // sums of several warps or groups to add up
+                const size_t smem = std::max(Backward<TX, TY, E, NV>::kThreadBytes * threads,
+                                             many ? 4 * (size_t)threads * E * NV : 0);
+                resident(kernel, threads, smem, cache);
+                parts = grad_grid(a, r);
+                kernel<<<parts, threads, smem, s>>>(a, r.lanes, r.groups, part);
+                ++*launches;
+                return cudaGetLastError();
+            });
+        }));
+    }
+    if (!params) return cudaSuccess;
+    ++*launches;
+    return launch_after(k_norm_param, (unsigned)((2 * a.width + 31) / 32), 1024, 0, s, a, part, (int)parts);
 }
 
 }  // namespace hiss
