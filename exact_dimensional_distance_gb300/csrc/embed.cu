@@ -1,10 +1,25 @@
 // Embedding lookup with scaling, and its gradient by sorted tokens.
 //
-// Forward: out[i] = scale * table[token[i]].  Backward: grad[v] = scale * sum
-// of dy[i] over the positions i that hold token v.  The positions are sorted
-// by token (stable radix sort), so each row of the gradient is the sum of one
-// contiguous run in position order: no floating-point atomics, and the same
-// bits every time.
+//   forward    out[i] = scale * table[token[i]]
+//   backward   grad[v] = scale * sum of dy[i] over the positions i that hold token v
+//
+// Both are bound by memory.  The forward pass reads the rows its tokens touch
+// and writes n rows.  The backward pass must read n rows of dy and
+// write the whole gradient, mostly zeros for a large vocabulary:
+//
+//   1. the positions are sorted by token (stable LSD radix sort, up to 9 bits
+//      per pass; tokens of a vocabulary below 2^18 take two), while the SMs that the sort
+//      leaves idle write the zeros of the rows without positions;
+//   2. k_sum cuts the sorted positions into units of kUnit: every unit has the
+//      same work however often a token occurs.  A run of equal tokens inside a unit is
+//      summed and written; the run that reaches over a unit's end leaves
+//      float32 partial sums;
+//   3. k_join adds the partial sums of each such run in unit order.
+//
+// Sums are float32 in an order that depends on the positions alone: no
+// floating-point atomics.  Few positions take one kernel instead (k_grad_few).
+#include <algorithm>
+
 #include "hiss_internal.cuh"
 #include "numeric.cuh"
 
@@ -12,71 +27,565 @@ namespace hiss {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kCols = 8;  // columns per lane
 
 // The table row of position i, or -1 for a row of zeros (padding, or a token
 // outside the table, which sets *bad).
-__device__ __forceinline__ int64_t row_of(const void *tokens, int bits, int64_t i, int64_t pad, int64_t vocab, int *bad)
+__device__ __forceinline__ int64_t row_of(const EmbedArgs &a, int64_t i, int *bad)
 {
-    const int64_t t = bits == 64 ? static_cast<const int64_t *>(tokens)[i] : static_cast<const int32_t *>(tokens)[i];
-    if (t == pad) return -1;
-    if (t < 0 || t >= vocab) {
-        *bad = 1;
+    const int64_t t =
+        a.token_bits == 64 ? static_cast<const int64_t *>(a.tokens)[i] : static_cast<const int32_t *>(a.tokens)[i];
+    if (t == a.pad) return -1;
+    if (t < 0 || t >= a.vocab) {
+        if (bad) *bad = 1;
         return -1;
     }
     return t;
 }
 
-template <typename TI, typename TO>
-__global__ void __launch_bounds__(kThreads) k_embed(EmbedArgs a)
+// ---- forward --------------------------------------------------------------------
+
+// lanes (a power of two up to 32) take one tile of lanes * E * NV columns of
+// one position.
+template <typename TI, typename TO, int E, int NV>
+__global__ void __launch_bounds__(kThreads) k_embed(EmbedArgs a, int lanes, int tiles)
 {
-    const int64_t total = a.n * a.width;
-    for (int64_t e = (int64_t)blockIdx.x * kThreads + threadIdx.x; e < total; e += (int64_t)gridDim.x * kThreads) {
-        const int64_t i = e / a.width, c = e - i * a.width;
-        const int64_t r = row_of(a.tokens, a.token_bits, i, a.pad, a.vocab, a.bad);
-        const float v = r < 0 ? 0.0f : a.scale * to_f32(static_cast<const TI *>(a.rows)[r * a.rows_stride + c]);
-        static_cast<TO *>(a.out)[i * a.out_stride + c] = from_f32<TO>(v);
+    const int per_block = kThreads / lanes;
+    const int lane = threadIdx.x & (lanes - 1);
+    const int64_t items = a.n * tiles, step = (int64_t)gridDim.x * per_block;
+    for (int64_t it = (int64_t)blockIdx.x * per_block + threadIdx.x / lanes; it < items; it += step) {
+        const int64_t i = tiles == 1 ? it : it / tiles;
+        const int c0 = ((int)(it - i * tiles) * lanes * NV + lane) * E;
+        const int64_t r = row_of(a, i, a.bad);
+        const TI *p = static_cast<const TI *>(a.rows) + r * a.rows_stride;
+        TO *q = static_cast<TO *>(a.out) + i * a.out_stride;
+        Pack<TI, E> v[NV];
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int c = c0 + k * lanes * E;
+            if (r >= 0 && c < a.width) v[k] = load_pack<TI, E>(p + c);
+        }
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int c = c0 + k * lanes * E;
+            if (c >= a.width) continue;
+            Pack<TO, E> o;
+#pragma unroll
+            for (int e = 0; e < E; ++e) o.v[e] = from_f32<TO>(r >= 0 ? a.scale * to_f32(v[k].v[e]) : 0.0f);
+            store_pack<TO, E>(q + c, o);
+        }
     }
 }
 
-// Sort keys: the token, or vocab for a position that contributes nothing.
-__global__ void __launch_bounds__(kThreads) k_token_keys(EmbedArgs a, uint64_t *keys, uint32_t *vals)
+// ---- the sort ---------------------------------------------------------------------
+
+constexpr int kSortThreads = 512;
+constexpr int kSortWarps = kSortThreads / 32;
+constexpr int kSortItems = 8;
+constexpr int kSortTile = kSortThreads * kSortItems;
+constexpr int kMaxBits = 9;  // one bin per thread
+constexpr int kMaxBins = 1 << kMaxBits;
+// Up to this many tiles each block of the scatter adds up the tiles' counts
+// itself; above, their prefix sums are a kernel of their own.
+constexpr int kSumTiles = 64;
+constexpr int kFillBlocks = 2 * kSMs;
+
+struct SortArgs {
+    const uint32_t *keys_in, *vals_in;  // NULL: the tokens and their positions
+    uint32_t *keys_out, *vals_out;
+    uint32_t *counts;    // [tiles][bins], exclusive over tiles once scanned; then [bins] totals
+    uint8_t *present;    // [vocab] token occurs (NULL: not wanted)
+    int tiles, shift, bits, scanned;
+    int fill, fills;     // this kernel writes part fill of fills of the empty rows (fills = 0: none)
+};
+
+__device__ __forceinline__ uint32_t key_at(const EmbedArgs &a, const SortArgs &s, int64_t i, int *bad)
 {
-    const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    if (i >= a.n) return;
-    const int64_t r = row_of(a.tokens, a.token_bits, i, a.pad, a.vocab, a.bad);
-    keys[i] = (uint64_t)(r < 0 ? a.vocab : r);
-    vals[i] = (uint32_t)i;
+    if (s.keys_in) return s.keys_in[i];
+    const int64_t r = row_of(a, i, bad);
+    return (uint32_t)(r < 0 ? a.vocab : r);
 }
 
-// First and one past the last sorted position of each token present.
-__global__ void __launch_bounds__(kThreads) k_token_runs(const uint64_t *keys, int64_t n, int64_t vocab, int32_t *first,
-                                                         int32_t *last)
+// Zeros for the rows of this kernel's part of the vocabulary that no position
+// holds, by the blocks past the sort's.
+template <typename TO, int E>
+__device__ void fill_empty(const EmbedArgs &a, const SortArgs &s)
 {
-    const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    if (i >= n) return;
-    const int64_t k = (int64_t)keys[i];
-    if (k >= vocab) return;
-    if (i == 0 || (int64_t)keys[i - 1] != k) first[k] = (int32_t)i;
-    if (i == n - 1 || (int64_t)keys[i + 1] != k) last[k] = (int32_t)(i + 1);
-}
-
-template <typename TI, typename TO>
-__global__ void __launch_bounds__(kThreads) k_embed_grad(EmbedArgs a, const uint32_t *order, const int32_t *first,
-                                                         const int32_t *last)
-{
-    const int64_t v = blockIdx.x;
-    const int32_t i0 = first[v], i1 = last[v];
-    if (a.accumulate && i1 <= i0) return;
-    TO *out = static_cast<TO *>(a.out) + v * a.out_stride;
-    for (int c = threadIdx.x; c < a.width; c += kThreads) {
-        float s = 0.0f;
-        for (int32_t i = i0; i < i1; ++i)
-            s += to_f32(static_cast<const TI *>(a.rows)[(int64_t)order[i] * a.rows_stride + c]);
-        s *= a.scale;
-        if (a.accumulate) s += to_f32(out[c]);
-        out[c] = from_f32<TO>(s);
+    const int lane = threadIdx.x & 31;
+    const int64_t v0 = a.vocab * s.fill / s.fills, v1 = a.vocab * (s.fill + 1) / s.fills;
+    const int64_t warp = (int64_t)(blockIdx.x - s.tiles) * kSortWarps + (threadIdx.x >> 5);
+    const int64_t warps = (int64_t)(gridDim.x - s.tiles) * kSortWarps;
+    Pack<TO, E> zero;
+#pragma unroll
+    for (int e = 0; e < E; ++e) zero.v[e] = from_f32<TO>(0.0f);
+    for (int64_t v = v0 + warp * 32; v < v1; v += warps * 32) {
+        unsigned empty = __ballot_sync(0xffffffffu, v + lane < v1 && !s.present[min(v + lane, v1 - 1)]);
+        while (empty) {
+            const int b = __ffs(empty) - 1;
+            empty &= empty - 1;
+            TO *p = static_cast<TO *>(a.out) + (v + b) * a.out_stride;
+            for (int c = lane * E; c < a.width; c += 32 * E) store_pack<TO, E>(p + c, zero);
+        }
     }
 }
+
+// Digit counts of each tile (and, in the first pass, which tokens occur).
+template <typename TO, int E>
+__global__ void __launch_bounds__(kSortThreads) k_sort_count(EmbedArgs a, SortArgs s)
+{
+    __shared__ uint32_t hist[kMaxBins];
+    let_next_start();
+    wait_for_previous();
+    if ((int)blockIdx.x >= s.tiles) {
+        fill_empty<TO, E>(a, s);
+        return;
+    }
+    hist[threadIdx.x] = 0;
+    __syncthreads();
+    const int lane = threadIdx.x & 31;
+    const uint32_t mask = (1u << s.bits) - 1u;
+    const int64_t base = (int64_t)blockIdx.x * kSortTile;
+    uint32_t key[kSortItems];
+#pragma unroll
+    for (int k = 0; k < kSortItems; ++k) {
+        const int64_t i = base + k * kSortThreads + threadIdx.x;
+        key[k] = i < a.n ? key_at(a, s, i, a.bad) : ~0u;
+    }
+#pragma unroll
+    for (int k = 0; k < kSortItems; ++k) {
+        const bool valid = base + k * kSortThreads + threadIdx.x < a.n;
+        if (s.present && !s.keys_in && valid && key[k] < (uint32_t)a.vocab) s.present[key[k]] = 1;
+        // equal digits of a warp are added once: a frequent token does not
+        // serialise the warp on one counter
+        const uint32_t d = valid ? (key[k] >> s.shift) & mask : kMaxBins;
+        const uint32_t peers = __match_any_sync(0xffffffffu, d);
+        if (valid && lane == __ffs(peers) - 1) atomicAdd(&hist[d], (uint32_t)__popc(peers));
+    }
+    __syncthreads();
+    const int bins = 1 << s.bits;
+    if ((int)threadIdx.x < bins) s.counts[(int64_t)blockIdx.x * bins + threadIdx.x] = hist[threadIdx.x];
+}
+
+// counts[t][bin] := sum over the tiles before t; totals behind them.  32 bins
+// per block, the tiles in 32 consecutive parts.
+__global__ void __launch_bounds__(1024) k_sort_scan(SortArgs s)
+{
+    __shared__ uint32_t sum[32][33];
+    let_next_start();
+    wait_for_previous();
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const int bins = 1 << s.bits, bin = blockIdx.x * 32 + lane;
+    const int t0 = (int)((int64_t)s.tiles * w / 32), t1 = (int)((int64_t)s.tiles * (w + 1) / 32);
+    uint32_t v = 0;
+    if (bin < bins)
+        for (int t = t0; t < t1; ++t) v += s.counts[(int64_t)t * bins + bin];
+    sum[w][lane] = v;
+    __syncthreads();
+    uint32_t run = 0;
+    for (int i = 0; i < w; ++i) run += sum[i][lane];
+    if (bin >= bins) return;
+    for (int t = t0; t < t1; ++t) {
+        const uint32_t c = s.counts[(int64_t)t * bins + bin];
+        s.counts[(int64_t)t * bins + bin] = run;
+        run += c;
+    }
+    if (w == 31) s.counts[(int64_t)s.tiles * bins + bin] = run;
+}
+
+// One stable pass: each tile's positions go behind those of the tiles before
+// it, digit by digit.
+template <typename TO, int E>
+__global__ void __launch_bounds__(kSortThreads) k_sort_scatter(EmbedArgs a, SortArgs s)
+{
+    __shared__ uint32_t whist[kSortWarps][kMaxBins];
+    __shared__ uint32_t base_of[kMaxBins];
+    __shared__ uint32_t warp_total[kSortWarps];
+    let_next_start();
+    wait_for_previous();
+    if ((int)blockIdx.x >= s.tiles) {
+        fill_empty<TO, E>(a, s);
+        return;
+    }
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int bins = 1 << s.bits, bin = threadIdx.x;
+    const uint32_t mask = (uint32_t)bins - 1u;
+    for (int i = threadIdx.x; i < kSortWarps * kMaxBins; i += kSortThreads) (&whist[0][0])[i] = 0;
+    // warp-contiguous items, in order
+    const int64_t base = (int64_t)blockIdx.x * kSortTile + warp * (32 * kSortItems);
+    uint32_t key[kSortItems], val[kSortItems], rank[kSortItems];
+#pragma unroll
+    for (int k = 0; k < kSortItems; ++k) {
+        const int64_t i = base + k * 32 + lane;
+        if (i < a.n) {
+            key[k] = key_at(a, s, i, nullptr);
+            val[k] = s.vals_in ? s.vals_in[i] : (uint32_t)i;
+        }
+    }
+    // this thread's bin: positions in the tiles before this one, and in all
+    uint32_t before = 0, total = 0;
+    if (bin < bins) {
+        if (s.scanned) {
+            before = s.counts[(int64_t)blockIdx.x * bins + bin];
+            total = s.counts[(int64_t)s.tiles * bins + bin];
+        } else {
+#pragma unroll 8
+            for (int t = 0; t < s.tiles; ++t) {
+                const uint32_t c = s.counts[(int64_t)t * bins + bin];
+                total += c;
+                if (t < (int)blockIdx.x) before += c;
+            }
+        }
+    }
+    uint32_t incl = total;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t t = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += t;
+    }
+    if (lane == 31) warp_total[warp] = incl;
+    __syncthreads();
+    uint32_t first = incl - total;
+    for (int i = 0; i < warp; ++i) first += warp_total[i];
+    base_of[bin] = first + before;
+#pragma unroll
+    for (int k = 0; k < kSortItems; ++k) {
+        const bool valid = base + k * 32 + lane < a.n;
+        const uint32_t d = valid ? (key[k] >> s.shift) & mask : kMaxBins;
+        const uint32_t peers = __match_any_sync(0xffffffffu, d);
+        const int leader = __ffs(peers) - 1;
+        uint32_t old = 0;
+        if (valid && lane == leader) {
+            old = whist[warp][d];
+            whist[warp][d] = old + __popc(peers);
+        }
+        rank[k] = __shfl_sync(0xffffffffu, old, leader) + __popc(peers & ((1u << lane) - 1u));
+        __syncwarp();
+    }
+    __syncthreads();
+    uint32_t run = base_of[bin];
+#pragma unroll
+    for (int w = 0; w < kSortWarps; ++w) {
+        const uint32_t c = whist[w][bin];
+        whist[w][bin] = run;
+        run += c;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kSortItems; ++k)
+        if (base + k * 32 + lane < a.n) {
+            const uint32_t at = whist[warp][(key[k] >> s.shift) & mask] + rank[k];
+            s.keys_out[at] = key[k];
+            s.vals_out[at] = val[k];
+        }
+}
+
+// ---- the sums ---------------------------------------------------------------------
+
+constexpr int kUnit = 32;  // sorted positions per unit
+
+struct SumArgs {
+    const uint32_t *keys, *vals;  // sorted tokens and their positions
+    float *part;                  // [units][2][width]: sum of the run that comes in from the unit
+                                  // before, and of the run that begins here and goes on
+    int64_t units;
+    int lanes, tiles;             // lanes * kCols columns per tile
+};
+
+// Write (or add) a finished row's columns.
+template <typename TO, int E, int NV>
+__device__ __forceinline__ void write_row(const EmbedArgs &a, uint32_t v, int c0, int lanes, const float (&s)[kCols])
+{
+    TO *p = static_cast<TO *>(a.out) + (int64_t)v * a.out_stride;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        const int c = c0 + k * lanes * E;
+        if (c >= a.width) continue;
+        Pack<TO, E> o;
+        if (a.accumulate) o = load_pack<TO, E>(p + c);
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            float x = a.scale * s[k * E + e];
+            if (a.accumulate) x += to_f32(o.v[e]);
+            o.v[e] = from_f32<TO>(x);
+        }
+        store_pack<TO, E>(p + c, o);
+    }
+}
+
+template <int E, int NV>
+__device__ __forceinline__ void write_part(const EmbedArgs &a, float *p, int c0, int lanes, const float (&s)[kCols])
+{
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        const int c = c0 + k * lanes * E;
+        if (c >= a.width) continue;
+        Pack<float, E> o;
+#pragma unroll
+        for (int e = 0; e < E; ++e) o.v[e] = s[k * E + e];
+        store_pack<float, E>(p + c, o);
+    }
+}
+
+template <typename TI, typename TO, int E>
+__global__ void __launch_bounds__(kThreads) k_sum(EmbedArgs a, SumArgs s)
+{
+    constexpr int NV = kCols / E;
+    constexpr int U = sizeof(TI) == 2 ? 8 : 4;  // rows in flight
+    let_next_start();
+    wait_for_previous();
+    const int64_t item = ((int64_t)blockIdx.x * kThreads + threadIdx.x) / s.lanes;
+    const int lane = threadIdx.x & (s.lanes - 1);
+    if (item >= s.units * s.tiles) return;
+    // tiles of a unit are neighbours: they read the same rows of dy
+    const int64_t unit = item / s.tiles;
+    const int c0 = ((int)(item - unit * s.tiles) * s.lanes * NV + lane) * E;
+    const int64_t i0 = unit * kUnit;
+    const int m = (int)min((int64_t)kUnit, a.n - i0);
+    const uint32_t vocab = (uint32_t)a.vocab;
+    uint32_t key = s.keys[i0];
+    if (key >= vocab) return;  // only positions without a row from here on
+    // does the run of the first key come in from the unit before?
+    bool inside = i0 == 0 || s.keys[i0 - 1] != key;
+    float *part = s.part + unit * 2 * a.width;
+    float acc[kCols];
+#pragma unroll
+    for (int c = 0; c < kCols; ++c) acc[c] = 0.0f;
+    for (int j = 0; j < m; j += U) {
+        uint32_t k[U];
+        Pack<TI, E> v[U][NV];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            k[u] = vocab;
+            if (j + u < m) {
+                k[u] = s.keys[i0 + j + u];
+                const TI *p = static_cast<const TI *>(a.rows) + (int64_t)s.vals[i0 + j + u] * a.rows_stride;
+#pragma unroll
+                for (int q = 0; q < NV; ++q) {
+                    const int c = c0 + q * s.lanes * E;
+                    if (c < a.width && k[u] < vocab) v[u][q] = load_pack<TI, E>(p + c);
+                }
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (k[u] != key) {
+                if (inside) write_row<TO, E, NV>(a, key, c0, s.lanes, acc);
+                else write_part<E, NV>(a, part, c0, s.lanes, acc);
+                key = k[u];
+                if (key >= vocab) return;
+                inside = true;
+#pragma unroll
+                for (int c = 0; c < kCols; ++c) acc[c] = 0.0f;
+            }
+#pragma unroll
+            for (int q = 0; q < NV; ++q)
+#pragma unroll
+                for (int e = 0; e < E; ++e) acc[q * E + e] += to_f32(v[u][q].v[e]);
+        }
+    }
+    const bool goes_on = i0 + m < a.n && s.keys[i0 + m] == key;
+    if (inside && !goes_on) write_row<TO, E, NV>(a, key, c0, s.lanes, acc);
+    else write_part<E, NV>(a, inside ? part + a.width : part, c0, s.lanes, acc);
+}
+
+constexpr int kJoinThreads = 512;
+constexpr int kJoinLong = 32;  // runs over more units than this are summed by a whole block
+
+// Rows whose run reaches over the end of unit u (and begins in u): the sum of
+// u's second part and of the first parts of the units that the run goes on in.
+// One group of lanes per unit and tile; a long run is left to its block, whose
+// groups each take a stretch of its units, added up in order.
+template <typename TO, int E>
+__global__ void __launch_bounds__(kJoinThreads) k_join(EmbedArgs a, SumArgs s)
+{
+    constexpr int NV = kCols / E;
+    __shared__ float sh[kJoinThreads * kCols];
+    __shared__ uint32_t long_key[kJoinThreads];  // key + 1 of each group's long run, 0: none
+    wait_for_previous();
+    const int lanes = s.lanes, groups = kJoinThreads / lanes;
+    const int group = threadIdx.x / lanes, lane = threadIdx.x & (lanes - 1);
+    const int tile = blockIdx.y;
+    const int c0 = (tile * lanes * NV + lane) * E;
+    const int64_t u0 = (int64_t)blockIdx.x * groups;
+    const uint32_t vocab = (uint32_t)a.vocab;
+    auto add_parts = [&](int64_t from, int64_t to, float(&acc)[kCols]) {
+#pragma unroll 4
+        for (int64_t u = from; u < to; ++u) {
+            const float *p = s.part + u * 2 * a.width;
+#pragma unroll
+            for (int q = 0; q < NV; ++q) {
+                const int c = c0 + q * lanes * E;
+                if (c >= a.width) continue;
+                const auto v = load_pack<float, E>(p + c);
+#pragma unroll
+                for (int e = 0; e < E; ++e) acc[q * E + e] += v.v[e];
+            }
+        }
+    };
+    // the second part of unit u
+    auto begin = [&](int64_t u, float(&acc)[kCols]) {
+        const float *p = s.part + (u * 2 + 1) * a.width;
+#pragma unroll
+        for (int q = 0; q < NV; ++q) {
+            const int c = c0 + q * lanes * E;
+            if (c >= a.width) continue;
+            const auto v = load_pack<float, E>(p + c);
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[q * E + e] = v.v[e];
+        }
+    };
+    if (lane == 0) long_key[group] = 0;
+    __syncthreads();
+    const int64_t u = u0 + group;
+    if (u + 1 < s.units) {
+        const int64_t end = (u + 1) * kUnit;  // first position of the next unit
+        const uint32_t key = s.keys[end];
+        const bool begins = s.keys[u * kUnit] != key || u == 0 || s.keys[u * kUnit - 1] != key;
+        if (key < vocab && s.keys[end - 1] == key && begins) {
+            // the run's last unit: the first whose successor begins with another token
+            int64_t last = u + 1;
+            for (bool more = true; more && last - u <= kJoinLong;) {
+                uint32_t k[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) k[i] = last + 1 + i < s.units ? s.keys[(last + 1 + i) * kUnit] : vocab;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    more = more && k[i] == key;
+                    last += more;
+                }
+            }
+            if (last - u <= kJoinLong) {
+                float acc[kCols];
+                begin(u, acc);
+                add_parts(u + 1, last + 1, acc);
+                write_row<TO, E, NV>(a, key, c0, lanes, acc);
+            } else if (lane == 0) {
+                long_key[group] = key + 1;
+            }
+        }
+    }
+    __syncthreads();
+    for (int g = 0; g < groups; ++g) {
+        if (!long_key[g]) continue;
+        const uint32_t key = long_key[g] - 1;
+        const int64_t b = u0 + g;
+        // the run's last unit by bisection over the units' first tokens (sorted)
+        int64_t lo = b + 1, hi = s.units;
+        while (hi - lo > 1) {
+            const int64_t mid = (lo + hi) >> 1;
+            if (s.keys[mid * kUnit] == key) lo = mid;
+            else hi = mid;
+        }
+        const int64_t count = lo - b;  // units b + 1 .. lo
+        float acc[kCols];
+#pragma unroll
+        for (int c = 0; c < kCols; ++c) acc[c] = 0.0f;
+        if (group == 0) begin(b, acc);
+        add_parts(b + 1 + count * group / groups, b + 1 + count * (group + 1) / groups, acc);
+        // pairs of groups, a fixed tree
+        for (int half = groups >> 1; half > 0; half >>= 1) {
+            __syncthreads();
+            if (group >= half && group < 2 * half)
+#pragma unroll
+                for (int c = 0; c < kCols; ++c) sh[c * kJoinThreads + threadIdx.x] = acc[c];
+            __syncthreads();
+            if (group < half)
+#pragma unroll
+                for (int c = 0; c < kCols; ++c) acc[c] += sh[c * kJoinThreads + threadIdx.x + half * lanes];
+        }
+        if (group == 0) write_row<TO, E, NV>(a, key, c0, lanes, acc);
+        __syncthreads();
+    }
+}
+
+// ---- few positions -------------------------------------------------------------------
+
+constexpr int64_t kFew = 1024;
+constexpr int kFewThreads = 256;
+constexpr int kFewFloats = 8192;  // accumulators of a block
+
+// One kernel without a sort: a block owns a range of rows and of columns (its
+// accumulators in shared memory), picks the positions whose token falls into
+// its rows, in order, and adds them up; every row of the range is written.
+template <typename TI, typename TO, int E>
+__global__ void __launch_bounds__(kFewThreads) k_grad_few(EmbedArgs a, int rows, int lanes)
+{
+    __shared__ float acc[kFewFloats];
+    __shared__ uint32_t found[kFew];     // (row in the range) << 10 | position
+    __shared__ uint32_t warp_count[kFewThreads / 32];
+    __shared__ uint8_t touched[kFewFloats];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t v0 = (int64_t)blockIdx.x * rows;
+    const int nrows = (int)min((int64_t)rows, a.vocab - v0);
+    const int cols = lanes * E;              // columns of the tile
+    const int c0 = blockIdx.y * cols;
+    for (int i = threadIdx.x; i < rows; i += kFewThreads) touched[i] = 0;
+    constexpr int R = kFew / kFewThreads;
+    int64_t r[R];
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+        const int64_t i = k * kFewThreads + threadIdx.x;
+        r[k] = i < a.n ? row_of(a, i, a.bad) : -1;
+    }
+    __syncthreads();
+    uint32_t count = 0;
+    for (int k = 0; k < R; ++k) {
+        const bool hit = r[k] >= v0 && r[k] < v0 + nrows;
+        const uint32_t m = __ballot_sync(0xffffffffu, hit);
+        if (lane == 0) warp_count[warp] = __popc(m);
+        __syncthreads();
+        uint32_t at = count;
+        for (int w = 0; w < kFewThreads / 32; ++w) {
+            if (w < warp) at += warp_count[w];
+            count += warp_count[w];
+        }
+        if (hit) {
+            found[at + __popc(m & ((1u << lane) - 1u))] = (uint32_t)(r[k] - v0) << 10 | (uint32_t)(k * kFewThreads + threadIdx.x);
+            touched[r[k] - v0] = 1;
+        }
+        __syncthreads();
+    }
+    // a group of lanes takes the rows of its residue: rows of other groups are not its concern
+    const int group = threadIdx.x / lanes, groups = kFewThreads / lanes, gl = threadIdx.x - group * lanes;
+    const int c = c0 + gl * E;
+    if (group >= groups || c >= a.width) return;
+    for (int i = group; i < nrows; i += groups)
+        if (touched[i])
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[i * cols + gl * E + e] = 0.0f;
+    constexpr int U = 8;  // rows in flight
+    for (uint32_t j = 0; j < count; j += U) {
+        Pack<TI, E> v[U];
+        int at[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const uint32_t f = j + u < count ? found[j + u] : 0u;
+            at[u] = j + u < count && (int)((f >> 10) % groups) == group ? (int)(f >> 10) * cols + gl * E : -1;
+            if (at[u] >= 0)
+                v[u] = load_pack<TI, E>(static_cast<const TI *>(a.rows) + (int64_t)(f & 1023u) * a.rows_stride + c);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (at[u] >= 0)
+#pragma unroll
+                for (int e = 0; e < E; ++e) acc[at[u] + e] += to_f32(v[u].v[e]);
+    }
+    for (int i = group; i < nrows; i += groups) {
+        if (a.accumulate && !touched[i]) continue;
+        TO *p = static_cast<TO *>(a.out) + (v0 + i) * a.out_stride + c;
+        Pack<TO, E> o;
+        if (a.accumulate) o = load_pack<TO, E>(p);
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            float x = touched[i] ? a.scale * acc[i * cols + gl * E + e] : 0.0f;
+            if (a.accumulate) x += to_f32(o.v[e]);
+            o.v[e] = from_f32<TO>(x);
+        }
+        store_pack<TO, E>(p, o);
+    }
+}
+
+// ---- dispatch ---------------------------------------------------------------------
 
 int bits_of(int64_t v)
 {
@@ -87,51 +596,159 @@ int bits_of(int64_t v)
 
 size_t up(size_t b) { return (b + 255) & ~(size_t)255; }
 
-}  // namespace
-
-cudaError_t embed(const EmbedArgs &a, cudaStream_t s, int64_t *launches)
+// Elements per access that both matrices allow.
+int pack_of(const EmbedArgs &a, int wide)
 {
-    const int64_t blocks = (a.n * a.width + kThreads - 1) / kThreads;
-    const unsigned grid = (unsigned)(blocks < 152 * 64 ? blocks : 152 * 64);
+    for (int e : {wide, 2})
+        if (a.width % e == 0 && rows_aligned(a.rows, a.rows_stride, a.rows_dtype, e) &&
+            rows_aligned(a.out, a.out_stride, a.out_dtype, e))
+            return e;
+    return 1;
+}
+
+template <int V>
+using Int = std::integral_constant<int, V>;
+
+// f(TI{}, TO{}, E) for the accesses of a.
+template <typename F>
+cudaError_t with_types(const EmbedArgs &a, F &&f)
+{
     return with_dtype(a.rows_dtype, [&](auto ti) {
         return with_dtype(a.out_dtype, [&](auto to) {
-            k_embed<decltype(ti), decltype(to)><<<grid, kThreads, 0, s>>>(a);
-            ++*launches;
-            return cudaGetLastError();
+            // 16 bytes of the narrower type
+            constexpr int W = sizeof(ti) == 4 && sizeof(to) == 4 ? 4 : 8;
+            const int e = pack_of(a, W);
+            if (e == W) return f(ti, to, Int<W>{});
+            if (e == 2) return f(ti, to, Int<2>{});
+            return f(ti, to, Int<1>{});
         });
     });
 }
 
-size_t embed_grad_tmp_bytes(const EmbedArgs &a)
+// Lanes (a power of two up to 32) for a row at kCols columns per lane, and the
+// tiles a wider row takes.
+void lanes_of(int width, int *lanes, int *tiles)
 {
-    return 2 * up(8 * (size_t)a.n) + 2 * up(4 * (size_t)a.n) + up(sort_tmp_bytes(a.n)) + 2 * up(4 * (size_t)a.vocab);
+    *lanes = 1;
+    while (*lanes < 32 && *lanes * kCols < width) *lanes <<= 1;
+    *tiles = (width + *lanes * kCols - 1) / (*lanes * kCols);
 }
 
-cudaError_t embed_grad(const EmbedArgs &a, void *tmp, int *flags, cudaStream_t s, int64_t *launches)
+struct GradLayout {
+    int passes = 0, tiles = 0, bins = 0;
+    int64_t units = 0;
+    size_t keys = 0, vals = 0, keys2 = 0, vals2 = 0, counts = 0, present = 0, part = 0, bytes = 0;
+};
+
+GradLayout layout(const EmbedArgs &a)
 {
-    char *p = static_cast<char *>(tmp);
-    auto take = [&](size_t b) { char *q = p; p += up(b); return q; };
-    uint64_t *keys = (uint64_t *)take(8 * (size_t)a.n), *keys_alt = (uint64_t *)take(8 * (size_t)a.n);
-    uint32_t *vals = (uint32_t *)take(4 * (size_t)a.n), *vals_alt = (uint32_t *)take(4 * (size_t)a.n);
-    void *sort_tmp = take(sort_tmp_bytes(a.n));
-    int32_t *first = (int32_t *)take(4 * (size_t)a.vocab), *last = (int32_t *)take(4 * (size_t)a.vocab);
-    HISS_TRY(cudaMemsetAsync(first, 0, 4 * (size_t)a.vocab, s));
-    HISS_TRY(cudaMemsetAsync(last, 0, 4 * (size_t)a.vocab, s));
-    int in_alt = 0;
-    if (a.n > 0) {
-        const unsigned blocks = (unsigned)((a.n + kThreads - 1) / kThreads);
-        k_token_keys<<<blocks, kThreads, 0, s>>>(a, keys, vals);
-        HISS_TRY(sort_pairs(keys, vals, keys_alt, vals_alt, a.n, bits_of(a.vocab), sort_tmp, flags, s, launches, &in_alt));
-        k_token_runs<<<blocks, kThreads, 0, s>>>(in_alt ? keys_alt : keys, a.n, a.vocab, first, last);
-        *launches += 2;
-    }
-    return with_dtype(a.rows_dtype, [&](auto ti) {
-        return with_dtype(a.out_dtype, [&](auto to) {
-            k_embed_grad<decltype(ti), decltype(to)><<<(unsigned)a.vocab, kThreads, 0, s>>>(a, in_alt ? vals_alt : vals,
-                                                                                           first, last);
+    GradLayout l;
+    if (a.n <= kFew) return l;
+    const int bits = bits_of(a.vocab);  // keys 0 .. vocab
+    l.passes = (bits + kMaxBits - 1) / kMaxBits;
+    l.bins = 1 << ((bits + l.passes - 1) / l.passes);
+    l.tiles = (int)((a.n + kSortTile - 1) / kSortTile);
+    l.units = (a.n + kUnit - 1) / kUnit;
+    size_t at = 0;
+    auto take = [&](size_t b) { const size_t p = at; at += up(b); return p; };
+    l.keys = take(4 * (size_t)a.n);
+    l.vals = take(4 * (size_t)a.n);
+    l.keys2 = take(4 * (size_t)a.n);
+    l.vals2 = take(4 * (size_t)a.n);
+    l.counts = take(4 * (size_t)l.bins * (l.tiles + 1));
+    l.present = take((size_t)a.vocab);
+    l.part = take(8 * (size_t)l.units * a.width);
+    l.bytes = at;
+    return l;
+}
+
+}  // namespace
+
+cudaError_t embed(const EmbedArgs &a, cudaStream_t s, int64_t *launches)
+{
+    return with_types(a, [&](auto ti, auto to, auto e) {
+        constexpr int E = decltype(e)::value, NV = E >= 8 ? 4 : 16 / E;
+        int lanes = 1;
+        while (lanes < 32 && lanes * E * NV < a.width) lanes <<= 1;
+        const int tiles = (a.width + lanes * E * NV - 1) / (lanes * E * NV);
+        const int64_t want = (a.n * tiles * lanes + kThreads - 1) / kThreads;
+        const unsigned grid = (unsigned)std::min<int64_t>(want, 16 * kSMs);
+        k_embed<decltype(ti), decltype(to), E, NV><<<grid, kThreads, 0, s>>>(a, lanes, tiles);
+        ++*launches;
+        return cudaGetLastError();
+    });
+}
+
+size_t embed_grad_tmp_bytes(const EmbedArgs &a) { return layout(a).bytes; }
+
+cudaError_t embed_grad(const EmbedArgs &a, void *tmp, int *, cudaStream_t st, int64_t *launches)
+{
+    const GradLayout l = layout(a);
+    if (!l.passes) {
+        return with_types(a, [&](auto ti, auto to, auto e) {
+            constexpr int E = decltype(e)::value;
+            // up to 32 lanes of columns; as many rows as the accumulators
+            // hold, fewer when that leaves SMs without a block
+            const int lanes = std::min((a.width + E - 1) / E, 64);
+            const int tiles = (a.width + lanes * E - 1) / (lanes * E);
+            int64_t rows = std::min<int64_t>(kFewFloats / (lanes * E), a.vocab);
+            while (rows > 8 && (a.vocab + rows - 1) / rows * tiles < 4 * kSMs) rows >>= 1;
+            const dim3 grid((unsigned)((a.vocab + rows - 1) / rows), tiles);
+            k_grad_few<decltype(ti), decltype(to), E><<<grid, kFewThreads, 0, st>>>(a, (int)rows, lanes);
             ++*launches;
             return cudaGetLastError();
         });
+    }
+    char *p = static_cast<char *>(tmp);
+    SortArgs s{};
+    s.counts = (uint32_t *)(p + l.counts);
+    s.tiles = l.tiles;
+    s.bits = bits_of(l.bins) - 1;
+    s.scanned = l.tiles > kSumTiles;
+    uint32_t *keys[2] = {(uint32_t *)(p + l.keys), (uint32_t *)(p + l.keys2)};
+    uint32_t *vals[2] = {(uint32_t *)(p + l.vals), (uint32_t *)(p + l.vals2)};
+    if (!a.accumulate) {
+        s.present = (uint8_t *)(p + l.present);
+        HISS_TRY(cudaMemsetAsync(s.present, 0, (size_t)a.vocab, st));
+    }
+    return with_types(a, [&](auto ti, auto to, auto e) {
+        using TO = decltype(to);
+        constexpr int E = decltype(e)::value;
+        // the empty rows are written in equal parts by the kernels after the first count
+        const int fills = a.accumulate ? 0 : 2 * l.passes - 1;
+        int filled = 0;
+        for (int i = 0; i < l.passes; ++i) {
+            s.shift = i * s.bits;
+            s.keys_in = i ? keys[(i - 1) & 1] : nullptr;
+            s.vals_in = i ? vals[(i - 1) & 1] : nullptr;
+            s.keys_out = keys[i & 1];
+            s.vals_out = vals[i & 1];
+            auto sorted = [&](auto kernel, bool fill) {
+                s.fills = fill ? fills : 0;
+                s.fill = filled;
+                filled += fill;
+                ++*launches;
+                return launch_after(kernel, l.tiles + (s.fills ? kFillBlocks : 0), kSortThreads, 0, st, a, s);
+            };
+            HISS_TRY(sorted(k_sort_count<TO, E>, i > 0));
+            if (s.scanned) {
+                HISS_TRY(launch_after(k_sort_scan, (l.bins + 31) / 32, 1024, 0, st, s));
+                ++*launches;
+            }
+            HISS_TRY(sorted(k_sort_scatter<TO, E>, true));
+        }
+        SumArgs m{};
+        m.keys = s.keys_out;
+        m.vals = s.vals_out;
+        m.part = (float *)(p + l.part);
+        m.units = l.units;
+        lanes_of(a.width, &m.lanes, &m.tiles);
+        const int64_t blocks = (l.units * m.tiles * m.lanes + kThreads - 1) / kThreads;
+        HISS_TRY(launch_after(k_sum<decltype(ti), TO, E>, (unsigned)blocks, kThreads, 0, st, a, m));
+        const int groups = kJoinThreads / m.lanes;
+        HISS_TRY(launch_after(k_join<TO, E>, dim3((unsigned)((l.units + groups - 1) / groups), m.tiles), kJoinThreads, 0, st, a, m));
+        *launches += 2;
+        return cudaSuccess;
     });
 }
 
