@@ -10,18 +10,20 @@
 //   1. the positions are sorted by token (stable LSD radix sort, up to 9 bits
 //      per pass; tokens of a vocabulary below 2^18 take two), while the SMs that the sort
 //      leaves idle write the zeros of the rows without positions;
-//   2. k_sum cuts the sorted positions into units of kUnit: every unit has the
-//      same work however often a token occurs.  A run of equal tokens inside a unit is
-//      summed and written; the run that reaches over a unit's end leaves
-//      float32 partial sums;
-//   3. k_join adds the partial sums of each such run in unit order.
+//   2. k_sum cuts the sorted positions into units of kUnit and sums runs of equal
+//      tokens: a run belongs to the unit it begins in, which follows it
+//      into the next unit.  A run that goes on past that one leaves a float32 partial
+//      sum per unit, so the work of a unit is bounded however often a token occurs;
+//   3. k_join adds the partial sums of each long run in unit order.
 //
 // Sums are float32 in an order that depends on the positions alone: no
 // floating-point atomics.  Few positions take one kernel instead (k_grad_few).
 #include <algorithm>
+#include <atomic>
 
 #include "hiss_internal.cuh"
 #include "numeric.cuh"
+#include "ptx.cuh"
 
 namespace hiss {
 namespace {
@@ -95,6 +97,7 @@ struct SortArgs {
     uint32_t *keys_out, *vals_out;
     uint32_t *counts;    // [tiles][bins], exclusive over tiles once scanned; then [bins] totals
     uint8_t *present;    // [vocab] token occurs (NULL: not wanted)
+    uint32_t *runs;      // set to 0 by the first kernel: number of long runs (SumArgs)
     int tiles, shift, bits, scanned;
     int fill, fills;     // this kernel writes part fill of fills of the empty rows (fills = 0: none)
 };
@@ -118,8 +121,9 @@ __device__ void fill_empty(const EmbedArgs &a, const SortArgs &s)
     Pack<TO, E> zero;
 #pragma unroll
     for (int e = 0; e < E; ++e) zero.v[e] = from_f32<TO>(0.0f);
-    for (int64_t v = v0 + warp * 32; v < v1; v += warps * 32) {
-        unsigned empty = __ballot_sync(0xffffffffu, v + lane < v1 && !s.present[min(v + lane, v1 - 1)]);
+    const int rows = (int)min((int64_t)32, (v1 - v0 + warps - 1) / warps);  // per warp and turn
+    for (int64_t v = v0 + warp * rows; v < v1; v += warps * rows) {
+        unsigned empty = __ballot_sync(0xffffffffu, lane < rows && v + lane < v1 && !s.present[min(v + lane, v1 - 1)]);
         while (empty) {
             const int b = __ffs(empty) - 1;
             empty &= empty - 1;
@@ -141,8 +145,8 @@ __global__ void __launch_bounds__(kSortThreads) k_sort_count(EmbedArgs a, SortAr
         return;
     }
     hist[threadIdx.x] = 0;
+    if (!s.keys_in && blockIdx.x == 0 && threadIdx.x == 0) *s.runs = 0;
     __syncthreads();
-    const int lane = threadIdx.x & 31;
     const uint32_t mask = (1u << s.bits) - 1u;
     const int64_t base = (int64_t)blockIdx.x * kSortTile;
     uint32_t key[kSortItems];
@@ -153,13 +157,9 @@ __global__ void __launch_bounds__(kSortThreads) k_sort_count(EmbedArgs a, SortAr
     }
 #pragma unroll
     for (int k = 0; k < kSortItems; ++k) {
-        const bool valid = base + k * kSortThreads + threadIdx.x < a.n;
-        if (s.present && !s.keys_in && valid && key[k] < (uint32_t)a.vocab) s.present[key[k]] = 1;
-        // equal digits of a warp are added once: a frequent token does not
-        // serialise the warp on one counter
-        const uint32_t d = valid ? (key[k] >> s.shift) & mask : kMaxBins;
-        const uint32_t peers = __match_any_sync(0xffffffffu, d);
-        if (valid && lane == __ffs(peers) - 1) atomicAdd(&hist[d], (uint32_t)__popc(peers));
+        if (base + k * kSortThreads + threadIdx.x >= a.n) continue;
+        if (s.present && !s.keys_in && key[k] < (uint32_t)a.vocab) s.present[key[k]] = 1;
+        atomicAdd(&hist[(key[k] >> s.shift) & mask], 1u);
     }
     __syncthreads();
     const int bins = 1 << s.bits;
@@ -247,18 +247,23 @@ __global__ void __launch_bounds__(kSortThreads) k_sort_scatter(EmbedArgs a, Sort
     uint32_t first = incl - total;
     for (int i = 0; i < warp; ++i) first += warp_total[i];
     base_of[bin] = first + before;
+    // lanes with the same digit, one ballot per bit (a match instruction takes
+    // as long as the warp has distinct digits)
 #pragma unroll
     for (int k = 0; k < kSortItems; ++k) {
         const bool valid = base + k * 32 + lane < a.n;
-        const uint32_t d = valid ? (key[k] >> s.shift) & mask : kMaxBins;
-        const uint32_t peers = __match_any_sync(0xffffffffu, d);
-        const int leader = __ffs(peers) - 1;
-        uint32_t old = 0;
-        if (valid && lane == leader) {
-            old = whist[warp][d];
-            whist[warp][d] = old + __popc(peers);
+        const uint32_t d = valid ? (key[k] >> s.shift) & mask : 0u;
+        uint32_t peers = __ballot_sync(0xffffffffu, valid);
+#pragma unroll
+        for (int b = 0; b < kMaxBits; ++b) {
+            const uint32_t set = __ballot_sync(0xffffffffu, (d >> b) & 1u);
+            peers &= (d >> b) & 1u ? set : ~set;
         }
-        rank[k] = __shfl_sync(0xffffffffu, old, leader) + __popc(peers & ((1u << lane) - 1u));
+        const uint32_t below = __popc(peers & ((1u << lane) - 1u));
+        rank[k] = 0;
+        if (valid) rank[k] = whist[warp][d] + below;
+        __syncwarp();
+        if (valid && below == 0) whist[warp][d] += __popc(peers);
         __syncwarp();
     }
     __syncthreads();
@@ -285,8 +290,10 @@ constexpr int kUnit = 32;  // sorted positions per unit
 
 struct SumArgs {
     const uint32_t *keys, *vals;  // sorted tokens and their positions
-    float *part;                  // [units][2][width]: sum of the run that comes in from the unit
-                                  // before, and of the run that begins here and goes on
+    float *part;                  // [units][2][width]: sum of the long run that comes in from the unit
+                                  // before, and of the long run that begins here
+    uint32_t *runs;               // [0]: number of long runs; then (key, first unit) of each
+    uint32_t *last;               // [vocab]: last unit of a long run
     int64_t units;
     int lanes, tiles;             // lanes * kCols columns per tile
 };
@@ -326,11 +333,18 @@ __device__ __forceinline__ void write_part(const EmbedArgs &a, float *p, int c0,
     }
 }
 
+constexpr int kAhead = 8;  // rows in flight per lane
+
+template <typename TI, int E>
+constexpr size_t sum_bytes() { return (size_t)kThreads * kAhead * kCols * sizeof(TI); }
+
 template <typename TI, typename TO, int E>
 __global__ void __launch_bounds__(kThreads) k_sum(EmbedArgs a, SumArgs s)
 {
     constexpr int NV = kCols / E;
-    constexpr int U = sizeof(TI) == 2 ? 8 : 4;  // rows in flight
+    using P = Pack<TI, E>;
+    constexpr bool kAsync = sizeof(TI) * E >= 4;  // single 16-bit elements cannot be copied asynchronously
+    extern __shared__ __align__(16) char ring[];
     let_next_start();
     wait_for_previous();
     const int64_t item = ((int64_t)blockIdx.x * kThreads + threadIdx.x) / s.lanes;
@@ -338,80 +352,108 @@ __global__ void __launch_bounds__(kThreads) k_sum(EmbedArgs a, SumArgs s)
     if (item >= s.units * s.tiles) return;
     // tiles of a unit are neighbours: they read the same rows of dy
     const int64_t unit = item / s.tiles;
-    const int c0 = ((int)(item - unit * s.tiles) * s.lanes * NV + lane) * E;
-    const int64_t i0 = unit * kUnit;
-    const int m = (int)min((int64_t)kUnit, a.n - i0);
-    const uint32_t vocab = (uint32_t)a.vocab;
-    uint32_t key = s.keys[i0];
-    if (key >= vocab) return;  // only positions without a row from here on
-    // does the run of the first key come in from the unit before?
-    bool inside = i0 == 0 || s.keys[i0 - 1] != key;
-    float *part = s.part + unit * 2 * a.width;
+    const int tile = (int)(item - unit * s.tiles);
+    const int c0 = (tile * s.lanes * NV + lane) * E;
+    const int64_t i0 = unit * kUnit, i1 = min(i0 + kUnit, a.n);
+    const uint32_t vocab = (uint32_t)a.vocab, none = ~0u;
+    auto key_of = [&](int64_t i) { return i >= 0 && i < a.n ? s.keys[i] : none; };
+    const uint32_t k0 = key_of(i0), k1 = key_of(i1 - 1);
+    const uint32_t prev = key_of(i0 - 1), prev_unit = key_of(i0 - kUnit), prev_unit2 = key_of(i0 - kUnit - 1);
+    const uint32_t next = key_of(i1), next_unit = key_of(i1 + kUnit);
+    if (k0 >= vocab) return;  // only positions without a row from here on
+    // the run that comes in: summed by the unit before when it began there and
+    // ends here, a part of a long run otherwise
+    const bool comes_in = prev == k0;
+    const bool long_in = comes_in && !((prev_unit != k0 || prev_unit2 != k0) && (next != k0 || k1 != k0));
+    // the run that goes out: followed into the next unit when it ends there
+    const bool goes_out = next == k1 && k1 < vocab;
+    const bool begins = goes_out && !(k0 == k1 && comes_in);
+    const bool long_out = goes_out && (!begins || next_unit == k1);
+    int64_t i = i0, end = i1;
+    if (comes_in && !long_in)
+        while (i < i1 && s.keys[i] == k0) ++i;
+    if (goes_out && !long_out)
+        while (end < a.n && s.keys[end] == k1) ++end;
+    while (end > i && s.keys[end - 1] >= vocab) --end;
+    if (long_out && begins && tile == 0 && lane == 0) {
+        const uint32_t at = atomicAdd(s.runs, 1u);
+        s.runs[1 + 2 * at] = k1;
+        s.runs[2 + 2 * at] = (uint32_t)unit;
+    }
+    if (long_in && (next != k0 || k1 != k0) && tile == 0 && lane == 0) s.last[k0] = (uint32_t)unit;
+    if (i >= end) return;
+
+    P *slot = reinterpret_cast<P *>(ring) + threadIdx.x;
+    auto fetch = [&](int64_t j) {
+        if (j < end) {
+            const TI *p = static_cast<const TI *>(a.rows) + (int64_t)s.vals[j] * a.rows_stride + c0;
+#pragma unroll
+            for (int q = 0; q < NV; ++q) {
+                if (c0 + q * s.lanes * E >= a.width) continue;
+                P *d = slot + ((j & (kAhead - 1)) * NV + q) * kThreads;
+                if constexpr (kAsync) copy_pack_async<TI, E>(d, p + q * s.lanes * E);
+                else *d = load_pack<TI, E>(p + q * s.lanes * E);
+            }
+        }
+        cp_async_commit();
+    };
+    for (int k = 0; k < kAhead - 1; ++k) fetch(i + k);
     float acc[kCols];
 #pragma unroll
     for (int c = 0; c < kCols; ++c) acc[c] = 0.0f;
-    for (int j = 0; j < m; j += U) {
-        uint32_t k[U];
-        Pack<TI, E> v[U][NV];
+    float *part = s.part + unit * 2 * a.width;
+    bool head = long_in;  // the current run is the long one that came in
+    uint32_t key = s.keys[i];
+    while (i < end) {
+        fetch(i + kAhead - 1);
+        cp_async_wait<kAhead - 1>();
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            k[u] = vocab;
-            if (j + u < m) {
-                k[u] = s.keys[i0 + j + u];
-                const TI *p = static_cast<const TI *>(a.rows) + (int64_t)s.vals[i0 + j + u] * a.rows_stride;
+        for (int q = 0; q < NV; ++q) {
+            const P v = slot[((i & (kAhead - 1)) * NV + q) * kThreads];
 #pragma unroll
-                for (int q = 0; q < NV; ++q) {
-                    const int c = c0 + q * s.lanes * E;
-                    if (c < a.width && k[u] < vocab) v[u][q] = load_pack<TI, E>(p + c);
-                }
-            }
+            for (int e = 0; e < E; ++e) acc[q * E + e] += to_f32(v.v[e]);
         }
+        ++i;
+        const uint32_t k = i < end ? s.keys[i] : none;
+        if (k == key) continue;
+        const bool tail = i >= end && long_out;
+        if (head || tail) write_part<E, NV>(a, head ? part : part + a.width, c0, s.lanes, acc);
+        else write_row<TO, E, NV>(a, key, c0, s.lanes, acc);
+        key = k;
+        head = false;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (k[u] != key) {
-                if (inside) write_row<TO, E, NV>(a, key, c0, s.lanes, acc);
-                else write_part<E, NV>(a, part, c0, s.lanes, acc);
-                key = k[u];
-                if (key >= vocab) return;
-                inside = true;
-#pragma unroll
-                for (int c = 0; c < kCols; ++c) acc[c] = 0.0f;
-            }
-#pragma unroll
-            for (int q = 0; q < NV; ++q)
-#pragma unroll
-                for (int e = 0; e < E; ++e) acc[q * E + e] += to_f32(v[u][q].v[e]);
-        }
+        for (int c = 0; c < kCols; ++c) acc[c] = 0.0f;
     }
-    const bool goes_on = i0 + m < a.n && s.keys[i0 + m] == key;
-    if (inside && !goes_on) write_row<TO, E, NV>(a, key, c0, s.lanes, acc);
-    else write_part<E, NV>(a, inside ? part + a.width : part, c0, s.lanes, acc);
 }
 
 constexpr int kJoinThreads = 512;
-constexpr int kJoinLong = 32;  // runs over more units than this are summed by a whole block
+constexpr int kJoinBlocks = 4 * kSMs;
 
-// Rows whose run reaches over the end of unit u (and begins in u): the sum of
-// u's second part and of the first parts of the units that the run goes on in.
-// One group of lanes per unit and tile; a long run is left to its block, whose
-// groups each take a stretch of its units, added up in order.
+// The row of each long run: the second part of the unit it begins in and the
+// first parts of the units up to its last.  One block per run and tile at a
+// time; its groups of lanes each take a stretch of the units, added up in a
+// fixed tree.
 template <typename TO, int E>
 __global__ void __launch_bounds__(kJoinThreads) k_join(EmbedArgs a, SumArgs s)
 {
     constexpr int NV = kCols / E;
-    __shared__ float sh[kJoinThreads * kCols];
-    __shared__ uint32_t long_key[kJoinThreads];  // key + 1 of each group's long run, 0: none
+    __shared__ float sh[kJoinThreads / 2 * kCols];
     wait_for_previous();
     const int lanes = s.lanes, groups = kJoinThreads / lanes;
     const int group = threadIdx.x / lanes, lane = threadIdx.x & (lanes - 1);
-    const int tile = blockIdx.y;
-    const int c0 = (tile * lanes * NV + lane) * E;
-    const int64_t u0 = (int64_t)blockIdx.x * groups;
-    const uint32_t vocab = (uint32_t)a.vocab;
-    auto add_parts = [&](int64_t from, int64_t to, float(&acc)[kCols]) {
+    const int64_t items = (int64_t)s.runs[0] * s.tiles;
+    for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
+        const int64_t run = it / s.tiles;
+        const int c0 = ((int)(it - run * s.tiles) * lanes * NV + lane) * E;
+        const uint32_t key = s.runs[1 + 2 * run];
+        const int64_t first = s.runs[2 + 2 * run], count = (int64_t)s.last[key] - first + 1;
+        float acc[kCols];
+#pragma unroll
+        for (int c = 0; c < kCols; ++c) acc[c] = 0.0f;
+        const int64_t to = first + count * (group + 1) / groups;
 #pragma unroll 4
-        for (int64_t u = from; u < to; ++u) {
-            const float *p = s.part + u * 2 * a.width;
+        for (int64_t u = first + count * group / groups; u < to; ++u) {
+            const float *p = s.part + (u * 2 + (u == first)) * a.width;
 #pragma unroll
             for (int q = 0; q < NV; ++q) {
                 const int c = c0 + q * lanes * E;
@@ -421,80 +463,18 @@ __global__ void __launch_bounds__(kJoinThreads) k_join(EmbedArgs a, SumArgs s)
                 for (int e = 0; e < E; ++e) acc[q * E + e] += v.v[e];
             }
         }
-    };
-    // the second part of unit u
-    auto begin = [&](int64_t u, float(&acc)[kCols]) {
-        const float *p = s.part + (u * 2 + 1) * a.width;
-#pragma unroll
-        for (int q = 0; q < NV; ++q) {
-            const int c = c0 + q * lanes * E;
-            if (c >= a.width) continue;
-            const auto v = load_pack<float, E>(p + c);
-#pragma unroll
-            for (int e = 0; e < E; ++e) acc[q * E + e] = v.v[e];
-        }
-    };
-    if (lane == 0) long_key[group] = 0;
-    __syncthreads();
-    const int64_t u = u0 + group;
-    if (u + 1 < s.units) {
-        const int64_t end = (u + 1) * kUnit;  // first position of the next unit
-        const uint32_t key = s.keys[end];
-        const bool begins = s.keys[u * kUnit] != key || u == 0 || s.keys[u * kUnit - 1] != key;
-        if (key < vocab && s.keys[end - 1] == key && begins) {
-            // the run's last unit: the first whose successor begins with another token
-            int64_t last = u + 1;
-            for (bool more = true; more && last - u <= kJoinLong;) {
-                uint32_t k[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) k[i] = last + 1 + i < s.units ? s.keys[(last + 1 + i) * kUnit] : vocab;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    more = more && k[i] == key;
-                    last += more;
-                }
-            }
-            if (last - u <= kJoinLong) {
-                float acc[kCols];
-                begin(u, acc);
-                add_parts(u + 1, last + 1, acc);
-                write_row<TO, E, NV>(a, key, c0, lanes, acc);
-            } else if (lane == 0) {
-                long_key[group] = key + 1;
-            }
-        }
-    }
-    __syncthreads();
-    for (int g = 0; g < groups; ++g) {
-        if (!long_key[g]) continue;
-        const uint32_t key = long_key[g] - 1;
-        const int64_t b = u0 + g;
-        // the run's last unit by bisection over the units' first tokens (sorted)
-        int64_t lo = b + 1, hi = s.units;
-        while (hi - lo > 1) {
-            const int64_t mid = (lo + hi) >> 1;
-            if (s.keys[mid * kUnit] == key) lo = mid;
-            else hi = mid;
-        }
-        const int64_t count = lo - b;  // units b + 1 .. lo
-        float acc[kCols];
-#pragma unroll
-        for (int c = 0; c < kCols; ++c) acc[c] = 0.0f;
-        if (group == 0) begin(b, acc);
-        add_parts(b + 1 + count * group / groups, b + 1 + count * (group + 1) / groups, acc);
-        // pairs of groups, a fixed tree
         for (int half = groups >> 1; half > 0; half >>= 1) {
+            const int at = threadIdx.x - half * lanes;
             __syncthreads();
             if (group >= half && group < 2 * half)
 #pragma unroll
-                for (int c = 0; c < kCols; ++c) sh[c * kJoinThreads + threadIdx.x] = acc[c];
+                for (int c = 0; c < kCols; ++c) sh[c * (kJoinThreads / 2) + at] = acc[c];
             __syncthreads();
             if (group < half)
 #pragma unroll
-                for (int c = 0; c < kCols; ++c) acc[c] += sh[c * kJoinThreads + threadIdx.x + half * lanes];
+                for (int c = 0; c < kCols; ++c) acc[c] += sh[c * (kJoinThreads / 2) + threadIdx.x];
         }
         if (group == 0) write_row<TO, E, NV>(a, key, c0, lanes, acc);
-        __syncthreads();
     }
 }
 
@@ -504,9 +484,9 @@ constexpr int64_t kFew = 1024;
 constexpr int kFewThreads = 256;
 constexpr int kFewFloats = 8192;  // accumulators of a block
 
-// One kernel without a sort: a block owns a range of rows and of columns (its
-// accumulators in shared memory), picks the positions whose token falls into
-// its rows, in order, and adds them up; every row of the range is written.
+// One kernel without a sort: a block owns some rows and a range of columns (its
+// accumulators in shared memory), picks the positions whose token is one of
+// its rows, in order, and adds them up; every one of its rows is written.
 template <typename TI, typename TO, int E>
 __global__ void __launch_bounds__(kFewThreads) k_grad_few(EmbedArgs a, int rows, int lanes)
 {
@@ -515,22 +495,25 @@ __global__ void __launch_bounds__(kFewThreads) k_grad_few(EmbedArgs a, int rows,
     __shared__ uint32_t warp_count[kFewThreads / 32];
     __shared__ uint8_t touched[kFewFloats];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t v0 = (int64_t)blockIdx.x * rows;
-    const int nrows = (int)min((int64_t)rows, a.vocab - v0);
+    // row i of the block is row i * blocks + block of the table: frequent
+    // tokens, which a vocabulary often has next to one another, go to different blocks
+    const uint32_t blocks = gridDim.x, block = blockIdx.x;
+    const int nrows = (int)((a.vocab - block + blocks - 1) / blocks);
     const int cols = lanes * E;              // columns of the tile
     const int c0 = blockIdx.y * cols;
     for (int i = threadIdx.x; i < rows; i += kFewThreads) touched[i] = 0;
     constexpr int R = kFew / kFewThreads;
-    int64_t r[R];
+    int r[R];  // row in the block, -1: another block's or none
 #pragma unroll
     for (int k = 0; k < R; ++k) {
         const int64_t i = k * kFewThreads + threadIdx.x;
-        r[k] = i < a.n ? row_of(a, i, a.bad) : -1;
+        const int64_t v = i < a.n ? row_of(a, i, a.bad) : -1;
+        r[k] = v >= 0 && (uint32_t)v % blocks == block ? (int)((uint32_t)v / blocks) : -1;
     }
     __syncthreads();
     uint32_t count = 0;
     for (int k = 0; k < R; ++k) {
-        const bool hit = r[k] >= v0 && r[k] < v0 + nrows;
+        const bool hit = r[k] >= 0;
         const uint32_t m = __ballot_sync(0xffffffffu, hit);
         if (lane == 0) warp_count[warp] = __popc(m);
         __syncthreads();
@@ -540,8 +523,8 @@ __global__ void __launch_bounds__(kFewThreads) k_grad_few(EmbedArgs a, int rows,
             count += warp_count[w];
         }
         if (hit) {
-            found[at + __popc(m & ((1u << lane) - 1u))] = (uint32_t)(r[k] - v0) << 10 | (uint32_t)(k * kFewThreads + threadIdx.x);
-            touched[r[k] - v0] = 1;
+            found[at + __popc(m & ((1u << lane) - 1u))] = (uint32_t)r[k] << 10 | (uint32_t)(k * kFewThreads + threadIdx.x);
+            touched[r[k]] = 1;
         }
         __syncthreads();
     }
@@ -572,7 +555,7 @@ __global__ void __launch_bounds__(kFewThreads) k_grad_few(EmbedArgs a, int rows,
     }
     for (int i = group; i < nrows; i += groups) {
         if (a.accumulate && !touched[i]) continue;
-        TO *p = static_cast<TO *>(a.out) + (v0 + i) * a.out_stride + c;
+        TO *p = static_cast<TO *>(a.out) + ((int64_t)i * blocks + block) * a.out_stride + c;
         Pack<TO, E> o;
         if (a.accumulate) o = load_pack<TO, E>(p);
 #pragma unroll
@@ -637,7 +620,7 @@ void lanes_of(int width, int *lanes, int *tiles)
 struct GradLayout {
     int passes = 0, tiles = 0, bins = 0;
     int64_t units = 0;
-    size_t keys = 0, vals = 0, keys2 = 0, vals2 = 0, counts = 0, present = 0, part = 0, bytes = 0;
+    size_t keys = 0, vals = 0, keys2 = 0, vals2 = 0, counts = 0, present = 0, part = 0, runs = 0, last = 0, bytes = 0;
 };
 
 GradLayout layout(const EmbedArgs &a)
@@ -658,6 +641,8 @@ GradLayout layout(const EmbedArgs &a)
     l.counts = take(4 * (size_t)l.bins * (l.tiles + 1));
     l.present = take((size_t)a.vocab);
     l.part = take(8 * (size_t)l.units * a.width);
+    l.runs = take(8 * (size_t)l.units + 4);  // a long run begins in a unit of its own
+    l.last = take(4 * (size_t)a.vocab);
     l.bytes = at;
     return l;
 }
@@ -702,6 +687,7 @@ cudaError_t embed_grad(const EmbedArgs &a, void *tmp, int *, cudaStream_t st, in
     char *p = static_cast<char *>(tmp);
     SortArgs s{};
     s.counts = (uint32_t *)(p + l.counts);
+    s.runs = (uint32_t *)(p + l.runs);
     s.tiles = l.tiles;
     s.bits = bits_of(l.bins) - 1;
     s.scanned = l.tiles > kSumTiles;
@@ -741,12 +727,23 @@ cudaError_t embed_grad(const EmbedArgs &a, void *tmp, int *, cudaStream_t st, in
         m.keys = s.keys_out;
         m.vals = s.vals_out;
         m.part = (float *)(p + l.part);
+        m.runs = s.runs;
+        m.last = (uint32_t *)(p + l.last);
         m.units = l.units;
         lanes_of(a.width, &m.lanes, &m.tiles);
         const int64_t blocks = (l.units * m.tiles * m.lanes + kThreads - 1) / kThreads;
-        HISS_TRY(launch_after(k_sum<decltype(ti), TO, E>, (unsigned)blocks, kThreads, 0, st, a, m));
-        const int groups = kJoinThreads / m.lanes;
-        HISS_TRY(launch_after(k_join<TO, E>, dim3((unsigned)((l.units + groups - 1) / groups), m.tiles), kJoinThreads, 0, st, a, m));
+        using TI = decltype(ti);
+        auto sum = k_sum<TI, TO, E>;
+        constexpr size_t smem = sum_bytes<TI, E>();
+        if (smem > 48 * 1024) {
+            static std::atomic<bool> allowed{false};
+            if (!allowed.load(std::memory_order_acquire)) {
+                HISS_TRY(cudaFuncSetAttribute(sum, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
+                allowed.store(true, std::memory_order_release);
+            }
+        }
+        HISS_TRY(launch_after(sum, (unsigned)blocks, kThreads, smem, st, a, m));
+        HISS_TRY(launch_after(k_join<TO, E>, kJoinBlocks, kJoinThreads, 0, st, a, m));
         *launches += 2;
         return cudaSuccess;
     });

@@ -90,7 +90,7 @@ struct Exchange {
 template <typename T, int E, int NV, int S>
 struct Stream {
     using P = Pack<T, E>;
-    static constexpr bool kAsync = sizeof(P) >= 4 && (sizeof(T) * E) % 4 == 0;
+    static constexpr bool kAsync = sizeof(T) * E >= 4;
     static constexpr size_t kThreadBytes = kAsync ? sizeof(P) * NV * S : 0;
     P *slot;
     P cur[kAsync ? 1 : NV], next[kAsync ? 1 : NV];
@@ -102,16 +102,7 @@ struct Stream {
     __device__ __forceinline__ void fetch(int st, int v, const T *p)
     {
         if constexpr (kAsync) {
-            char *d = reinterpret_cast<char *>(slot + (st * NV + v) * blockDim.x);
-            const char *q = reinterpret_cast<const char *>(p);
-            if constexpr (sizeof(T) * E >= 16) {
-#pragma unroll
-                for (size_t i = 0; i < sizeof(T) * E; i += 16) cp_async16(d + i, q + i);
-            } else if constexpr (sizeof(T) * E == 8) {
-                asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(d)), "l"(q) : "memory");
-            } else {
-                asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(d)), "l"(q) : "memory");
-            }
+            copy_pack_async<T, E>(slot + (st * NV + v) * blockDim.x, p);
         } else {
             next[v] = load_pack<T, E>(p);
         }
