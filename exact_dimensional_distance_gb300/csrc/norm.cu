@@ -27,13 +27,14 @@ namespace {
 
 constexpr int kMaxLanes = 512;  // of a group, and threads of a block
 constexpr int kMaxWarps = kMaxLanes / 32;
-constexpr int kRingBytes = 208 * 1024;  // shared memory that a ring of a full block may take
+constexpr size_t kSharedBytes = 216 * 1024;  // dynamic shared memory of a block
 
 // ---- groups ---------------------------------------------------------------------
 
 struct Group {
     int lanes, id, lane;   // lanes per group; this thread's group in the block and lane in the group
     int warps, warp;       // warps per group and this thread's warp in the group (NARROW: 1 and 0)
+    int span;              // half the power of two that covers the warps
 };
 
 template <bool NARROW>
@@ -45,6 +46,8 @@ __device__ __forceinline__ Group group_of(int lanes)
     g.lane = threadIdx.x - g.id * lanes;
     g.warps = NARROW ? 1 : lanes >> 5;
     g.warp = NARROW ? 0 : g.lane >> 5;
+    g.span = 0;
+    while (g.warps > (g.span ? 2 * g.span : 1)) g.span = g.span ? 2 * g.span : 1;
     return g;
 }
 
@@ -74,6 +77,22 @@ __device__ __forceinline__ float warp_sum(const Group &g, float v)
     return v;
 }
 
+// Sum over the first lanes of a warp that hold a value per warp of the group
+// (the others hold 0), in every lane.
+__device__ __forceinline__ float group_sum(const Group &g, float v)
+{
+    for (int o = g.span; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return __shfl_sync(0xffffffffu, v, 0);
+}
+
+// 1 / sqrt(v): the hardware's approximation and one Newton step.
+__device__ __forceinline__ float inv_sqrt(float v)
+{
+    const float r = rsqrtf(v);
+    const float n = fmaf(0.5f * r, fmaf(-v * r, r, 1.0f), r);
+    return r > 0.0f && r < INFINITY ? n : r;  // v = 0, infinite, negative or NaN: as it is
+}
+
 // One float2 per warp of a group, double-buffered by parity so that one
 // barrier per row is enough: a warp that writes a buffer again has passed the
 // barrier of the row between, which every reader of the buffer's old contents
@@ -81,6 +100,13 @@ __device__ __forceinline__ float warp_sum(const Group &g, float v)
 struct Exchange {
     float2 slot[2][kMaxWarps];
 };
+
+// A lane's elements are handled as float32 pairs, in chunks: the pairs of a
+// pack, or two packs of one element.
+template <int E>
+constexpr int kPairs = E == 1 ? 1 : E / 2;
+template <int E, int NV>
+constexpr int kChunks = E == 1 ? NV / 2 : NV;
 
 // ---- the rows to come -------------------------------------------------------------
 
@@ -107,10 +133,21 @@ struct Stream {
             next[v] = load_pack<T, E>(p);
         }
     }
-    __device__ __forceinline__ P get(int st, int v) const
+    // Chunk c of the row in stage st: a pack as float32 pairs, or two packs of
+    // one element as a pair, the second 0 unless the row reaches it.
+    __device__ __forceinline__ void get(int st, int c, bool second, float2 (&x)[kPairs<E>]) const
     {
-        if constexpr (kAsync) return slot[(st * NV + v) * blockDim.x];
-        else return cur[v];
+        auto pack = [&](int v) {
+            if constexpr (kAsync) return slot[(st * NV + v) * blockDim.x];
+            else return cur[v];
+        };
+        if constexpr (E == 1) {
+            x[0] = make_float2(to_f32(pack(2 * c).v[0]), second ? to_f32(pack(2 * c + 1).v[0]) : 0.0f);
+        } else {
+            const P p = pack(c);
+#pragma unroll
+            for (int h = 0; h < E / 2; ++h) x[h] = pair_of(p.v + 2 * h);
+        }
     }
     // Make the row fetched last the current one (register form).
     __device__ __forceinline__ void turn()
@@ -121,10 +158,11 @@ struct Stream {
     }
 };
 
-// Rows in flight per thread: what fits kRingBytes, at most 4.
-constexpr int stages(size_t row_bytes)
+// Rows in the ring: at most 4, so many that a block of kMaxLanes threads fits
+// with other bytes per lane beside the ring.
+constexpr int stages(size_t row_bytes, size_t other)
 {
-    const int s = (int)(kRingBytes / (kMaxLanes * row_bytes));
+    const int s = (int)((kSharedBytes / kMaxLanes - other) / row_bytes);
     return s > 4 ? 4 : s;
 }
 
@@ -155,7 +193,7 @@ Rows plan_rows(const NormArgs &a, bool has32, int threads)
     Rows r;
     const int e = fits(wide) ? wide : half && fits(2) ? 2 : 1;
     int per = 16;
-    if (has32 && e == wide && a.width > per * kMaxLanes) per = 32;
+    if (has32 && e == wide && (a.width > per * kMaxLanes || (half && a.width >= 1024))) per = 32;
     const int lanes = (a.width + per - 1) / per;
     if (lanes > kMaxLanes) return r;
     r.e = e;
@@ -184,7 +222,7 @@ int resident(K kernel, int threads, size_t smem, Residency &cache)
     std::atomic<int> &c = cache.blocks[threads / 32];
     int v = c.load(std::memory_order_acquire);
     if (v == 0) {
-        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 220 * 1024) != cudaSuccess ||
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSharedBytes) != cudaSuccess ||
             cudaOccupancyMaxActiveBlocksPerMultiprocessor(&v, kernel, threads, smem) != cudaSuccess || v < 1)
             v = 1;
         c.store(v, std::memory_order_release);
@@ -192,47 +230,102 @@ int resident(K kernel, int threads, size_t smem, Residency &cache)
     return v;
 }
 
+// ---- parameters -----------------------------------------------------------------
+
+// The weights (or biases) of a lane's columns, as float32 pairs, for every row
+// the block takes: in registers, or with four packs of 8 elements in shared
+// memory (one copy per block, 16-byte accesses without bank conflicts): 64
+// registers of them would halve the warps per SM.
+template <bool NARROW, int E, int NV>
+struct Params {
+    static constexpr bool kShared = E == 8 && NV == 4;
+    static constexpr size_t kLaneBytes = kShared ? 4 * E * NV : 0;  // of shared memory
+    float2 held[kShared ? 1 : kChunks<E, NV>][kPairs<E>];
+    float4 *sh;
+    int lanes;
+
+    // Called by every thread; the block synchronises before the first get.
+    __device__ __forceinline__ void open(const Group &g, const void *p, int dtype, float none, int col, int vs, int width,
+                                         char *base)
+    {
+        sh = reinterpret_cast<float4 *>(base) + g.lane;
+        lanes = g.lanes;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            float t[E];
+#pragma unroll
+            for (int e = 0; e < E; ++e) t[e] = none;
+            if (p && col + v * vs < width) load_params<E>(p, dtype, col + v * vs, t);
+            if constexpr (kShared) {
+                if (g.id == 0)
+#pragma unroll
+                    for (int e = 0; e < E; e += 4)
+                        sh[(v * (E / 4) + e / 4) * lanes] = make_float4(t[e], t[e + 1], t[e + 2], t[e + 3]);
+            } else if constexpr (E == 1) {
+                if (v & 1) held[v / 2][0].y = t[0];
+                else held[v / 2][0].x = t[0];
+            } else {
+#pragma unroll
+                for (int h = 0; h < E / 2; ++h) held[v][h] = make_float2(t[2 * h], t[2 * h + 1]);
+            }
+        }
+    }
+    __device__ __forceinline__ void get(int c, float2 (&t)[kPairs<E>]) const
+    {
+        if constexpr (kShared) {
+#pragma unroll
+            for (int q = 0; q < E / 4; ++q) {
+                const float4 f = sh[(c * (E / 4) + q) * lanes];
+                t[2 * q] = make_float2(f.x, f.y);
+                t[2 * q + 1] = make_float2(f.z, f.w);
+            }
+        } else {
+#pragma unroll
+            for (int h = 0; h < kPairs<E>; ++h) t[h] = held[c][h];
+        }
+    }
+};
+
+// Store chunk c of a row at p (the lane's first column).
+template <typename T, int E>
+__device__ __forceinline__ void store_chunk(T *p, int c, int vs, bool second, const float2 (&r)[kPairs<E>])
+{
+    if constexpr (E == 1) {
+        p[2 * c * vs] = from_f32<T>(r[0].x);
+        if (second) p[(2 * c + 1) * vs] = from_f32<T>(r[0].y);
+    } else {
+        Pack<T, E> o;
+#pragma unroll
+        for (int h = 0; h < E / 2; ++h) set_pair(o.v + 2 * h, r[h]);
+        store_pack<T, E>(p + c * vs, o);
+    }
+}
+
 // ---- forward --------------------------------------------------------------------
 
-template <typename TX, typename TY, int E, int NV, bool NARROW>
+template <typename TX, int E, int NV>
 struct Forward {
-    static constexpr int kStages = stages(sizeof(TX) * E * NV);
+    static constexpr size_t kParamBytes = 2 * Params<false, E, NV>::kLaneBytes;
+    static constexpr int kStages = stages(sizeof(TX) * E * NV, kParamBytes);
+    static_assert(kStages >= 2, "a row ahead");
     using X = Stream<TX, E, NV, kStages>;
-    static constexpr size_t kThreadBytes = X::kThreadBytes;
+    static size_t smem(int threads, int lanes) { return X::kThreadBytes * threads + kParamBytes * lanes; }
 };
 
 template <typename TX, typename TY, int E, int NV, bool NARROW>
 __global__ void __launch_bounds__(kMaxLanes) k_norm(NormArgs a, int lanes, int groups)
 {
-    using F = Forward<TX, TY, E, NV, NARROW>;
-    constexpr int S = F::kStages, C = NV * E;
+    using F = Forward<TX, E, NV>;
+    using PA = Params<NARROW, E, NV>;
+    constexpr int S = F::kStages, C = NV * E, H = kPairs<E>, NC = kChunks<E, NV>;
     extern __shared__ __align__(16) char ring[];
     __shared__ Exchange ex[kMaxWarps];
     const Group g = group_of<NARROW>(lanes);
     const int col = column_of<NARROW, E, NV>(g);
     const int vs = E * (NARROW ? lanes : 32);
-    float w[C], b[C];
-#pragma unroll
-    for (int v = 0; v < NV; ++v) {
-        float t[E];
-#pragma unroll
-        for (int e = 0; e < E; ++e) w[v * E + e] = 1.0f, b[v * E + e] = 0.0f;
-        if (col + v * vs >= a.width) continue;
-        if (a.weight) {
-            load_params<E>(a.weight, a.p_dtype, col + v * vs, t);
-#pragma unroll
-            for (int e = 0; e < E; ++e) w[v * E + e] = t[e];
-        }
-        if (a.bias) {
-            load_params<E>(a.bias, a.p_dtype, col + v * vs, t);
-#pragma unroll
-            for (int e = 0; e < E; ++e) b[v * E + e] = t[e];
-        }
-    }
-    const float width = (float)a.width;
-    // columns of this thread's warp, and of warp (lane id) of the group
-    auto columns = [&](int i) { return (float)min(max(a.width - i * 32 * C, 0), 32 * C); };
-    const float my_n = NARROW ? width : columns(g.warp), lane_n = NARROW ? 0.0f : columns(threadIdx.x & 31);
+    // the row reaches chunk c, and (packs of one element) its second half
+    auto has = [&](int c) { return col + (E == 1 ? 2 * c : c) * vs < a.width; };
+    auto has_second = [&](int c) { return E > 1 || col + (2 * c + 1) * vs < a.width; };
     const int64_t step = (int64_t)gridDim.x * groups;
     int64_t row = (int64_t)blockIdx.x * groups + g.id;
     // the loop runs for whole warps: as long as the warp's first row exists
@@ -254,6 +347,16 @@ __global__ void __launch_bounds__(kMaxLanes) k_norm(NormArgs a, int lanes, int g
     } else {
         fetch(0, row);
     }
+    PA w, b;
+    char *params = ring + F::X::kThreadBytes * blockDim.x;
+    w.open(g, a.weight, a.p_dtype, 1.0f, col, vs, a.width, params);
+    b.open(g, a.bias, a.p_dtype, 0.0f, col, vs, a.width, params + PA::kLaneBytes * lanes);
+    if constexpr (PA::kShared) __syncthreads();
+    const float inv_width = 1.0f / (float)a.width;
+    // columns of this thread's warp, and of warp (lane id) of the group
+    auto columns = [&](int i) { return (float)min(max(a.width - i * 32 * C, 0), 32 * C); };
+    const float my_n = NARROW ? (float)a.width : columns(g.warp), inv_my_n = my_n > 0.0f ? 1.0f / my_n : 0.0f;
+    const float lane_n = NARROW ? 0.0f : columns(threadIdx.x & 31);
     int st = 0;
     for (int parity = 0; first < a.n; first += step, row += step, parity ^= 1) {
         if constexpr (F::X::kAsync) {
@@ -263,49 +366,51 @@ __global__ void __launch_bounds__(kMaxLanes) k_norm(NormArgs a, int lanes, int g
             xs.turn();
             fetch(0, row + step);
         }
-        float x[C];
-        float s = 0.0f;
+        float2 x[NC][H];
+        float2 s2 = both(0.0f);
 #pragma unroll
-        for (int v = 0; v < NV; ++v) {
-            const auto p = xs.get(st, v);
+        for (int c = 0; c < NC; ++c)
+            if (has(c)) {
+                xs.get(st, c, has_second(c), x[c]);
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-                x[v * E + e] = to_f32(p.v[e]);
-                if (col + v * vs < a.width) s += x[v * E + e];
+                for (int h = 0; h < H; ++h) s2 = __fadd2_rn(s2, x[c][h]);
             }
-        }
         // mean and sum of squared differences of the warp's columns, then of the
         // row from those of its warps: M2 = sum of (M2_w + n_w (m_w - m)^2)
-        float mean = my_n > 0.0f ? warp_sum<NARROW>(g, s) / my_n : 0.0f;
-        float q = 0.0f;
+        float mean = warp_sum<NARROW>(g, s2.x + s2.y) * inv_my_n;
+        float2 q2 = both(0.0f);
 #pragma unroll
-        for (int v = 0; v < NV; ++v)
+        for (int c = 0; c < NC; ++c)
+            if (has(c))
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const float d = x[v * E + e] - mean;
-                if (col + v * vs < a.width) q = fmaf(d, d, q);
-            }
-        q = warp_sum<NARROW>(g, q);
+                for (int h = 0; h < H; ++h) {
+                    float2 d = __fadd2_rn(x[c][h], both(-mean));
+                    if (!has_second(c)) d.y = 0.0f;
+                    q2 = __ffma2_rn(d, d, q2);
+                }
+        float q = warp_sum<NARROW>(g, q2.x + q2.y);
         if (!NARROW && g.warps > 1) {
             float2 *slot = ex[g.id].slot[parity];
             if ((threadIdx.x & 31) == 0) slot[g.warp] = make_float2(mean, q);
             group_barrier(g);
             const float2 mine = (threadIdx.x & 31) < g.warps ? slot[threadIdx.x & 31] : make_float2(0.0f, 0.0f);
-            mean = warp_sum<NARROW>(g, lane_n * mine.x) / width;
+            mean = group_sum(g, lane_n * mine.x) * inv_width;
             const float d = mine.x - mean;
-            q = warp_sum<NARROW>(g, lane_n > 0.0f ? fmaf(lane_n * d, d, mine.y) : 0.0f);
+            q = group_sum(g, lane_n > 0.0f ? fmaf(lane_n * d, d, mine.y) : 0.0f);
         }
-        const float rstd = 1.0f / sqrtf(q / width + a.eps);
+        const float rstd = inv_sqrt(q * inv_width + a.eps);
         if (row < a.n) {
             TY *y = static_cast<TY *>(a.y) + row * a.y_stride + col;
 #pragma unroll
-            for (int v = 0; v < NV; ++v) {
-                if (col + v * vs >= a.width) continue;
-                Pack<TY, E> o;
+            for (int c = 0; c < NC; ++c) {
+                if (!has(c)) continue;
+                float2 tw[H], tb[H], r[H];
+                w.get(c, tw);
+                b.get(c, tb);
 #pragma unroll
-                for (int e = 0; e < E; ++e)
-                    o.v[e] = from_f32<TY>(fmaf((x[v * E + e] - mean) * rstd, w[v * E + e], b[v * E + e]));
-                store_pack<TY, E>(y + v * vs, o);
+                for (int h = 0; h < H; ++h)
+                    r[h] = __ffma2_rn(__fmul2_rn(__fadd2_rn(x[c][h], both(-mean)), both(rstd)), tw[h], tb[h]);
+                store_chunk<TY, E>(y, c, vs, has_second(c), r);
             }
             if (g.lane == 0) {
                 if (a.mean) a.mean[row] = mean;
@@ -320,10 +425,18 @@ __global__ void __launch_bounds__(kMaxLanes) k_norm(NormArgs a, int lanes, int g
 
 template <typename TX, typename TY, int E, int NV>
 struct Backward {
-    static constexpr int kStages = stages((sizeof(TX) + sizeof(TY)) * E * NV);
+    static constexpr size_t kParamBytes = Params<false, E, NV>::kLaneBytes;
+    static constexpr int kStages = stages((sizeof(TX) + sizeof(TY)) * E * NV, kParamBytes);
+    static_assert(kStages >= 2, "a row ahead");
     using X = Stream<TX, E, NV, kStages>;
     using Y = Stream<TY, E, NV, kStages>;
     static constexpr size_t kThreadBytes = X::kThreadBytes + Y::kThreadBytes;
+    // the ring and the weights; the ring's memory holds the column sums of half of the
+    // block's threads at the end
+    static size_t smem(int threads, int lanes, bool many)
+    {
+        return std::max(kThreadBytes * threads + kParamBytes * lanes, many ? 4 * (size_t)threads * E * NV : 0);
+    }
 };
 
 // Each block leaves its column sums in part[block][0 .. width) (dw) and
@@ -332,33 +445,16 @@ template <typename TX, typename TY, int E, int NV, bool NARROW>
 __global__ void __launch_bounds__(kMaxLanes) k_norm_grad(NormArgs a, int lanes, int groups, float *part)
 {
     using B = Backward<TX, TY, E, NV>;
-    constexpr int S = B::kStages, C = NV * E;
-    // with 32 elements per lane the weights are read again for each row (they
-    // stay in L1); 96 registers of them and the column sums would spill
-    constexpr bool kHeld = C <= 16;
+    using PA = Params<NARROW, E, NV>;
+    constexpr int S = B::kStages, H = kPairs<E>, NC = kChunks<E, NV>;
     extern __shared__ __align__(16) char ring[];
     __shared__ Exchange ex[kMaxWarps];
     const Group g = group_of<NARROW>(lanes);
     const int col = column_of<NARROW, E, NV>(g);
     const int vs = E * (NARROW ? lanes : 32);
-    float w[kHeld ? C : 1], dw[C], db[C];
-    auto weights = [&](int v, float(&t)[E]) {
-#pragma unroll
-        for (int e = 0; e < E; ++e) t[e] = 1.0f;
-        if (a.weight && col + v * vs < a.width) load_params<E>(a.weight, a.p_dtype, col + v * vs, t);
-    };
-#pragma unroll
-    for (int v = 0; v < NV; ++v) {
-        if constexpr (kHeld) {
-            float t[E];
-            weights(v, t);
-#pragma unroll
-            for (int e = 0; e < E; ++e) w[v * E + e] = t[e];
-        }
-#pragma unroll
-        for (int e = 0; e < E; ++e) dw[v * E + e] = 0.0f, db[v * E + e] = 0.0f;
-    }
-    const float width = (float)a.width;
+    // the row reaches chunk c, and (packs of one element) its second half
+    auto has = [&](int c) { return col + (E == 1 ? 2 * c : c) * vs < a.width; };
+    auto has_second = [&](int c) { return E > 1 || col + (2 * c + 1) * vs < a.width; };
     const int64_t step = (int64_t)gridDim.x * groups;
     int64_t row = (int64_t)blockIdx.x * groups + g.id;
     int64_t first = row - (NARROW ? (threadIdx.x & 31) / lanes : 0);
@@ -385,6 +481,15 @@ __global__ void __launch_bounds__(kMaxLanes) k_norm_grad(NormArgs a, int lanes, 
     constexpr int A = kAhead ? S - 1 : 1;  // rows fetched before the loop
 #pragma unroll
     for (int i = 0; i < A; ++i) fetch(i, row + i * step);
+    PA w;
+    w.open(g, a.weight, a.p_dtype, 1.0f, col, vs, a.width, ring + B::kThreadBytes * blockDim.x);
+    if constexpr (PA::kShared) __syncthreads();
+    float2 dw[NC][H], db[NC][H];
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+        for (int h = 0; h < H; ++h) dw[c][h] = db[c][h] = both(0.0f);
+    const float inv_width = 1.0f / (float)a.width;
     float mean_n = row < a.n ? a.mean[row] : 0.0f, rstd_n = row < a.n ? a.rstd[row] : 0.0f;
     int st = 0;
     for (int parity = 0; first < a.n; first += step, row += step, parity ^= 1) {
@@ -402,59 +507,56 @@ __global__ void __launch_bounds__(kMaxLanes) k_norm_grad(NormArgs a, int lanes, 
             mean_n = a.mean[row + step];
             rstd_n = a.rstd[row + step];
         }
-        float sg = 0.0f, sgh = 0.0f;
+        float2 sg2 = both(0.0f), sgh2 = both(0.0f);
         if (row < a.n) {
 #pragma unroll
-            for (int v = 0; v < NV; ++v) {
-                if (col + v * vs >= a.width) continue;
-                const auto px = xs.get(st, v);
-                const auto py = ys.get(st, v);
-                float t[E];
-                if constexpr (!kHeld) weights(v, t);
+            for (int c = 0; c < NC; ++c) {
+                if (!has(c)) continue;
+                float2 x[H], d[H], t[H];
+                xs.get(st, c, has_second(c), x);
+                ys.get(st, c, has_second(c), d);
+                w.get(c, t);
 #pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    const int k = v * E + e;
-                    const float d = to_f32(py.v[e]);
-                    const float h = (to_f32(px.v[e]) - mean) * rstd;
-                    const float gr = d * (kHeld ? w[kHeld ? k : 0] : t[e]);
-                    db[k] += d;
-                    dw[k] = fmaf(d, h, dw[k]);
-                    sg += gr;
-                    sgh = fmaf(gr, h, sgh);
+                for (int h = 0; h < H; ++h) {
+                    float2 n = __fmul2_rn(__fadd2_rn(x[h], both(-mean)), both(rstd));
+                    if (!has_second(c)) n.y = 0.0f;  // dy is 0 there
+                    const float2 gr = __fmul2_rn(d[h], t[h]);
+                    db[c][h] = __fadd2_rn(db[c][h], d[h]);
+                    dw[c][h] = __ffma2_rn(d[h], n, dw[c][h]);
+                    sg2 = __fadd2_rn(sg2, gr);
+                    sgh2 = __ffma2_rn(gr, n, sgh2);
                 }
             }
         }
         if (a.dx) {
-            sg = warp_sum<NARROW>(g, sg);
-            sgh = warp_sum<NARROW>(g, sgh);
+            float sg = warp_sum<NARROW>(g, sg2.x + sg2.y), sgh = warp_sum<NARROW>(g, sgh2.x + sgh2.y);
             if (!NARROW && g.warps > 1) {
                 float2 *slot = ex[g.id].slot[parity];
                 if ((threadIdx.x & 31) == 0) slot[g.warp] = make_float2(sg, sgh);
                 group_barrier(g);
                 const float2 mine = (threadIdx.x & 31) < g.warps ? slot[threadIdx.x & 31] : make_float2(0.0f, 0.0f);
-                sg = warp_sum<NARROW>(g, mine.x);
-                sgh = warp_sum<NARROW>(g, mine.y);
+                sg = group_sum(g, mine.x);
+                sgh = group_sum(g, mine.y);
             }
-            const float mg = sg / width, mgh = sgh / width;
+            // dx = g r - (h (r mean(g h)) + r mean(g))
+            const float2 mg = both(-rstd * (sg * inv_width)), mgh = both(-rstd * (sgh * inv_width));
             if (row < a.n) {
                 TX *dx = static_cast<TX *>(a.dx) + row * a.dx_stride + col;
 #pragma unroll
-                for (int v = 0; v < NV; ++v) {
-                    if (col + v * vs >= a.width) continue;
+                for (int c = 0; c < NC; ++c) {
+                    if (!has(c)) continue;
                     // read and computed again: holding h and g from above would
                     // take 2 registers per element
-                    const auto px = xs.get(st, v);
-                    const auto py = ys.get(st, v);
-                    float t[E];
-                    if constexpr (!kHeld) weights(v, t);
-                    Pack<TX, E> o;
+                    float2 x[H], d[H], t[H], r[H];
+                    xs.get(st, c, has_second(c), x);
+                    ys.get(st, c, has_second(c), d);
+                    w.get(c, t);
 #pragma unroll
-                    for (int e = 0; e < E; ++e) {
-                        const float h = (to_f32(px.v[e]) - mean) * rstd;
-                        const float gr = to_f32(py.v[e]) * (kHeld ? w[kHeld ? v * E + e : 0] : t[e]);
-                        o.v[e] = from_f32<TX>(rstd * (gr - mg - h * mgh));
+                    for (int h = 0; h < H; ++h) {
+                        const float2 n = __fmul2_rn(__fadd2_rn(x[h], both(-mean)), both(rstd));
+                        r[h] = __ffma2_rn(__fmul2_rn(d[h], t[h]), both(rstd), __ffma2_rn(n, mgh, mg));
                     }
-                    store_pack<TX, E>(dx + v * vs, o);
+                    store_chunk<TX, E>(dx, c, vs, has_second(c), r);
                 }
             }
         }
@@ -465,43 +567,45 @@ __global__ void __launch_bounds__(kMaxLanes) k_norm_grad(NormArgs a, int lanes, 
     // the block's column sums: over the groups of a warp, then over the warps (or
     // groups of warps) in a fixed tree, through the ring's memory
     cp_async_wait<0>();
-    float *sh = reinterpret_cast<float *>(ring);
+    float2 *sh = reinterpret_cast<float2 *>(ring);  // (dw, db) of an element
+    auto sums = [&](auto f) {
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+#pragma unroll
+            for (int h = 0; h < H; ++h) {
+                f(2 * (c * H + h), dw[c][h].x, db[c][h].x);
+                f(2 * (c * H + h) + 1, dw[c][h].y, db[c][h].y);
+            }
+    };
     if (NARROW)
         for (int o = lanes; o < 32; o <<= 1)
-#pragma unroll
-            for (int k = 0; k < C; ++k) {
-                dw[k] += __shfl_xor_sync(0xffffffffu, dw[k], o);
-                db[k] += __shfl_xor_sync(0xffffffffu, db[k], o);
-            }
+            sums([&](int, float &p, float &q) {
+                p += __shfl_xor_sync(0xffffffffu, p, o);
+                q += __shfl_xor_sync(0xffffffffu, q, o);
+            });
     const int unit_lanes = NARROW ? 32 : lanes;
     const int unit = threadIdx.x / unit_lanes, lane = threadIdx.x - unit * unit_lanes;
     for (int half = blockDim.x / unit_lanes / 2; half > 0; half >>= 1) {
         __syncthreads();
         const int stride = half * unit_lanes;
         if (unit >= half && unit < 2 * half)
-#pragma unroll
-            for (int k = 0; k < C; ++k) {
-                sh[(2 * k) * stride + (unit - half) * unit_lanes + lane] = dw[k];
-                sh[(2 * k + 1) * stride + (unit - half) * unit_lanes + lane] = db[k];
-            }
+            sums([&](int k, float &p, float &q) { sh[k * stride + (unit - half) * unit_lanes + lane] = make_float2(p, q); });
         __syncthreads();
         if (unit < half)
-#pragma unroll
-            for (int k = 0; k < C; ++k) {
-                dw[k] += sh[(2 * k) * stride + unit * unit_lanes + lane];
-                db[k] += sh[(2 * k + 1) * stride + unit * unit_lanes + lane];
-            }
+            sums([&](int k, float &p, float &q) {
+                const float2 o = sh[k * stride + unit * unit_lanes + lane];
+                p += o.x;
+                q += o.y;
+            });
     }
     if (unit == 0 && lane < lanes) {
-        float *p = part + (int64_t)blockIdx.x * 2 * a.width;
+        float *p = part + (int64_t)blockIdx.x * 2 * a.width + col;
 #pragma unroll
-        for (int v = 0; v < NV; ++v)
-            if (col + v * vs < a.width)
-#pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    p[col + v * vs + e] = dw[v * E + e];
-                    p[a.width + col + v * vs + e] = db[v * E + e];
-                }
+        for (int c = 0; c < NC; ++c)
+            if (has(c)) {
+                store_chunk<float, E>(p, c, vs, has_second(c), dw[c]);
+                store_chunk<float, E>(p + a.width, c, vs, has_second(c), db[c]);
+            }
     }
     let_next_start();
 }
@@ -658,8 +762,9 @@ unsigned grid_for(const NormArgs &a, const Rows &r, int per_sm)
 
 Rows plan_forward(const NormArgs &a) { return plan_rows(a, true, 256); }
 
-// 32 float32 elements per lane would not leave room for two rows in the ring.
-Rows plan_backward(const NormArgs &a) { return plan_rows(a, a.x_dtype != HISS_F32, kMaxLanes); }
+// 32 elements per lane with a float32 operand would not leave room for two
+// rows in the ring.
+Rows plan_backward(const NormArgs &a) { return plan_rows(a, a.y_dtype != HISS_F32, kMaxLanes); }
 
 // Blocks (and parts) of the backward pass: one per SM, so that there are few
 // parts to add up.
@@ -684,7 +789,7 @@ cudaError_t layer_norm(const NormArgs &a, cudaStream_t s, int64_t *launches)
             static Residency cache;
             auto kernel = k_norm<TX, TY, E, NV, NARROW>;
             const int threads = r.lanes * r.groups;
-            const size_t smem = Forward<TX, TY, E, NV, NARROW>::kThreadBytes * threads;
+            const size_t smem = Forward<TX, E, NV>::smem(threads, r.lanes);
             const unsigned grid = grid_for(a, r, resident(kernel, threads, smem, cache));
             kernel<<<grid, threads, smem, s>>>(a, r.lanes, r.groups);
             return cudaGetLastError();
@@ -721,14 +826,13 @@ cudaError_t layer_norm_grad(const NormArgs &a, void *tmp, cudaStream_t s, int64_
                 }
                 return cudaGetLastError();
             }
-            return with_packs<TX, sizeof(TX) == 2>(r, [&](auto e, auto nv, auto narrow) {
+            return with_packs<TX, sizeof(TY) == 2>(r, [&](auto e, auto nv, auto narrow) {
                 constexpr int E = decltype(e)::value, NV = decltype(nv)::value;
                 static Residency cache;
                 auto kernel = k_norm_grad<TX, TY, E, NV, decltype(narrow)::value>;
                 const int threads = r.lanes * r.groups;
                 const bool many = threads > (r.narrow ? 32 : r.lanes);  // sums of several warps or groups to add up
-                const size_t smem = std::max(Backward<TX, TY, E, NV>::kThreadBytes * threads,
-                                             many ? 4 * (size_t)threads * E * NV : 0);
+                const size_t smem = Backward<TX, TY, E, NV>::smem(threads, r.lanes, many);
                 resident(kernel, threads, smem, cache);
                 parts = grad_grid(a, r);
                 kernel<<<parts, threads, smem, s>>>(a, r.lanes, r.groups, part);

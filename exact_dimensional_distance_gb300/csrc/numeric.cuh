@@ -57,6 +57,28 @@ __device__ __forceinline__ void store_pack(T *p, const Pack<T, E> &v)
     *reinterpret_cast<Pack<T, E> *>(p) = v;
 }
 
+// Pairs of elements as float32 pairs, which the f32x2 instructions
+// (__fadd2_rn, __fmul2_rn, __ffma2_rn: two round-to-nearest operations each) take.
+__device__ __forceinline__ float2 pair_of(const float *p) { return make_float2(p[0], p[1]); }
+__device__ __forceinline__ float2 pair_of(const __half *p)
+{
+    return __half22float2(*reinterpret_cast<const __half2 *>(p));
+}
+__device__ __forceinline__ float2 pair_of(const __nv_bfloat16 *p)
+{
+    return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(p));
+}
+__device__ __forceinline__ void set_pair(float *p, float2 v) { p[0] = v.x, p[1] = v.y; }
+__device__ __forceinline__ void set_pair(__half *p, float2 v)
+{
+    *reinterpret_cast<__half2 *>(p) = __floats2half2_rn(v.x, v.y);
+}
+__device__ __forceinline__ void set_pair(__nv_bfloat16 *p, float2 v)
+{
+    *reinterpret_cast<__nv_bfloat162 *>(p) = __floats2bfloat162_rn(v.x, v.y);
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
 // Asynchronous copy of a pack of at least 4 bytes to shared memory.
 template <typename T, int E>
 __device__ __forceinline__ void copy_pack_async(Pack<T, E> *d, const T *p)
