@@ -174,32 +174,57 @@ def _device_tensor(ptr, n, typestr):
     return torch.as_tensor(DeviceArray(ptr, (n,), typestr), device="cuda")
 
 
+_DTYPES = {}  # hiss_dtype of a torch dtype, filled on first use (torch is imported late)
+
+
 def _dtype(t):
     """The hiss_dtype of a torch dtype."""
-    import torch
-    code = {torch.float32: HISS_F32, torch.float16: HISS_F16, torch.bfloat16: HISS_BF16}.get(t)
+    code = _DTYPES.get(t)
     if code is None:
-        raise ValueError("float32, float16 or bfloat16 expected, not %s" % t)
+        import torch
+        _DTYPES.update({torch.float32: HISS_F32, torch.float16: HISS_F16, torch.bfloat16: HISS_BF16})
+        code = _DTYPES.get(t)
+        if code is None:
+            raise ValueError("float32, float16 or bfloat16 expected, not %s" % t)
     return code
 
 
 def _matrix(t, name):
-    """t as rows of unit column stride, a copy only where its strides need one."""
-    if t.dim() < 1:
-        raise ValueError("%s: at least one dimension expected" % name)
-    m = t if t.dim() == 2 else t.reshape(-1, t.shape[-1])
-    if m.shape[1] < 1 or m.shape[1] > HISS_MAX_WIDTH:
-        raise ValueError("%s: width %d is outside 1..%d" % (name, m.shape[1], HISS_MAX_WIDTH))
-    return m if m.stride(1) == 1 else m.contiguous()
+    """t as rows of unit column stride, a copy only where its strides need one:
+    (matrix, rows, width, row stride)."""
+    if t.dim() != 2:
+        if t.dim() < 1:
+            raise ValueError("%s: at least one dimension expected" % name)
+        t = t.reshape(-1, t.shape[-1]) if t.shape[-1] else t.new_empty((0, 0))
+    n, d = t.shape
+    if d < 1 or d > HISS_MAX_WIDTH:
+        raise ValueError("%s: width %d is outside 1..%d" % (name, d, HISS_MAX_WIDTH))
+    row, column = t.stride()
+    if column != 1:
+        t = t.contiguous()
+        row = d
+    return t, n, d, row if n > 1 else d
 
 
-def _stride(m):
-    """Row stride of a matrix (the width where a single row's stride says nothing)."""
-    return m.stride(0) if m.shape[0] > 1 else m.shape[1]
+def _out_matrix(t, name):
+    """As _matrix without a copy (t is written)."""
+    m = t
+    if t.dim() != 2:
+        try:
+            m = t.view(-1, t.shape[-1])
+        except RuntimeError:
+            raise ValueError("%s: rows of unit stride expected" % name) from None
+    n, d = m.shape
+    row, column = m.stride()
+    if column != 1 and d > 1:
+        raise ValueError("%s: rows of unit stride expected" % name)
+    return m, row if n > 1 else d
 
 
-def _ptr(t):
-    return t.data_ptr() if t is not None else None
+def _raw_stream(index):
+    """cudaStream_t of torch's current stream on a device."""
+    import torch
+    return torch.cuda.current_stream(index).cuda_stream
 
 
 class Gradients:
@@ -257,6 +282,12 @@ class Join:
         if not torch.cuda.is_available():
             raise RuntimeError("a CUDA device is required")
         self.stream = stream if stream is not None else torch.cuda.current_stream()
+        self._torch = torch
+        self._device = self.stream.device
+        self._index = self.stream.device_index
+        self._raw = self.stream.cuda_stream
+        # the same value without building a Stream object, where torch has it
+        self._current = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)
         h = _p()
         _check(hiss_create(ctypes.byref(h), _p(self.stream.cuda_stream)), None, "hiss_create")
         self._h = h
@@ -497,123 +528,131 @@ class Join:
     # stream, that stream's earlier work is waited for on the device first and
     # its later work waits for the call.
 
-    def _enqueue(self, call, what, tensors):
-        import torch
+    def _enqueue(self, fn, args, what, tensors):
         for t in tensors:
-            if t is not None and (not t.is_cuda or t.device != self.stream.device):
+            if t is not None and t.get_device() != self._index:
                 raise ValueError("%s: CUDA tensors on the context's device expected" % what)
-        cur = torch.cuda.current_stream(self.stream.device)
-        if cur.cuda_stream == self.stream.cuda_stream:
-            _check(call(), self._h, what)
+        if self._current(self._index) == self._raw:
+            rc = fn(self._h, *args)
+            if rc != HISS_OK:
+                raise HissError(rc, self._h, what)
             return
+        cur = self._torch.cuda.current_stream(self._index)
         self.stream.wait_stream(cur)
-        _check(call(), self._h, what)
+        rc = fn(self._h, *args)
         for t in tensors:  # keep the allocator from reusing them before the context's stream is done
             if t is not None:
                 t.record_stream(self.stream)
         cur.wait_stream(self.stream)
+        _check(rc, self._h, what)
 
-    @staticmethod
-    def _tokens(tokens):
-        import torch
-        if tokens.dtype not in (torch.int32, torch.int64):
-            raise ValueError("int32 or int64 tokens expected, not %s" % tokens.dtype)
-        return tokens.contiguous()
+    def _tokens(self, tokens):
+        """(contiguous tokens, bits)."""
+        if tokens.dtype == self._torch.int64:
+            return tokens.contiguous(), 64
+        if tokens.dtype == self._torch.int32:
+            return tokens.contiguous(), 32
+        raise ValueError("int32 or int64 tokens expected, not %s" % tokens.dtype)
+
+    def _out(self, out, shape, dtype, name="out"):
+        """out, checked, or a new tensor."""
+        if out is None:
+            return self._torch.empty(shape, dtype=dtype, device=self._device)
+        if out.shape != shape or (dtype is not None and out.dtype != dtype):
+            raise ValueError("%s: shape or type differs from the result's" % name)
+        return out
 
     def embed(self, tokens, table, scale=1.0, pad=None, dtype=None, out=None):
         """scale * table[tokens] (hiss_embed): tokens int32 or int64 of any
         shape, table (vocab, width); zeros where tokens == pad.  dtype: the result's
         type (default: the table's); out: a tensor of shape
         (*tokens.shape, width) that receives it."""
-        import torch
-        t, w = self._tokens(tokens), _matrix(table, "table")
+        t, bits = self._tokens(tokens)
         if table.dim() != 2:
             raise ValueError("table: (vocab, width) expected")
-        if out is None:
-            out = torch.empty((*tokens.shape, w.shape[1]), dtype=dtype or table.dtype, device=table.device)
-        elif out.shape != (*tokens.shape, w.shape[1]) or (dtype is not None and out.dtype != dtype):
-            raise ValueError("out: shape or type differs from the result's")
-        o = self._out_matrix(out, "out")
-        self._enqueue(lambda: hiss_embed(
-            self._h, w.data_ptr(), _dtype(w.dtype), w.shape[0], w.shape[1], _stride(w), t.data_ptr(),
-            8 * t.element_size(), t.numel(), HISS_NO_PAD if pad is None else int(pad), float(scale), o.data_ptr(),
-            _dtype(o.dtype), _stride(o)), "hiss_embed", (t, w, o))
+        w, vocab, width, stride = _matrix(table, "table")
+        out = self._out(out, (*tokens.shape, width), dtype if out is not None else dtype or table.dtype)
+        o, o_stride = _out_matrix(out, "out")
+        self._enqueue(hiss_embed, (w.data_ptr(), _dtype(w.dtype), vocab, width, stride, t.data_ptr(), bits, t.numel(),
+                                   HISS_NO_PAD if pad is None else pad, scale, o.data_ptr(), _dtype(o.dtype),
+                                   o_stride), "hiss_embed", (t, w, o))
         return out
 
     def embed_grad(self, tokens, dy, vocab, scale=1.0, pad=None, dtype=None, out=None, accumulate=False):
         """Gradient of ``embed`` with respect to its table (hiss_embed_grad):
         dy (*tokens.shape, width); returns (vocab, width) of the given dtype
         (default: dy's), or out, to which it is added with accumulate."""
-        import torch
-        t, g = self._tokens(tokens), _matrix(dy, "dy")
+        t, bits = self._tokens(tokens)
+        g, _, width, stride = _matrix(dy, "dy")
         if dy.shape[:-1] != tokens.shape:
             raise ValueError("dy: shape (*tokens.shape, width) expected")
-        if out is None:
-            if accumulate:
-                raise ValueError("accumulate needs out")
-            out = torch.empty((int(vocab), g.shape[1]), dtype=dtype or dy.dtype, device=dy.device)
-        elif out.shape != (int(vocab), g.shape[1]) or (dtype is not None and out.dtype != dtype):
-            raise ValueError("out: shape or type differs from the result's")
-        o = self._out_matrix(out, "out")
-        self._enqueue(lambda: hiss_embed_grad(
-            self._h, g.data_ptr(), _dtype(g.dtype), _stride(g), t.data_ptr(), 8 * t.element_size(), t.numel(),
-            HISS_NO_PAD if pad is None else int(pad), float(scale), o.shape[0], g.shape[1], 1 if accumulate else 0,
-            o.data_ptr(), _dtype(o.dtype), _stride(o)), "hiss_embed_grad", (t, g, o))
+        if out is None and accumulate:
+            raise ValueError("accumulate needs out")
+        vocab = int(vocab)
+        out = self._out(out, (max(vocab, 0), width), dtype if out is not None else dtype or dy.dtype)
+        o, o_stride = _out_matrix(out, "out")
+        self._enqueue(hiss_embed_grad, (g.data_ptr(), _dtype(g.dtype), stride, t.data_ptr(), bits, t.numel(),
+                                        HISS_NO_PAD if pad is None else pad, scale, vocab, width,
+                                        1 if accumulate else 0, o.data_ptr(), _dtype(o.dtype), o_stride),
+                      "hiss_embed_grad", (t, g, o))
         return out
 
     def layer_norm(self, x, weight=None, bias=None, eps=1e-5, dtype=None, out=None):
         """Layer norm over the last dimension (hiss_layer_norm): (y, mean,
         rstd), the statistics float32 of shape x.shape[:-1].  dtype: y's type, x's
         (default) or float32."""
-        import torch
-        m = _matrix(x, "x")
-        p = self._params(m.shape[1], weight, bias)
-        if out is None:
-            out = torch.empty(x.shape, dtype=dtype or x.dtype, device=x.device)
-        elif out.shape != x.shape or (dtype is not None and out.dtype != dtype):
-            raise ValueError("out: shape or type differs from the result's")
-        o = self._out_matrix(out, "out")
-        mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
-        rstd = torch.empty_like(mean)
-        self._enqueue(lambda: hiss_layer_norm(
-            self._h, m.data_ptr(), _dtype(m.dtype), _stride(m), m.shape[0], m.shape[1], _ptr(weight), _ptr(bias), p,
-            float(eps), o.data_ptr(), _dtype(o.dtype), _stride(o), mean.data_ptr(), rstd.data_ptr()),
-            "hiss_layer_norm", (m, weight, bias, o, mean, rstd))
+        m, n, width, stride = _matrix(x, "x")
+        p = self._params(width, weight, bias)
+        shape = x.shape
+        out = self._out(out, shape, dtype if out is not None else dtype or x.dtype)
+        o, o_stride = _out_matrix(out, "out")
+        torch = self._torch
+        mean = torch.empty(shape[:-1], dtype=torch.float32, device=self._device)
+        rstd = torch.empty(shape[:-1], dtype=torch.float32, device=self._device)
+        self._enqueue(hiss_layer_norm, (m.data_ptr(), _dtype(m.dtype), stride, n, width,
+                                        None if weight is None else weight.data_ptr(),
+                                        None if bias is None else bias.data_ptr(), p, eps, o.data_ptr(),
+                                        _dtype(o.dtype), o_stride, mean.data_ptr(), rstd.data_ptr()),
+                      "hiss_layer_norm", (m, weight, bias, o, mean, rstd))
         return out, mean, rstd
 
     def layer_norm_grad(self, dy, x, mean, rstd, weight=None, param_dtype=None):
         """Gradient of ``layer_norm`` (hiss_layer_norm_grad): (dx, dweight,
         dbias).  dweight and dbias have the weight's type, or param_dtype
         (default: float32) without a weight."""
-        import torch
-        g, m = _matrix(dy, "dy"), _matrix(x, "x")
-        if dy.shape != x.shape or mean.shape != x.shape[:-1] or rstd.shape != x.shape[:-1]:
+        torch = self._torch
+        m, n, width, stride = _matrix(x, "x")
+        g, _, _, g_stride = _matrix(dy, "dy")
+        shape = x.shape
+        if dy.shape != shape or mean.shape != shape[:-1] or rstd.shape != shape[:-1]:
             raise ValueError("dy, mean and rstd do not match x")
         if mean.dtype != torch.float32 or rstd.dtype != torch.float32:
             raise ValueError("mean and rstd: float32 expected")
-        p = self._params(m.shape[1], weight, None)
+        p = self._params(width, weight, None)
         pt = weight.dtype if weight is not None else param_dtype or torch.float32
         if weight is None:
             p = _dtype(pt)
-        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        dw = torch.empty(m.shape[1], dtype=pt, device=x.device)
-        db = torch.empty_like(dw)
+        dx = torch.empty(shape, dtype=x.dtype, device=self._device)
+        dw = torch.empty(width, dtype=pt, device=self._device)
+        db = torch.empty(width, dtype=pt, device=self._device)
         mean, rstd = mean.contiguous(), rstd.contiguous()
-        self._enqueue(lambda: hiss_layer_norm_grad(
-            self._h, g.data_ptr(), _dtype(g.dtype), _stride(g), m.data_ptr(), _dtype(m.dtype), _stride(m),
-            mean.data_ptr(), rstd.data_ptr(), _ptr(weight), p, m.shape[0], m.shape[1], dx.data_ptr(), m.shape[1],
-            dw.data_ptr(), db.data_ptr()), "hiss_layer_norm_grad", (g, m, mean, rstd, weight, dx, dw, db))
+        self._enqueue(hiss_layer_norm_grad, (g.data_ptr(), _dtype(g.dtype), g_stride, m.data_ptr(), _dtype(m.dtype),
+                                             stride, mean.data_ptr(), rstd.data_ptr(),
+                                             None if weight is None else weight.data_ptr(), p, n, width,
+                                             dx.data_ptr(), width, dw.data_ptr(), db.data_ptr()),
+                      "hiss_layer_norm_grad", (g, m, mean, rstd, weight, dx, dw, db))
         return dx, dw, db
 
     def clip_grads(self, grads, max_norm):
         """Clip by the global norm (hiss_clip_grads): grads is a ``Gradients``
         or a sequence of tensors, clipped in place.  Returns the norm before
         clipping (float32 CUDA scalar)."""
-        import torch
         g = grads if isinstance(grads, Gradients) else Gradients(grads)
-        norm = torch.empty((), dtype=torch.float32, device=self.stream.device)
-        self._enqueue(lambda: hiss_clip_grads(self._h, g.array, len(g), float(max_norm), norm.data_ptr()),
-                      "hiss_clip_grads", (norm, *g.grads[:1]) if self._on_stream() else (norm, *g.grads, *g.out))
+        norm = self._torch.empty((), dtype=self._torch.float32, device=self._device)
+        # one device for all (checked by Gradients); all are recorded on another stream
+        same = self._current(self._index) == self._raw
+        self._enqueue(hiss_clip_grads, (g.array, len(g.grads), max_norm, norm.data_ptr()), "hiss_clip_grads",
+                      (norm, *g.grads[:1]) if same else (norm, *g.grads, *g.out))
         return norm
 
     def finish(self):
@@ -621,28 +660,16 @@ class Join:
         the last call was neither padding nor in the table."""
         _check(hiss_finish(self._h), self._h, "hiss_finish")
 
-    def _on_stream(self):
-        import torch
-        return torch.cuda.current_stream(self.stream.device).cuda_stream == self.stream.cuda_stream
-
     @staticmethod
     def _params(width, weight, bias):
         """The hiss_dtype of weight and bias."""
-        kinds = {t.dtype for t in (weight, bias) if t is not None}
-        if len(kinds) > 1:
-            raise ValueError("weight and bias of one type expected")
+        kind = None
         for t in (weight, bias):
-            if t is not None and (t.shape != (width,) or (width > 1 and t.stride(0) != 1)):
+            if t is None:
+                continue
+            if t.dim() != 1 or t.shape[0] != width or (width > 1 and t.stride(0) != 1):
                 raise ValueError("weight and bias: contiguous vectors of %d entries expected" % width)
-        return _dtype(kinds.pop()) if kinds else HISS_F32
-
-    @staticmethod
-    def _out_matrix(t, name):
-        """t as rows without a copy (it is written)."""
-        try:
-            m = t if t.dim() == 2 else t.view(-1, t.shape[-1])
-        except RuntimeError:
-            m = None
-        if m is None or (m.shape[1] > 1 and m.stride(1) != 1):
-            raise ValueError("%s: rows of unit stride expected" % name)
-        return m
+            if kind is not None and t.dtype != kind:
+                raise ValueError("weight and bias of one type expected")
+            kind = t.dtype
+        return HISS_F32 if kind is None else _dtype(kind)

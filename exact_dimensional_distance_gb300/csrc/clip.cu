@@ -4,9 +4,9 @@
 //
 // Two launches whatever the number of tensors (up to kMaxTensors; further
 // tensors go to further launches): k_sum_squares leaves one float64 partial sum per
-// block, and every block of k_clip adds all of them up in the same order (a few
-// KB from L2, cheaper than a launch for it), so every block has the same
-// factor.  The list of tensors travels in the kernels' parameters: no copy to
+// block, its last block to finish adds them up in the blocks' order and
+// leaves the factor, and k_clip scales.  float64 runs at a sixty-fourth of
+// float32's rate, so it is kept to one thread or one block at a time.  The list of tensors travels in the kernels' parameters: no copy to
 // the device, nothing to keep alive after the call, and a captured graph holds its own.
 //
 // The work is cut into chunks of one tensor each, dealt out to the blocks in
@@ -24,7 +24,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kBlocksPerSM = 4;
+constexpr int kBlocksPerSM = 5;
 constexpr int kMaxBlocks = kSMs * kBlocksPerSM;
 constexpr int kUnroll = 4;         // accesses in flight per thread
 constexpr int kMaxTensors = 1000;  // 29 KB of parameters per launch (the limit is 32,764 bytes)
@@ -41,58 +41,73 @@ struct TensorList {
     int32_t chunk;           // elements per chunk, a multiple of 2048
 };
 
-// Sum of the squares of a pack in float32.  A result that is not well inside
-// float32's range (some square overflowed or lost bits to underflow) is
-// computed again in float64 and added to *wide; 0 is returned for it.
-// A pack whose sum is at least 2^-80 loses at most 8 * 2^-126 to underflow.
-template <typename T, int E>
-__device__ __forceinline__ float pack_squares(const Pack<T, E> &p, double *wide)
+// Adds the squares of U packs to *narrow in float32.  A pack whose sum is not
+// well inside float32's range (some square overflowed or lost bits to
+// underflow) is computed again in float64 and added to *wide instead.  A pack
+// whose sum is at least 2^-80 loses at most 8 * 2^-126 to underflow.  One branch
+// for all U packs: with one per pack the compiler waits for each load in turn.
+template <typename T, int E, int U>
+__device__ __forceinline__ void add_squares(const Pack<T, E> (&p)[U], float *narrow, double *wide)
 {
-    float s = 0.0f;
+    float s[U];
+    bool odd = false;
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-        const float v = to_f32(p.v[e]);
-        s = fmaf(v, v, s);
-    }
-    if (!(s >= 0x1p-80f && s <= 0x1p100f)) {
-        double w = 0.0;
-        for (int e = 0; e < E; ++e) {
-            const double v = to_f32(p.v[e]);
-            w += v * v;
+    for (int u = 0; u < U; ++u) {
+        if constexpr (E == 1) {
+            const float v = to_f32(p[u].v[0]);
+            s[u] = v * v;
+        } else {
+            float2 q = both(0.0f);
+#pragma unroll
+            for (int e = 0; e < E; e += 2) {
+                const float2 v = pair_of(p[u].v + e);
+                q = __ffma2_rn(v, v, q);
+            }
+            s[u] = q.x + q.y;
         }
-        *wide += w;
-        s = 0.0f;
+        odd = odd || !(s[u] >= 0x1p-80f && s[u] <= 0x1p100f);
     }
-    return s;
+    if (odd) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (s[u] >= 0x1p-80f && s[u] <= 0x1p100f) continue;
+            s[u] = 0.0f;
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const double v = to_f32(p[u].v[e]);
+                *wide += v * v;
+            }
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) *narrow += s[u];
 }
 
-// Sum of squares of x[0 .. n) over the block; each thread returns its share.
-// A float32 sum covers kUnroll packs; above that the sums are float64.
+// Adds this thread's share of the sum of squares of x[0 .. n).
 template <typename T>
-__device__ double chunk_squares(const T *x, int64_t n)
+__device__ void chunk_squares(const T *x, int64_t n, float &narrow, double &wide)
 {
     constexpr int E = 16 / sizeof(T);
-    double wide = 0.0;
-    float narrow = 0.0f;
     const int head = (int)min((int64_t)((16 - (reinterpret_cast<uintptr_t>(x) & 15)) & 15) / (int)sizeof(T), n);
-    if ((int)threadIdx.x < head) narrow += pack_squares<T, 1>(load_pack<T, 1>(x + threadIdx.x), &wide);
     const T *v = x + head;
     const int packs = (int)((n - head) / E);
+    // the few elements before the first and behind the last pack
+    const int tail = (int)(n - head) - packs * E, t = (int)threadIdx.x;
+    if (t < head + tail) {
+        const Pack<T, 1> p[1] = {load_pack<T, 1>(t < head ? x + t : v + (int64_t)packs * E + (t - head))};
+        add_squares<T, 1, 1>(p, &narrow, &wide);
+    }
     int i = threadIdx.x;
     for (; i + (kUnroll - 1) * kThreads < packs; i += kUnroll * kThreads) {
         Pack<T, E> p[kUnroll];
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) p[u] = load_pack<T, E>(v + (int64_t)(i + u * kThreads) * E);
-        float s = 0.0f;
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) s += pack_squares<T, E>(p[u], &wide);
-        wide += (double)s;
+        add_squares<T, E, kUnroll>(p, &narrow, &wide);
     }
-    for (; i < packs; i += kThreads) narrow += pack_squares<T, E>(load_pack<T, E>(v + (int64_t)i * E), &wide);
-    const int tail = (int)(n - head) - packs * E;
-    if ((int)threadIdx.x < tail)
-        narrow += pack_squares<T, 1>(load_pack<T, 1>(v + (int64_t)packs * E + threadIdx.x), &wide);
-    return wide + (double)narrow;
+    for (; i < packs; i += kThreads) {
+        const Pack<T, E> p[1] = {load_pack<T, E>(v + (int64_t)i * E)};
+        add_squares<T, E, 1>(p, &narrow, &wide);
+    }
 }
 
 // The tensor that holds a chunk.
@@ -108,33 +123,76 @@ __device__ __forceinline__ int tensor_of(const TensorList<CAP> &l, int chunk)
     return lo;
 }
 
-// Sum of v over the block, the same bits in every thread.
+// The sums over the lists so far, and what k_clip reads.
+struct ClipState {
+    unsigned done;   // blocks of the last list's kernel that have finished (0 between calls)
+    float factor;
+};
+
+// Sum over the block of a float64 per thread, in thread 0.
 __device__ __forceinline__ double block_sum(double v)
 {
-    __shared__ double part[kWarps];
+    __shared__ double warp_part[kWarps];
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
     __syncthreads();
-    double s = 0.0;
-    for (int w = 0; w < kWarps; ++w) s += part[w];
-    return s;
+    if ((threadIdx.x & 31) == 0) warp_part[threadIdx.x >> 5] = v;
+    __syncthreads();
+    if (threadIdx.x == 0)
+        for (int w = 1; w < kWarps; ++w) v += warp_part[w];
+    return v;
 }
 
+// part: where this list's blocks leave their sums; all, parts: the sums of
+// every list; last: this is the last list.
 template <int CAP>
-__global__ void __launch_bounds__(kThreads) k_sum_squares(const __grid_constant__ TensorList<CAP> l, double *part)
+__global__ void __launch_bounds__(kThreads, kBlocksPerSM)
+    k_sum_squares(const __grid_constant__ TensorList<CAP> l, double *part, const double *all, int parts, bool last,
+                  float max_norm, float *norm, ClipState *state)
 {
+    __shared__ double warp_part[kWarps];
+    __shared__ bool finish;
     wait_for_previous();
-    double s = 0.0;
+    // float32 over the thread's share of one chunk (at most 128 elements of
+    // the usual chunk sizes) and then over a warp, float64 above that
+    float narrow = 0.0f;
+    double wide = 0.0;
     const int chunks = l.first[l.count];
     for (int c = blockIdx.x; c < chunks; c += gridDim.x) {
+        if (c != (int)blockIdx.x) {
+            wide += (double)narrow;
+            narrow = 0.0f;
+        }
         const int t = tensor_of(l, c);
         const int64_t at = (int64_t)(c - l.first[t]) * l.chunk, n = min((int64_t)l.chunk, l.n[t] - at);
-        if (l.dtype[t] == HISS_F32) s += chunk_squares(static_cast<const float *>(l.in[t]) + at, n);
-        else if (l.dtype[t] == HISS_F16) s += chunk_squares(static_cast<const __half *>(l.in[t]) + at, n);
-        else s += chunk_squares(static_cast<const __nv_bfloat16 *>(l.in[t]) + at, n);
+        if (l.dtype[t] == HISS_F32) chunk_squares(static_cast<const float *>(l.in[t]) + at, n, narrow, wide);
+        else if (l.dtype[t] == HISS_F16) chunk_squares(static_cast<const __half *>(l.in[t]) + at, n, narrow, wide);
+        else chunk_squares(static_cast<const __nv_bfloat16 *>(l.in[t]) + at, n, narrow, wide);
     }
-    s = block_sum(s);
-    if (threadIdx.x == 0) part[blockIdx.x] = s;
+    for (int o = 16; o > 0; o >>= 1) narrow += __shfl_xor_sync(0xffffffffu, narrow, o);
+    if (__any_sync(0xffffffffu, __double_as_longlong(wide) != 0))
+        for (int o = 16; o > 0; o >>= 1) wide += __shfl_xor_sync(0xffffffffu, wide, o);
+    if ((threadIdx.x & 31) == 0) warp_part[threadIdx.x >> 5] = wide + (double)narrow;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        double s = warp_part[0];
+        for (int w = 1; w < kWarps; ++w) s += warp_part[w];
+        part[blockIdx.x] = s;
+        __threadfence();
+        finish = last && atomicAdd(&state->done, 1u) == gridDim.x - 1;
+    }
+    __syncthreads();
+    if (finish) {
+        __threadfence();
+        double s = 0.0;
+        for (int i = threadIdx.x; i < parts; i += kThreads) s += *(volatile const double *)(all + i);
+        s = block_sum(s);
+        if (threadIdx.x == 0) {
+            const double total = sqrt(s);
+            *norm = (float)total;
+            state->factor = isfinite(total) && total > (double)max_norm ? (float)((double)max_norm / total) : 1.0f;
+            state->done = 0;
+        }
+    }
     let_next_start();
 }
 
@@ -176,15 +234,11 @@ __device__ void chunk_scale(const T *x, T *y, int64_t n, float f)
 }
 
 template <int CAP>
-__global__ void __launch_bounds__(kThreads) k_clip(const __grid_constant__ TensorList<CAP> l, const double *part, int parts,
-                                                   float max_norm, float *norm)
+__global__ void __launch_bounds__(kThreads, kBlocksPerSM)
+    k_clip(const __grid_constant__ TensorList<CAP> l, const ClipState *state)
 {
     wait_for_previous();
-    double s = 0.0;
-    for (int i = threadIdx.x; i < parts; i += kThreads) s += part[i];
-    const double total = sqrt(block_sum(s));
-    const float f = isfinite(total) && total > (double)max_norm ? (float)((double)max_norm / total) : 1.0f;
-    if (blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)total;
+    const float f = state->factor;
     const int chunks = l.first[l.count];
     for (int i = blockIdx.x; i < chunks; i += gridDim.x) {
         const int c = chunks - 1 - i;
@@ -248,8 +302,8 @@ Plan plan(const hiss_tensor *t, int64_t count)
 }
 
 template <int CAP>
-cudaError_t run(const hiss_tensor *t, int64_t count, const Plan &p, float max_norm, float *norm, double *part,
-                cudaStream_t s, int64_t *launches)
+cudaError_t run(const hiss_tensor *t, int64_t count, const Plan &p, float max_norm, float *norm, ClipState *state,
+                double *part, cudaStream_t s, int64_t *launches)
 {
     TensorList<CAP> l;
     int parts = 0;
@@ -257,7 +311,8 @@ cudaError_t run(const hiss_tensor *t, int64_t count, const Plan &p, float max_no
     do {
         fill(l, t, count, &i, p.chunk);
         const int blocks = std::max(1, std::min(kMaxBlocks, l.first[l.count]));
-        HISS_TRY(launch_after(k_sum_squares<CAP>, blocks, kThreads, 0, s, l, part + parts));
+        HISS_TRY(launch_after(k_sum_squares<CAP>, blocks, kThreads, 0, s, l, part + parts, part, parts + blocks, i >= count,
+                              max_norm, norm, state));
         parts += blocks;
         ++*launches;
     } while (i < count);
@@ -266,7 +321,7 @@ cudaError_t run(const hiss_tensor *t, int64_t count, const Plan &p, float max_no
         if (p.lists > 1) fill(l, t, count, &i, p.chunk);
         else i = count;
         const int blocks = std::max(1, std::min(kMaxBlocks, l.first[l.count]));
-        HISS_TRY(launch_after(k_clip<CAP>, blocks, kThreads, 0, s, l, part, parts, max_norm, norm));
+        HISS_TRY(launch_after(k_clip<CAP>, blocks, kThreads, 0, s, l, state));
         ++*launches;
     } while (i < count);
     return cudaSuccess;
@@ -274,18 +329,21 @@ cudaError_t run(const hiss_tensor *t, int64_t count, const Plan &p, float max_no
 
 }  // namespace
 
+size_t clip_state_bytes() { return sizeof(ClipState); }
+
 size_t clip_tmp_bytes(const hiss_tensor *t, int64_t count)
 {
     return 8 * (size_t)kMaxBlocks * (size_t)std::max<int64_t>(1, plan(t, count).lists);
 }
 
-cudaError_t clip_grads(const hiss_tensor *t, int64_t count, float max_norm, float *norm, void *tmp, cudaStream_t s,
-                       int64_t *launches)
+cudaError_t clip_grads(const hiss_tensor *t, int64_t count, float max_norm, float *norm, void *state, void *tmp,
+                       cudaStream_t s, int64_t *launches)
 {
     const Plan p = plan(t, count);
     double *part = static_cast<double *>(tmp);
-    if (p.used <= kFewTensors) return run<kFewTensors>(t, count, p, max_norm, norm, part, s, launches);
-    return run<kMaxTensors>(t, count, p, max_norm, norm, part, s, launches);
+    ClipState *c = static_cast<ClipState *>(state);
+    if (p.used <= kFewTensors) return run<kFewTensors>(t, count, p, max_norm, norm, c, part, s, launches);
+    return run<kMaxTensors>(t, count, p, max_norm, norm, c, part, s, launches);
 }
 
 }  // namespace hiss

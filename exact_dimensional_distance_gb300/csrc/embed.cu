@@ -29,20 +29,17 @@ namespace hiss {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kCols = 8;  // columns per lane
+constexpr int kCols = 16;  // columns per lane of the sums
 
-// The table row of position i, or -1 for a row of zeros (padding, or a token
-// outside the table, which sets *bad).
-__device__ __forceinline__ int64_t row_of(const EmbedArgs &a, int64_t i, int *bad)
+// The table row of position i; kPadRow for padding and kBadRow for a token
+// outside the table, both rows of zeros.  The caller raises *a.bad once it has
+// issued its loads (a store between them would make each wait for the last).
+constexpr int64_t kPadRow = -1, kBadRow = -2;
+__device__ __forceinline__ int64_t row_of(const EmbedArgs &a, int64_t i)
 {
     const int64_t t =
         a.token_bits == 64 ? static_cast<const int64_t *>(a.tokens)[i] : static_cast<const int32_t *>(a.tokens)[i];
-    if (t == a.pad) return -1;
-    if (t < 0 || t >= a.vocab) {
-        if (bad) *bad = 1;
-        return -1;
-    }
-    return t;
+    return t == a.pad ? kPadRow : t < 0 || t >= a.vocab ? kBadRow : t;
 }
 
 // ---- forward --------------------------------------------------------------------
@@ -58,7 +55,7 @@ __global__ void __launch_bounds__(kThreads) k_embed(EmbedArgs a, int lanes, int 
     for (int64_t it = (int64_t)blockIdx.x * per_block + threadIdx.x / lanes; it < items; it += step) {
         const int64_t i = tiles == 1 ? it : it / tiles;
         const int c0 = ((int)(it - i * tiles) * lanes * NV + lane) * E;
-        const int64_t r = row_of(a, i, a.bad);
+        const int64_t r = row_of(a, i);
         const TI *p = static_cast<const TI *>(a.rows) + r * a.rows_stride;
         TO *q = static_cast<TO *>(a.out) + i * a.out_stride;
         Pack<TI, E> v[NV];
@@ -76,6 +73,7 @@ __global__ void __launch_bounds__(kThreads) k_embed(EmbedArgs a, int lanes, int 
             for (int e = 0; e < E; ++e) o.v[e] = from_f32<TO>(r >= 0 ? a.scale * to_f32(v[k].v[e]) : 0.0f);
             store_pack<TO, E>(q + c, o);
         }
+        if (r == kBadRow) *a.bad = 1;
     }
 }
 
@@ -83,82 +81,94 @@ __global__ void __launch_bounds__(kThreads) k_embed(EmbedArgs a, int lanes, int 
 
 constexpr int kSortThreads = 512;
 constexpr int kSortWarps = kSortThreads / 32;
-constexpr int kSortItems = 8;
-constexpr int kSortTile = kSortThreads * kSortItems;
+constexpr int kMaxItems = 8;  // positions per thread
 constexpr int kMaxBits = 9;  // one bin per thread
 constexpr int kMaxBins = 1 << kMaxBits;
 // Up to this many tiles each block of the scatter adds up the tiles' counts
-// itself; above, their prefix sums are a kernel of their own.
-constexpr int kSumTiles = 64;
+// itself; above, their prefix sums are a kernel of their own.  Tiles are as small
+// as this allows, down to one position per thread: the sort is a chain
+// of latencies, and few large tiles leave it on few SMs (65,536 positions in
+// 16 tiles: 11 us for the first count).
+constexpr int kSumTiles = 128;
 constexpr int kFillBlocks = 2 * kSMs;
 
 struct SortArgs {
-    const uint32_t *keys_in, *vals_in;  // NULL: the tokens and their positions
-    uint32_t *keys_out, *vals_out;
+    const uint2 *in;     // (key, position); NULL: the tokens and their positions
+    uint2 *out;
     uint32_t *counts;    // [tiles][bins], exclusive over tiles once scanned; then [bins] totals
     uint8_t *present;    // [vocab] token occurs (NULL: not wanted)
     uint32_t *runs;      // set to 0 by the first kernel: number of long runs (SumArgs)
     int tiles, shift, bits, scanned;
     int fill, fills;     // this kernel writes part fill of fills of the empty rows (fills = 0: none)
+    int store;           // bytes per store that the gradient's rows allow
 };
 
-__device__ __forceinline__ uint32_t key_at(const EmbedArgs &a, const SortArgs &s, int64_t i, int *bad)
+// Entry i: the token (vocab for a position without a row) and its position.
+__device__ __forceinline__ uint2 entry(const EmbedArgs &a, const SortArgs &s, int64_t i, bool *bad)
 {
-    if (s.keys_in) return s.keys_in[i];
-    const int64_t r = row_of(a, i, bad);
-    return (uint32_t)(r < 0 ? a.vocab : r);
+    if (s.in) return s.in[i];
+    const int64_t r = row_of(a, i);
+    *bad = *bad || r == kBadRow;
+    return make_uint2((uint32_t)(r < 0 ? a.vocab : r), (uint32_t)i);
 }
 
-// Zeros for the rows of this kernel's part of the vocabulary that no position
-// holds, by the blocks past the sort's.
-template <typename TO, int E>
+template <typename T>
+__device__ __forceinline__ void zero_row(char *p, int64_t bytes, int lane)
+{
+    for (int64_t i = lane * sizeof(T); i < bytes; i += 32 * sizeof(T)) *reinterpret_cast<T *>(p + i) = T{};
+}
+
+// Zeros (all bits 0 in every type) for the rows of this kernel's part of the
+// vocabulary that no position holds, by the blocks past the sort's.
 __device__ void fill_empty(const EmbedArgs &a, const SortArgs &s)
 {
     const int lane = threadIdx.x & 31;
     const int64_t v0 = a.vocab * s.fill / s.fills, v1 = a.vocab * (s.fill + 1) / s.fills;
     const int64_t warp = (int64_t)(blockIdx.x - s.tiles) * kSortWarps + (threadIdx.x >> 5);
     const int64_t warps = (int64_t)(gridDim.x - s.tiles) * kSortWarps;
-    Pack<TO, E> zero;
-#pragma unroll
-    for (int e = 0; e < E; ++e) zero.v[e] = from_f32<TO>(0.0f);
+    const int size = a.out_dtype == HISS_F32 ? 4 : 2;
+    const int64_t bytes = (int64_t)a.width * size, stride = a.out_stride * size;
     const int rows = (int)min((int64_t)32, (v1 - v0 + warps - 1) / warps);  // per warp and turn
     for (int64_t v = v0 + warp * rows; v < v1; v += warps * rows) {
         unsigned empty = __ballot_sync(0xffffffffu, lane < rows && v + lane < v1 && !s.present[min(v + lane, v1 - 1)]);
         while (empty) {
-            const int b = __ffs(empty) - 1;
+            char *p = static_cast<char *>(a.out) + (v + __ffs(empty) - 1) * stride;
             empty &= empty - 1;
-            TO *p = static_cast<TO *>(a.out) + (v + b) * a.out_stride;
-            for (int c = lane * E; c < a.width; c += 32 * E) store_pack<TO, E>(p + c, zero);
+            if (s.store == 16) zero_row<uint4>(p, bytes, lane);
+            else if (s.store == 4) zero_row<uint32_t>(p, bytes, lane);
+            else zero_row<uint16_t>(p, bytes, lane);
         }
     }
 }
 
 // Digit counts of each tile (and, in the first pass, which tokens occur).
-template <typename TO, int E>
+template <int ITEMS>
 __global__ void __launch_bounds__(kSortThreads) k_sort_count(EmbedArgs a, SortArgs s)
 {
     __shared__ uint32_t hist[kMaxBins];
     let_next_start();
     wait_for_previous();
     if ((int)blockIdx.x >= s.tiles) {
-        fill_empty<TO, E>(a, s);
+        fill_empty(a, s);
         return;
     }
     hist[threadIdx.x] = 0;
-    if (!s.keys_in && blockIdx.x == 0 && threadIdx.x == 0) *s.runs = 0;
+    if (!s.in && blockIdx.x == 0 && threadIdx.x == 0) *s.runs = 0;
     __syncthreads();
     const uint32_t mask = (1u << s.bits) - 1u;
-    const int64_t base = (int64_t)blockIdx.x * kSortTile;
-    uint32_t key[kSortItems];
+    const int64_t base = (int64_t)blockIdx.x * (kSortThreads * ITEMS);
+    uint32_t key[ITEMS];
+    bool bad = false;
 #pragma unroll
-    for (int k = 0; k < kSortItems; ++k) {
+    for (int k = 0; k < ITEMS; ++k) {
         const int64_t i = base + k * kSortThreads + threadIdx.x;
-        key[k] = i < a.n ? key_at(a, s, i, a.bad) : ~0u;
+        key[k] = i < a.n ? entry(a, s, i, &bad).x : ~0u;
     }
+    if (bad) *a.bad = 1;
 #pragma unroll
-    for (int k = 0; k < kSortItems; ++k) {
+    for (int k = 0; k < ITEMS; ++k) {
         if (base + k * kSortThreads + threadIdx.x >= a.n) continue;
-        if (s.present && !s.keys_in && key[k] < (uint32_t)a.vocab) s.present[key[k]] = 1;
+        if (s.present && !s.in && key[k] < (uint32_t)a.vocab) s.present[key[k]] = 1;
         atomicAdd(&hist[(key[k] >> s.shift) & mask], 1u);
     }
     __syncthreads();
@@ -194,7 +204,7 @@ __global__ void __launch_bounds__(1024) k_sort_scan(SortArgs s)
 
 // One stable pass: each tile's positions go behind those of the tiles before
 // it, digit by digit.
-template <typename TO, int E>
+template <int ITEMS>
 __global__ void __launch_bounds__(kSortThreads) k_sort_scatter(EmbedArgs a, SortArgs s)
 {
     __shared__ uint32_t whist[kSortWarps][kMaxBins];
@@ -203,7 +213,7 @@ __global__ void __launch_bounds__(kSortThreads) k_sort_scatter(EmbedArgs a, Sort
     let_next_start();
     wait_for_previous();
     if ((int)blockIdx.x >= s.tiles) {
-        fill_empty<TO, E>(a, s);
+        fill_empty(a, s);
         return;
     }
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -211,16 +221,13 @@ __global__ void __launch_bounds__(kSortThreads) k_sort_scatter(EmbedArgs a, Sort
     const uint32_t mask = (uint32_t)bins - 1u;
     for (int i = threadIdx.x; i < kSortWarps * kMaxBins; i += kSortThreads) (&whist[0][0])[i] = 0;
     // warp-contiguous items, in order
-    const int64_t base = (int64_t)blockIdx.x * kSortTile + warp * (32 * kSortItems);
-    uint32_t key[kSortItems], val[kSortItems], rank[kSortItems];
+    const int64_t base = (int64_t)blockIdx.x * (kSortThreads * ITEMS) + warp * (32 * ITEMS);
+    uint2 item[ITEMS];
+    uint32_t rank[ITEMS];
+    bool bad = false;
 #pragma unroll
-    for (int k = 0; k < kSortItems; ++k) {
-        const int64_t i = base + k * 32 + lane;
-        if (i < a.n) {
-            key[k] = key_at(a, s, i, nullptr);
-            val[k] = s.vals_in ? s.vals_in[i] : (uint32_t)i;
-        }
-    }
+    for (int k = 0; k < ITEMS; ++k)
+        if (base + k * 32 + lane < a.n) item[k] = entry(a, s, base + k * 32 + lane, &bad);
     // this thread's bin: positions in the tiles before this one, and in all
     uint32_t before = 0, total = 0;
     if (bin < bins) {
@@ -228,7 +235,7 @@ __global__ void __launch_bounds__(kSortThreads) k_sort_scatter(EmbedArgs a, Sort
             before = s.counts[(int64_t)blockIdx.x * bins + bin];
             total = s.counts[(int64_t)s.tiles * bins + bin];
         } else {
-#pragma unroll 8
+#pragma unroll 32
             for (int t = 0; t < s.tiles; ++t) {
                 const uint32_t c = s.counts[(int64_t)t * bins + bin];
                 total += c;
@@ -250,9 +257,9 @@ __global__ void __launch_bounds__(kSortThreads) k_sort_scatter(EmbedArgs a, Sort
     // lanes with the same digit, one ballot per bit (a match instruction takes
     // as long as the warp has distinct digits)
 #pragma unroll
-    for (int k = 0; k < kSortItems; ++k) {
+    for (int k = 0; k < ITEMS; ++k) {
         const bool valid = base + k * 32 + lane < a.n;
-        const uint32_t d = valid ? (key[k] >> s.shift) & mask : 0u;
+        const uint32_t d = valid ? (item[k].x >> s.shift) & mask : 0u;
         uint32_t peers = __ballot_sync(0xffffffffu, valid);
 #pragma unroll
         for (int b = 0; b < kMaxBits; ++b) {
@@ -276,12 +283,8 @@ __global__ void __launch_bounds__(kSortThreads) k_sort_scatter(EmbedArgs a, Sort
     }
     __syncthreads();
 #pragma unroll
-    for (int k = 0; k < kSortItems; ++k)
-        if (base + k * 32 + lane < a.n) {
-            const uint32_t at = whist[warp][(key[k] >> s.shift) & mask] + rank[k];
-            s.keys_out[at] = key[k];
-            s.vals_out[at] = val[k];
-        }
+    for (int k = 0; k < ITEMS; ++k)
+        if (base + k * 32 + lane < a.n) s.out[whist[warp][(item[k].x >> s.shift) & mask] + rank[k]] = item[k];
 }
 
 // ---- the sums ---------------------------------------------------------------------
@@ -289,7 +292,7 @@ __global__ void __launch_bounds__(kSortThreads) k_sort_scatter(EmbedArgs a, Sort
 constexpr int kUnit = 32;  // sorted positions per unit
 
 struct SumArgs {
-    const uint32_t *keys, *vals;  // sorted tokens and their positions
+    const uint2 *items;           // sorted (token, position)
     float *part;                  // [units][2][width]: sum of the long run that comes in from the unit
                                   // before, and of the long run that begins here
     uint32_t *runs;               // [0]: number of long runs; then (key, first unit) of each
@@ -333,7 +336,7 @@ __device__ __forceinline__ void write_part(const EmbedArgs &a, float *p, int c0,
     }
 }
 
-constexpr int kAhead = 8;  // rows in flight per lane
+constexpr int kAhead = 4;  // rows in flight per lane
 
 template <typename TI, int E>
 constexpr size_t sum_bytes() { return (size_t)kThreads * kAhead * kCols * sizeof(TI); }
@@ -354,9 +357,9 @@ __global__ void __launch_bounds__(kThreads) k_sum(EmbedArgs a, SumArgs s)
     const int64_t unit = item / s.tiles;
     const int tile = (int)(item - unit * s.tiles);
     const int c0 = (tile * s.lanes * NV + lane) * E;
-    const int64_t i0 = unit * kUnit, i1 = min(i0 + kUnit, a.n);
+    const int n = (int)a.n, i0 = (int)unit * kUnit, i1 = min(i0 + kUnit, n);
     const uint32_t vocab = (uint32_t)a.vocab, none = ~0u;
-    auto key_of = [&](int64_t i) { return i >= 0 && i < a.n ? s.keys[i] : none; };
+    auto key_of = [&](int i) { return i >= 0 && i < n ? s.items[i].x : none; };
     const uint32_t k0 = key_of(i0), k1 = key_of(i1 - 1);
     const uint32_t prev = key_of(i0 - 1), prev_unit = key_of(i0 - kUnit), prev_unit2 = key_of(i0 - kUnit - 1);
     const uint32_t next = key_of(i1), next_unit = key_of(i1 + kUnit);
@@ -369,12 +372,12 @@ __global__ void __launch_bounds__(kThreads) k_sum(EmbedArgs a, SumArgs s)
     const bool goes_out = next == k1 && k1 < vocab;
     const bool begins = goes_out && !(k0 == k1 && comes_in);
     const bool long_out = goes_out && (!begins || next_unit == k1);
-    int64_t i = i0, end = i1;
+    int i = i0, end = i1;
     if (comes_in && !long_in)
-        while (i < i1 && s.keys[i] == k0) ++i;
+        while (i < i1 && s.items[i].x == k0) ++i;
     if (goes_out && !long_out)
-        while (end < a.n && s.keys[end] == k1) ++end;
-    while (end > i && s.keys[end - 1] >= vocab) --end;
+        while (end < n && s.items[end].x == k1) ++end;
+    while (end > i && s.items[end - 1].x >= vocab) --end;
     if (long_out && begins && tile == 0 && lane == 0) {
         const uint32_t at = atomicAdd(s.runs, 1u);
         s.runs[1 + 2 * at] = k1;
@@ -384,9 +387,9 @@ __global__ void __launch_bounds__(kThreads) k_sum(EmbedArgs a, SumArgs s)
     if (i >= end) return;
 
     P *slot = reinterpret_cast<P *>(ring) + threadIdx.x;
-    auto fetch = [&](int64_t j) {
+    auto fetch = [&](int j) {
         if (j < end) {
-            const TI *p = static_cast<const TI *>(a.rows) + (int64_t)s.vals[j] * a.rows_stride + c0;
+            const TI *p = static_cast<const TI *>(a.rows) + (int64_t)s.items[j].y * a.rows_stride + c0;
 #pragma unroll
             for (int q = 0; q < NV; ++q) {
                 if (c0 + q * s.lanes * E >= a.width) continue;
@@ -403,18 +406,26 @@ __global__ void __launch_bounds__(kThreads) k_sum(EmbedArgs a, SumArgs s)
     for (int c = 0; c < kCols; ++c) acc[c] = 0.0f;
     float *part = s.part + unit * 2 * a.width;
     bool head = long_in;  // the current run is the long one that came in
-    uint32_t key = s.keys[i];
+    uint32_t key = s.items[i].x;
     while (i < end) {
         fetch(i + kAhead - 1);
         cp_async_wait<kAhead - 1>();
 #pragma unroll
         for (int q = 0; q < NV; ++q) {
             const P v = slot[((i & (kAhead - 1)) * NV + q) * kThreads];
+            if constexpr (E == 1) {
+                acc[q] += to_f32(v.v[0]);
+            } else {
 #pragma unroll
-            for (int e = 0; e < E; ++e) acc[q * E + e] += to_f32(v.v[e]);
+                for (int e = 0; e < E; e += 2) {
+                    const float2 p = __fadd2_rn(make_float2(acc[q * E + e], acc[q * E + e + 1]), pair_of(v.v + e));
+                    acc[q * E + e] = p.x;
+                    acc[q * E + e + 1] = p.y;
+                }
+            }
         }
         ++i;
-        const uint32_t k = i < end ? s.keys[i] : none;
+        const uint32_t k = i < end ? s.items[i].x : none;
         if (k == key) continue;
         const bool tail = i >= end && long_out;
         if (head || tail) write_part<E, NV>(a, head ? part : part + a.width, c0, s.lanes, acc);
@@ -427,24 +438,24 @@ __global__ void __launch_bounds__(kThreads) k_sum(EmbedArgs a, SumArgs s)
 }
 
 constexpr int kJoinThreads = 512;
-constexpr int kJoinBlocks = 4 * kSMs;
+constexpr int kJoinBlocks = 2 * kSMs;
 
 // The row of each long run: the second part of the unit it begins in and the
 // first parts of the units up to its last.  One block per run and tile at a
-// time; its groups of lanes each take a stretch of the units, added up in a
-// fixed tree.
+// time; its groups of lanes each take a stretch of the units, and a thread per
+// column adds the groups up in order.
 template <typename TO, int E>
 __global__ void __launch_bounds__(kJoinThreads) k_join(EmbedArgs a, SumArgs s)
 {
     constexpr int NV = kCols / E;
-    __shared__ float sh[kJoinThreads / 2 * kCols];
+    __shared__ float sh[kJoinThreads * kCols];  // [group][column of the tile]
     wait_for_previous();
-    const int lanes = s.lanes, groups = kJoinThreads / lanes;
+    const int lanes = s.lanes, groups = kJoinThreads / lanes, cols = lanes * kCols;
     const int group = threadIdx.x / lanes, lane = threadIdx.x & (lanes - 1);
     const int64_t items = (int64_t)s.runs[0] * s.tiles;
     for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
         const int64_t run = it / s.tiles;
-        const int c0 = ((int)(it - run * s.tiles) * lanes * NV + lane) * E;
+        const int tile0 = (int)(it - run * s.tiles) * cols;
         const uint32_t key = s.runs[1 + 2 * run];
         const int64_t first = s.runs[2 + 2 * run], count = (int64_t)s.last[key] - first + 1;
         float acc[kCols];
@@ -453,28 +464,33 @@ __global__ void __launch_bounds__(kJoinThreads) k_join(EmbedArgs a, SumArgs s)
         const int64_t to = first + count * (group + 1) / groups;
 #pragma unroll 4
         for (int64_t u = first + count * group / groups; u < to; ++u) {
-            const float *p = s.part + (u * 2 + (u == first)) * a.width;
+            const float *p = s.part + (u * 2 + (u == first)) * a.width + tile0;
 #pragma unroll
             for (int q = 0; q < NV; ++q) {
-                const int c = c0 + q * lanes * E;
-                if (c >= a.width) continue;
+                const int c = (q * lanes + lane) * E;
+                if (tile0 + c >= a.width) continue;
                 const auto v = load_pack<float, E>(p + c);
 #pragma unroll
                 for (int e = 0; e < E; ++e) acc[q * E + e] += v.v[e];
             }
         }
-        for (int half = groups >> 1; half > 0; half >>= 1) {
-            const int at = threadIdx.x - half * lanes;
-            __syncthreads();
-            if (group >= half && group < 2 * half)
 #pragma unroll
-                for (int c = 0; c < kCols; ++c) sh[c * (kJoinThreads / 2) + at] = acc[c];
-            __syncthreads();
-            if (group < half)
+        for (int q = 0; q < NV; ++q) {
+            Pack<float, E> v;
 #pragma unroll
-                for (int c = 0; c < kCols; ++c) acc[c] += sh[c * (kJoinThreads / 2) + threadIdx.x];
+            for (int e = 0; e < E; ++e) v.v[e] = acc[q * E + e];
+            store_pack<float, E>(sh + group * cols + (q * lanes + lane) * E, v);
         }
-        if (group == 0) write_row<TO, E, NV>(a, key, c0, lanes, acc);
+        __syncthreads();
+        for (int c = threadIdx.x; c < cols && tile0 + c < a.width; c += kJoinThreads) {
+            float x = 0.0f;
+            for (int g = 0; g < groups; ++g) x += sh[g * cols + c];
+            x *= a.scale;
+            TO *p = static_cast<TO *>(a.out) + (int64_t)key * a.out_stride + tile0 + c;
+            if (a.accumulate) x += to_f32(*p);
+            *p = from_f32<TO>(x);
+        }
+        __syncthreads();
     }
 }
 
@@ -504,12 +520,15 @@ __global__ void __launch_bounds__(kFewThreads) k_grad_few(EmbedArgs a, int rows,
     for (int i = threadIdx.x; i < rows; i += kFewThreads) touched[i] = 0;
     constexpr int R = kFew / kFewThreads;
     int r[R];  // row in the block, -1: another block's or none
+    bool bad = false;
 #pragma unroll
     for (int k = 0; k < R; ++k) {
         const int64_t i = k * kFewThreads + threadIdx.x;
-        const int64_t v = i < a.n ? row_of(a, i, a.bad) : -1;
+        const int64_t v = i < a.n ? row_of(a, i) : kPadRow;
+        bad = bad || v == kBadRow;
         r[k] = v >= 0 && (uint32_t)v % blocks == block ? (int)((uint32_t)v / blocks) : -1;
     }
+    if (bad) *a.bad = 1;
     __syncthreads();
     uint32_t count = 0;
     for (int k = 0; k < R; ++k) {
@@ -618,9 +637,9 @@ void lanes_of(int width, int *lanes, int *tiles)
 }
 
 struct GradLayout {
-    int passes = 0, tiles = 0, bins = 0;
+    int passes = 0, items = 1, tiles = 0, bins = 0;
     int64_t units = 0;
-    size_t keys = 0, vals = 0, keys2 = 0, vals2 = 0, counts = 0, present = 0, part = 0, runs = 0, last = 0, bytes = 0;
+    size_t sorted[2] = {}, counts = 0, present = 0, part = 0, runs = 0, last = 0, bytes = 0;
 };
 
 GradLayout layout(const EmbedArgs &a)
@@ -630,14 +649,12 @@ GradLayout layout(const EmbedArgs &a)
     const int bits = bits_of(a.vocab);  // keys 0 .. vocab
     l.passes = (bits + kMaxBits - 1) / kMaxBits;
     l.bins = 1 << ((bits + l.passes - 1) / l.passes);
-    l.tiles = (int)((a.n + kSortTile - 1) / kSortTile);
+    while (l.items < kMaxItems && a.n > (int64_t)kSumTiles * kSortThreads * l.items) l.items <<= 1;
+    l.tiles = (int)((a.n + kSortThreads * l.items - 1) / (kSortThreads * l.items));
     l.units = (a.n + kUnit - 1) / kUnit;
     size_t at = 0;
     auto take = [&](size_t b) { const size_t p = at; at += up(b); return p; };
-    l.keys = take(4 * (size_t)a.n);
-    l.vals = take(4 * (size_t)a.n);
-    l.keys2 = take(4 * (size_t)a.n);
-    l.vals2 = take(4 * (size_t)a.n);
+    for (size_t &p : l.sorted) p = take(8 * (size_t)a.n);
     l.counts = take(4 * (size_t)l.bins * (l.tiles + 1));
     l.present = take((size_t)a.vocab);
     l.part = take(8 * (size_t)l.units * a.width);
@@ -666,7 +683,7 @@ cudaError_t embed(const EmbedArgs &a, cudaStream_t s, int64_t *launches)
 
 size_t embed_grad_tmp_bytes(const EmbedArgs &a) { return layout(a).bytes; }
 
-cudaError_t embed_grad(const EmbedArgs &a, void *tmp, int *, cudaStream_t st, int64_t *launches)
+cudaError_t embed_grad(const EmbedArgs &a, void *tmp, cudaStream_t st, int64_t *launches)
 {
     const GradLayout l = layout(a);
     if (!l.passes) {
@@ -691,41 +708,47 @@ cudaError_t embed_grad(const EmbedArgs &a, void *tmp, int *, cudaStream_t st, in
     s.tiles = l.tiles;
     s.bits = bits_of(l.bins) - 1;
     s.scanned = l.tiles > kSumTiles;
-    uint32_t *keys[2] = {(uint32_t *)(p + l.keys), (uint32_t *)(p + l.keys2)};
-    uint32_t *vals[2] = {(uint32_t *)(p + l.vals), (uint32_t *)(p + l.vals2)};
+    uint2 *items[2] = {(uint2 *)(p + l.sorted[0]), (uint2 *)(p + l.sorted[1])};
     if (!a.accumulate) {
         s.present = (uint8_t *)(p + l.present);
         HISS_TRY(cudaMemsetAsync(s.present, 0, (size_t)a.vocab, st));
     }
-    return with_types(a, [&](auto ti, auto to, auto e) {
-        using TO = decltype(to);
-        constexpr int E = decltype(e)::value;
-        // the empty rows are written in equal parts by the kernels after the first count
-        const int fills = a.accumulate ? 0 : 2 * l.passes - 1;
-        int filled = 0;
+    for (s.store = 16; s.store > 2; s.store /= 4) {
+        const int e = s.store / (int)dtype_bytes(a.out_dtype);
+        if (e > 0 && a.width % e == 0 && rows_aligned(a.out, a.out_stride, a.out_dtype, e)) break;
+    }
+    if (s.store < 2) s.store = 2;
+    // the empty rows are written in equal parts by the kernels after the first count
+    const int fills = a.accumulate ? 0 : 2 * l.passes - 1;
+    int filled = 0;
+    auto sorted = [&](auto kernel, bool fill) {
+        s.fills = fill ? fills : 0;
+        s.fill = filled;
+        filled += fill;
+        ++*launches;
+        return launch_after(kernel, l.tiles + (s.fills ? kFillBlocks : 0), kSortThreads, 0, st, a, s);
+    };
+    auto sort = [&](auto per_thread) {
+        constexpr int ITEMS = decltype(per_thread)::value;
         for (int i = 0; i < l.passes; ++i) {
             s.shift = i * s.bits;
-            s.keys_in = i ? keys[(i - 1) & 1] : nullptr;
-            s.vals_in = i ? vals[(i - 1) & 1] : nullptr;
-            s.keys_out = keys[i & 1];
-            s.vals_out = vals[i & 1];
-            auto sorted = [&](auto kernel, bool fill) {
-                s.fills = fill ? fills : 0;
-                s.fill = filled;
-                filled += fill;
-                ++*launches;
-                return launch_after(kernel, l.tiles + (s.fills ? kFillBlocks : 0), kSortThreads, 0, st, a, s);
-            };
-            HISS_TRY(sorted(k_sort_count<TO, E>, i > 0));
+            s.in = i ? items[(i - 1) & 1] : nullptr;
+            s.out = items[i & 1];
+            HISS_TRY(sorted(k_sort_count<ITEMS>, i > 0));
             if (s.scanned) {
                 HISS_TRY(launch_after(k_sort_scan, (l.bins + 31) / 32, 1024, 0, st, s));
                 ++*launches;
             }
-            HISS_TRY(sorted(k_sort_scatter<TO, E>, true));
+            HISS_TRY(sorted(k_sort_scatter<ITEMS>, true));
         }
+        return cudaSuccess;
+    };
+    HISS_TRY(l.items == 1 ? sort(Int<1>{}) : l.items == 2 ? sort(Int<2>{}) : l.items == 4 ? sort(Int<4>{}) : sort(Int<8>{}));
+    return with_types(a, [&](auto ti, auto to, auto e) {
+        using TO = decltype(to);
+        constexpr int E = decltype(e)::value;
         SumArgs m{};
-        m.keys = s.keys_out;
-        m.vals = s.vals_out;
+        m.items = s.out;
         m.part = (float *)(p + l.part);
         m.runs = s.runs;
         m.last = (uint32_t *)(p + l.last);

@@ -90,9 +90,10 @@ struct hiss_ctx {
     // exact kNN: per-batch pair scratch, done flags, active query ids
     DBuf k_keys, k_vals, k_keys_alt, k_vals_alt, k_sort_tmp, k_d2, k_prow, k_done, k_active;
 
-    // operators on parameters and activations: workspace, and a device int
-    // that records an out-of-range token until hiss_finish reads it
-    DBuf op_tmp, op_flags;
+    // operators on parameters and activations: workspace, what the clipping
+    // kernels keep from call to call, and a device int that records an
+    // out-of-range token until hiss_finish reads it
+    DBuf op_tmp, op_clip, op_bad;
 
     hiss_stats st{};
     cudaEvent_t ev[8] = {};
@@ -1255,11 +1256,12 @@ int embed_args_ok(const EmbedArgs &a, int64_t rows_n, int64_t out_n)
     return HISS_OK;
 }
 
-int ensure_op_flags(hiss_ctx *ctx)
+// A buffer that is zero when it is new.
+int ensure_zeroed(hiss_ctx *ctx, DBuf &b, size_t bytes)
 {
-    if (ctx->op_flags.p) return HISS_OK;
-    ST(ensure(ctx, ctx->op_flags, sizeof(int) * (kNumFlags + 1)));
-    CK(cudaMemsetAsync(ctx->op_flags.p, 0, sizeof(int) * (kNumFlags + 1), ctx->stream));
+    if (b.p) return HISS_OK;
+    ST(ensure(ctx, b, bytes));
+    CK(cudaMemsetAsync(b.p, 0, bytes, ctx->stream));
     return HISS_OK;
 }
 
@@ -1313,7 +1315,7 @@ void hiss_destroy(hiss_ctx *ctx)
                    &ctx->q_bound, &ctx->q_work_key, &ctx->q_cell_idx, &ctx->q_work, &ctx->k_keys,
                    &ctx->k_vals, &ctx->k_keys_alt, &ctx->k_vals_alt, &ctx->k_sort_tmp, &ctx->k_d2, &ctx->k_prow,
                    &ctx->k_done, &ctx->k_active, &ctx->row_ptr2, &ctx->cols2, &ctx->row_ptr_sub, &ctx->unit_tile, &ctx->unit_chunk,
-                   &ctx->query_ids2, &ctx->query_rows2, &ctx->op_tmp, &ctx->op_flags};
+                   &ctx->query_ids2, &ctx->query_rows2, &ctx->op_tmp, &ctx->op_clip, &ctx->op_bad};
     if (ctx->copy_stream) cudaStreamSynchronize(ctx->copy_stream);
     for (DBuf *b : all) release(ctx, *b);
     cudaStreamSynchronize(ctx->stream);
@@ -1581,8 +1583,8 @@ int hiss_embed(hiss_ctx *ctx, const void *d_table, int32_t table_dtype, int64_t 
                 d_out, out_dtype, out_stride, 0, nullptr};
     ST(embed_args_ok(a, vocab, n));
     if (n == 0) return HISS_OK;
-    ST(ensure_op_flags(ctx));
-    a.bad = as<int>(ctx->op_flags) + kNumFlags;
+    ST(ensure_zeroed(ctx, ctx->op_bad, sizeof(int)));
+    a.bad = as<int>(ctx->op_bad);
     CK(embed(a, ctx->stream, &ctx->launches));
     return HISS_OK;
 }
@@ -1596,10 +1598,10 @@ int hiss_embed_grad(hiss_ctx *ctx, const void *d_dy, int32_t dy_dtype, int64_t d
                 d_grad, grad_dtype, grad_stride, accumulate, nullptr};
     if (accumulate != 0 && accumulate != 1) return HISS_E_ARG;
     ST(embed_args_ok(a, n, vocab));
-    ST(ensure_op_flags(ctx));
+    ST(ensure_zeroed(ctx, ctx->op_bad, sizeof(int)));
     ST(ensure(ctx, ctx->op_tmp, embed_grad_tmp_bytes(a)));
-    a.bad = as<int>(ctx->op_flags) + kNumFlags;
-    CK(embed_grad(a, ctx->op_tmp.p, as<int>(ctx->op_flags), ctx->stream, &ctx->launches));
+    a.bad = as<int>(ctx->op_bad);
+    CK(embed_grad(a, ctx->op_tmp.p, ctx->stream, &ctx->launches));
     return HISS_OK;
 }
 
@@ -1706,24 +1708,20 @@ int hiss_clip_grads(hiss_ctx *ctx, const hiss_tensor *tensors, int64_t count, fl
         if ((t.out && t.out != t.in && overlap(in, out)) || overlap(norm, in) || overlap(norm, out)) return HISS_E_ARG;
     }
     ST(ensure(ctx, ctx->op_tmp, clip_tmp_bytes(tensors, count)));
-    CK(clip_grads(tensors, count, max_norm, d_norm, ctx->op_tmp.p, ctx->stream, &ctx->launches));
+    ST(ensure_zeroed(ctx, ctx->op_clip, clip_state_bytes()));
+    CK(clip_grads(tensors, count, max_norm, d_norm, ctx->op_clip.p, ctx->op_tmp.p, ctx->stream, &ctx->launches));
     return HISS_OK;
 }
 
 int hiss_finish(hiss_ctx *ctx)
 {
     ST(enter(ctx));
-    if (!ctx->op_flags.p) return sync(ctx);
-    int h[kNumFlags + 1];
-    CK(cudaMemcpyAsync(h, ctx->op_flags.p, sizeof(h), cudaMemcpyDeviceToHost, ctx->stream));
-    CK(cudaMemsetAsync(ctx->op_flags.p, 0, sizeof(h), ctx->stream));
+    if (!ctx->op_bad.p) return sync(ctx);
+    int bad = 0;
+    CK(cudaMemcpyAsync(&bad, ctx->op_bad.p, sizeof(bad), cudaMemcpyDeviceToHost, ctx->stream));
+    CK(cudaMemsetAsync(ctx->op_bad.p, 0, sizeof(bad), ctx->stream));
     ST(sync(ctx));
-    if (h[kFlagSortTimeout]) {
-        snprintf(ctx->cuda_err, sizeof(ctx->cuda_err), "token sort look-back exceeded its wait limit");
-        ctx->sticky = HISS_E_CUDA;
-        return HISS_E_CUDA;
-    }
-    return h[kNumFlags] ? HISS_E_ARG : HISS_OK;
+    return bad ? HISS_E_ARG : HISS_OK;
 }
 
 }  // extern "C"

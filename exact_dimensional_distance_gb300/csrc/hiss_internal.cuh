@@ -249,7 +249,7 @@ struct EmbedArgs {
 cudaError_t embed(const EmbedArgs &a, cudaStream_t s, int64_t *launches);
 // Workspace of embed_grad in bytes.
 size_t embed_grad_tmp_bytes(const EmbedArgs &a);
-cudaError_t embed_grad(const EmbedArgs &a, void *tmp, int *flags, cudaStream_t s, int64_t *launches);
+cudaError_t embed_grad(const EmbedArgs &a, void *tmp, cudaStream_t s, int64_t *launches);
 
 struct NormArgs {
     const void *x, *dy;    // dy: backward only
@@ -267,8 +267,11 @@ cudaError_t layer_norm(const NormArgs &a, cudaStream_t s, int64_t *launches);
 size_t layer_norm_grad_tmp_bytes(const NormArgs &a);
 cudaError_t layer_norm_grad(const NormArgs &a, void *tmp, cudaStream_t s, int64_t *launches);
 
+// state: clip_state_bytes() of device memory, zero before the first call and
+// left to the calls from then on.
+size_t clip_state_bytes();
 size_t clip_tmp_bytes(const hiss_tensor *t, int64_t count);
-cudaError_t clip_grads(const hiss_tensor *t, int64_t count, float max_norm, float *norm, void *tmp, cudaStream_t s,
-                       int64_t *launches);
+cudaError_t clip_grads(const hiss_tensor *t, int64_t count, float max_norm, float *norm, void *state, void *tmp,
+                       cudaStream_t s, int64_t *launches);
 
 }  // namespace hiss
