@@ -84,23 +84,25 @@ constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kMaxItems = 8;  // positions per thread
 constexpr int kMaxBits = 9;  // one bin per thread
 constexpr int kMaxBins = 1 << kMaxBits;
-// Up to this many tiles each block of the scatter adds up the tiles' counts
-// itself; above, their prefix sums are a kernel of their own.  Tiles are as small
-// as this allows, down to one position per thread: the sort is a chain
-// of latencies, and few large tiles leave it on few SMs (65,536 positions in
-// 16 tiles: 11 us for the first count).
-constexpr int kSumTiles = 128;
-constexpr int kFillBlocks = 2 * kSMs;
+// The sort is a chain of latencies.  Tiles are as small as kManyTiles
+// allows: few large ones leave it on few SMs.  Up to kSumTiles each block of the
+// scatter adds up the tiles' counts itself; above, their prefix sums are a kernel of
+// their own.
+constexpr int kManyTiles = 128;
+constexpr int kSumTiles = 32;
+constexpr int kBitmapWords = 8192;  // of a block's bitmap of tokens (32 KB: a vocabulary of 262,144)
 
 struct SortArgs {
     const uint2 *in;     // (key, position); NULL: the tokens and their positions
     uint2 *out;
-    uint32_t *counts;    // [tiles][bins], exclusive over tiles once scanned; then [bins] totals
-    uint8_t *present;    // [vocab] token occurs (NULL: not wanted)
-    uint32_t *runs;      // set to 0 by the first kernel: number of long runs (SumArgs)
+    uint32_t *counts;    // digit counts of the input's tiles: [tiles][bins], exclusive over the
+                         // tiles once scanned; then [bins] totals
+    uint32_t *counts_out;  // the next digit's counts of the output's tiles (NULL: last pass)
+    uint32_t *present;   // [ceil(vocab / 32)] bit: the token occurs (NULL: not wanted); 0 between calls
+    uint32_t *runs;      // number of long runs (SumArgs), set to 0 by the first kernel
+    uint32_t *clear;     // the later passes' counts, set to 0 by the first kernel
+    int64_t clear_n;
     int tiles, shift, bits, scanned;
-    int fill, fills;     // this kernel writes part fill of fills of the empty rows (fills = 0: none)
-    int store;           // bytes per store that the gradient's rows allow
 };
 
 // Entry i: the token (vocab for a position without a row) and its position.
@@ -118,42 +120,54 @@ __device__ __forceinline__ void zero_row(char *p, int64_t bytes, int lane)
     for (int64_t i = lane * sizeof(T); i < bytes; i += 32 * sizeof(T)) *reinterpret_cast<T *>(p + i) = T{};
 }
 
-// Zeros (all bits 0 in every type) for the rows of this kernel's part of the
-// vocabulary that no position holds, by the blocks past the sort's.
-__device__ void fill_empty(const EmbedArgs &a, const SortArgs &s)
+// Zeros (all bits 0 in every type) for the rows that no position holds, in
+// this kernel's share [f0, f1) of kShares of the vocabulary.  warp of warps.
+constexpr int kShares = 8, kScatterShare = 2;
+struct Fill {
+    const uint32_t *present;
+    int f0, f1;
+    int store;           // bytes per store that the gradient's rows allow
+    int blocks;          // blocks of the kernel that do this, behind the others
+};
+__device__ void fill_empty(const EmbedArgs &a, const Fill &f, int64_t warp, int64_t warps)
 {
     const int lane = threadIdx.x & 31;
-    const int64_t v0 = a.vocab * s.fill / s.fills, v1 = a.vocab * (s.fill + 1) / s.fills;
-    const int64_t warp = (int64_t)(blockIdx.x - s.tiles) * kSortWarps + (threadIdx.x >> 5);
-    const int64_t warps = (int64_t)(gridDim.x - s.tiles) * kSortWarps;
+    const int64_t words = (a.vocab + 31) / 32;
+    const int64_t v0 = words * f.f0 / kShares * 32, v1 = min(words * f.f1 / kShares * 32, a.vocab);
     const int size = a.out_dtype == HISS_F32 ? 4 : 2;
     const int64_t bytes = (int64_t)a.width * size, stride = a.out_stride * size;
-    const int rows = (int)min((int64_t)32, (v1 - v0 + warps - 1) / warps);  // per warp and turn
+    int rows = 32;  // per warp and turn: a power of two, so that they share a word
+    while (rows > 1 && (v1 - v0) < warps * rows) rows >>= 1;
     for (int64_t v = v0 + warp * rows; v < v1; v += warps * rows) {
-        unsigned empty = __ballot_sync(0xffffffffu, lane < rows && v + lane < v1 && !s.present[min(v + lane, v1 - 1)]);
+        uint32_t empty = ~(f.present[v >> 5] >> (v & 31));
+        if (rows < 32) empty &= (1u << rows) - 1u;
         while (empty) {
-            char *p = static_cast<char *>(a.out) + (v + __ffs(empty) - 1) * stride;
+            const int64_t r = v + __ffs(empty) - 1;
             empty &= empty - 1;
-            if (s.store == 16) zero_row<uint4>(p, bytes, lane);
-            else if (s.store == 4) zero_row<uint32_t>(p, bytes, lane);
+            if (r >= v1) break;
+            char *p = static_cast<char *>(a.out) + r * stride;
+            if (f.store == 16) zero_row<uint4>(p, bytes, lane);
+            else if (f.store == 4) zero_row<uint32_t>(p, bytes, lane);
             else zero_row<uint16_t>(p, bytes, lane);
         }
     }
 }
 
-// Digit counts of each tile (and, in the first pass, which tokens occur).
+// First digit's counts of each tile, and which tokens occur.
 template <int ITEMS>
 __global__ void __launch_bounds__(kSortThreads) k_sort_count(EmbedArgs a, SortArgs s)
 {
     __shared__ uint32_t hist[kMaxBins];
-    let_next_start();
+    extern __shared__ uint32_t bitmap[];  // the tile's tokens, up to kBitmapWords
+    const int words = s.present ? (int)((a.vocab + 31) / 32) : 0;
+    const bool merge = words <= kBitmapWords;
     wait_for_previous();
-    if ((int)blockIdx.x >= s.tiles) {
-        fill_empty(a, s);
-        return;
-    }
     hist[threadIdx.x] = 0;
-    if (!s.in && blockIdx.x == 0 && threadIdx.x == 0) *s.runs = 0;
+    if (merge)
+        for (int i = threadIdx.x; i < words; i += kSortThreads) bitmap[i] = 0;
+    if (blockIdx.x == 0 && threadIdx.x == 0) *s.runs = 0;
+    for (int64_t i = (int64_t)blockIdx.x * kSortThreads + threadIdx.x; i < s.clear_n; i += (int64_t)gridDim.x * kSortThreads)
+        s.clear[i] = 0;
     __syncthreads();
     const uint32_t mask = (1u << s.bits) - 1u;
     const int64_t base = (int64_t)blockIdx.x * (kSortThreads * ITEMS);
@@ -168,12 +182,19 @@ __global__ void __launch_bounds__(kSortThreads) k_sort_count(EmbedArgs a, SortAr
 #pragma unroll
     for (int k = 0; k < ITEMS; ++k) {
         if (base + k * kSortThreads + threadIdx.x >= a.n) continue;
-        if (s.present && !s.in && key[k] < (uint32_t)a.vocab) s.present[key[k]] = 1;
+        // the tile's tokens are collected first: frequent ones share a few
+        // sectors, and one access per position to those is served in turn
+        if (words && key[k] < (uint32_t)a.vocab)
+            atomicOr(merge ? &bitmap[key[k] >> 5] : &s.present[key[k] >> 5], 1u << (key[k] & 31));
         atomicAdd(&hist[(key[k] >> s.shift) & mask], 1u);
     }
     __syncthreads();
+    if (merge)
+        for (int i = threadIdx.x; i < words; i += kSortThreads)
+            if (bitmap[i]) atomicOr(&s.present[i], bitmap[i]);
     const int bins = 1 << s.bits;
     if ((int)threadIdx.x < bins) s.counts[(int64_t)blockIdx.x * bins + threadIdx.x] = hist[threadIdx.x];
+    let_next_start();
 }
 
 // counts[t][bin] := sum over the tiles before t; totals behind them.  32 bins
@@ -181,7 +202,6 @@ __global__ void __launch_bounds__(kSortThreads) k_sort_count(EmbedArgs a, SortAr
 __global__ void __launch_bounds__(1024) k_sort_scan(SortArgs s)
 {
     __shared__ uint32_t sum[32][33];
-    let_next_start();
     wait_for_previous();
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const int bins = 1 << s.bits, bin = blockIdx.x * 32 + lane;
@@ -200,20 +220,20 @@ __global__ void __launch_bounds__(1024) k_sort_scan(SortArgs s)
         run += c;
     }
     if (w == 31) s.counts[(int64_t)s.tiles * bins + bin] = run;
+    let_next_start();
 }
 
 // One stable pass: each tile's positions go behind those of the tiles before
-// it, digit by digit.
+// it, digit by digit.  Counts the next digit of the tiles it writes to on the way.
 template <int ITEMS>
-__global__ void __launch_bounds__(kSortThreads) k_sort_scatter(EmbedArgs a, SortArgs s)
+__global__ void __launch_bounds__(kSortThreads) k_sort_scatter(EmbedArgs a, SortArgs s, Fill f)
 {
     __shared__ uint32_t whist[kSortWarps][kMaxBins];
     __shared__ uint32_t base_of[kMaxBins];
     __shared__ uint32_t warp_total[kSortWarps];
-    let_next_start();
     wait_for_previous();
     if ((int)blockIdx.x >= s.tiles) {
-        fill_empty(a, s);
+        fill_empty(a, f, (int64_t)(blockIdx.x - s.tiles) * kSortWarps + (threadIdx.x >> 5), (int64_t)f.blocks * kSortWarps);
         return;
     }
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -284,7 +304,13 @@ __global__ void __launch_bounds__(kSortThreads) k_sort_scatter(EmbedArgs a, Sort
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < ITEMS; ++k)
-        if (base + k * 32 + lane < a.n) s.out[whist[warp][(item[k].x >> s.shift) & mask] + rank[k]] = item[k];
+        if (base + k * 32 + lane < a.n) {
+            const uint32_t at = whist[warp][(item[k].x >> s.shift) & mask] + rank[k];
+            s.out[at] = item[k];
+            if (s.counts_out)
+                atomicAdd(&s.counts_out[(int64_t)(at / (kSortThreads * ITEMS)) * bins + ((item[k].x >> (s.shift + s.bits)) & mask)], 1u);
+        }
+    let_next_start();
 }
 
 // ---- the sums ---------------------------------------------------------------------
@@ -297,8 +323,10 @@ struct SumArgs {
                                   // before, and of the long run that begins here
     uint32_t *runs;               // [0]: number of long runs; then (key, first unit) of each
     uint32_t *last;               // [vocab]: last unit of a long run
+    uint32_t *present;            // cleared at the end
     int64_t units;
     int lanes, tiles;             // lanes * kCols columns per tile
+    int blocks;                   // of k_sum that sum (the others write empty rows)
 };
 
 // Write (or add) a finished row's columns.
@@ -341,22 +369,29 @@ constexpr int kAhead = 4;  // rows in flight per lane
 template <typename TI, int E>
 constexpr size_t sum_bytes() { return (size_t)kThreads * kAhead * kCols * sizeof(TI); }
 
-template <typename TI, typename TO, int E>
-__global__ void __launch_bounds__(kThreads) k_sum(EmbedArgs a, SumArgs s)
+// FULL: 32 lanes, so that a lane's packs are a constant distance apart.
+template <typename TI, typename TO, int E, bool FULL>
+__global__ void __launch_bounds__(kThreads) k_sum(EmbedArgs a, SumArgs s, Fill f)
 {
     constexpr int NV = kCols / E;
     using P = Pack<TI, E>;
     constexpr bool kAsync = sizeof(TI) * E >= 4;  // single 16-bit elements cannot be copied asynchronously
     extern __shared__ __align__(16) char ring[];
-    let_next_start();
     wait_for_previous();
-    const int64_t item = ((int64_t)blockIdx.x * kThreads + threadIdx.x) / s.lanes;
-    const int lane = threadIdx.x & (s.lanes - 1);
+    if ((int)blockIdx.x >= s.blocks) {
+        fill_empty(a, f, (int64_t)(blockIdx.x - s.blocks) * (kThreads / 32) + (threadIdx.x >> 5),
+                   (int64_t)f.blocks * (kThreads / 32));
+        return;
+    }
+    const int lanes = FULL ? 32 : s.lanes;
+    const int64_t item = ((int64_t)blockIdx.x * kThreads + threadIdx.x) / lanes;
+    const int lane = threadIdx.x & (lanes - 1);
     if (item >= s.units * s.tiles) return;
     // tiles of a unit are neighbours: they read the same rows of dy
     const int64_t unit = item / s.tiles;
     const int tile = (int)(item - unit * s.tiles);
-    const int c0 = (tile * s.lanes * NV + lane) * E;
+    const int c0 = (tile * lanes * NV + lane) * E;
+    const int packs = min(NV, (a.width - tile * lanes * kCols + lanes * E - 1) / (lanes * E));  // of a row in this tile
     const int n = (int)a.n, i0 = (int)unit * kUnit, i1 = min(i0 + kUnit, n);
     const uint32_t vocab = (uint32_t)a.vocab, none = ~0u;
     auto key_of = [&](int i) { return i >= 0 && i < n ? s.items[i].x : none; };
@@ -387,15 +422,17 @@ __global__ void __launch_bounds__(kThreads) k_sum(EmbedArgs a, SumArgs s)
     if (i >= end) return;
 
     P *slot = reinterpret_cast<P *>(ring) + threadIdx.x;
+    const TI *rows = static_cast<const TI *>(a.rows) + c0;
     auto fetch = [&](int j) {
         if (j < end) {
-            const TI *p = static_cast<const TI *>(a.rows) + (int64_t)s.items[j].y * a.rows_stride + c0;
+            const TI *p = rows + (int64_t)s.items[j].y * a.rows_stride;
+            P *d = slot + (j & (kAhead - 1)) * (NV * kThreads);
 #pragma unroll
             for (int q = 0; q < NV; ++q) {
-                if (c0 + q * s.lanes * E >= a.width) continue;
-                P *d = slot + ((j & (kAhead - 1)) * NV + q) * kThreads;
-                if constexpr (kAsync) copy_pack_async<TI, E>(d, p + q * s.lanes * E);
-                else *d = load_pack<TI, E>(p + q * s.lanes * E);
+                if (q >= packs) break;
+                if (q == packs - 1 && c0 + q * lanes * E >= a.width) break;
+                if constexpr (kAsync) copy_pack_async<TI, E>(d + q * kThreads, p + q * lanes * E);
+                else d[q * kThreads] = load_pack<TI, E>(p + q * lanes * E);
             }
         }
         cp_async_commit();
@@ -412,6 +449,7 @@ __global__ void __launch_bounds__(kThreads) k_sum(EmbedArgs a, SumArgs s)
         cp_async_wait<kAhead - 1>();
 #pragma unroll
         for (int q = 0; q < NV; ++q) {
+            if (q >= packs) break;
             const P v = slot[((i & (kAhead - 1)) * NV + q) * kThreads];
             if constexpr (E == 1) {
                 acc[q] += to_f32(v.v[0]);
@@ -428,13 +466,14 @@ __global__ void __launch_bounds__(kThreads) k_sum(EmbedArgs a, SumArgs s)
         const uint32_t k = i < end ? s.items[i].x : none;
         if (k == key) continue;
         const bool tail = i >= end && long_out;
-        if (head || tail) write_part<E, NV>(a, head ? part : part + a.width, c0, s.lanes, acc);
-        else write_row<TO, E, NV>(a, key, c0, s.lanes, acc);
+        if (head || tail) write_part<E, NV>(a, head ? part : part + a.width, c0, lanes, acc);
+        else write_row<TO, E, NV>(a, key, c0, lanes, acc);
         key = k;
         head = false;
 #pragma unroll
         for (int c = 0; c < kCols; ++c) acc[c] = 0.0f;
     }
+    let_next_start();
 }
 
 constexpr int kJoinThreads = 512;
@@ -452,6 +491,9 @@ __global__ void __launch_bounds__(kJoinThreads) k_join(EmbedArgs a, SumArgs s)
     wait_for_previous();
     const int lanes = s.lanes, groups = kJoinThreads / lanes, cols = lanes * kCols;
     const int group = threadIdx.x / lanes, lane = threadIdx.x & (lanes - 1);
+    if (s.present)
+        for (int64_t i = (int64_t)blockIdx.x * kJoinThreads + threadIdx.x; i < (a.vocab + 31) / 32; i += (int64_t)gridDim.x * kJoinThreads)
+            s.present[i] = 0;
     const int64_t items = (int64_t)s.runs[0] * s.tiles;
     for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
         const int64_t run = it / s.tiles;
@@ -639,7 +681,7 @@ void lanes_of(int width, int *lanes, int *tiles)
 struct GradLayout {
     int passes = 0, items = 1, tiles = 0, bins = 0;
     int64_t units = 0;
-    size_t sorted[2] = {}, counts = 0, present = 0, part = 0, runs = 0, last = 0, bytes = 0;
+    size_t sorted[2] = {}, counts = 0, counts_later = 0, later_n = 0, part = 0, runs = 0, last = 0, bytes = 0;
 };
 
 GradLayout layout(const EmbedArgs &a)
@@ -649,14 +691,16 @@ GradLayout layout(const EmbedArgs &a)
     const int bits = bits_of(a.vocab);  // keys 0 .. vocab
     l.passes = (bits + kMaxBits - 1) / kMaxBits;
     l.bins = 1 << ((bits + l.passes - 1) / l.passes);
-    while (l.items < kMaxItems && a.n > (int64_t)kSumTiles * kSortThreads * l.items) l.items <<= 1;
+    while (l.items < kMaxItems && a.n > (int64_t)kManyTiles * kSortThreads * l.items) l.items <<= 1;
     l.tiles = (int)((a.n + kSortThreads * l.items - 1) / (kSortThreads * l.items));
     l.units = (a.n + kUnit - 1) / kUnit;
     size_t at = 0;
     auto take = [&](size_t b) { const size_t p = at; at += up(b); return p; };
     for (size_t &p : l.sorted) p = take(8 * (size_t)a.n);
-    l.counts = take(4 * (size_t)l.bins * (l.tiles + 1));
-    l.present = take((size_t)a.vocab);
+    const size_t counts_n = (size_t)l.bins * (l.tiles + 1);
+    l.counts = take(4 * counts_n);
+    l.later_n = counts_n * (l.passes - 1);
+    l.counts_later = take(4 * l.later_n);
     l.part = take(8 * (size_t)l.units * a.width);
     l.runs = take(8 * (size_t)l.units + 4);  // a long run begins in a unit of its own
     l.last = take(4 * (size_t)a.vocab);
@@ -683,7 +727,9 @@ cudaError_t embed(const EmbedArgs &a, cudaStream_t s, int64_t *launches)
 
 size_t embed_grad_tmp_bytes(const EmbedArgs &a) { return layout(a).bytes; }
 
-cudaError_t embed_grad(const EmbedArgs &a, void *tmp, cudaStream_t st, int64_t *launches)
+size_t embed_grad_present_bytes(const EmbedArgs &a) { return a.accumulate || a.n <= kFew ? 0 : 4 * (size_t)((a.vocab + 31) / 32); }
+
+cudaError_t embed_grad(const EmbedArgs &a, void *tmp, uint32_t *present, cudaStream_t st, int64_t *launches)
 {
     const GradLayout l = layout(a);
     if (!l.passes) {
@@ -709,37 +755,40 @@ cudaError_t embed_grad(const EmbedArgs &a, void *tmp, cudaStream_t st, int64_t *
     s.bits = bits_of(l.bins) - 1;
     s.scanned = l.tiles > kSumTiles;
     uint2 *items[2] = {(uint2 *)(p + l.sorted[0]), (uint2 *)(p + l.sorted[1])};
-    if (!a.accumulate) {
-        s.present = (uint8_t *)(p + l.present);
-        HISS_TRY(cudaMemsetAsync(s.present, 0, (size_t)a.vocab, st));
+    s.present = a.accumulate ? nullptr : present;
+    s.clear = (uint32_t *)(p + l.counts_later);
+    s.clear_n = (int64_t)l.later_n;
+    // the empty rows: an eighth with each scatter, whose latencies leave the
+    // memory idle, and the rest beside the sums
+    Fill f{};
+    f.present = s.present;
+    for (f.store = 16; f.store > 2; f.store = f.store == 4 ? 2 : 4) {
+        const int e = f.store / (int)dtype_bytes(a.out_dtype);
+        if (a.width % e == 0 && rows_aligned(a.out, a.out_stride, a.out_dtype, e)) break;
     }
-    for (s.store = 16; s.store > 2; s.store /= 4) {
-        const int e = s.store / (int)dtype_bytes(a.out_dtype);
-        if (e > 0 && a.width % e == 0 && rows_aligned(a.out, a.out_stride, a.out_dtype, e)) break;
-    }
-    if (s.store < 2) s.store = 2;
-    // the empty rows are written in equal parts by the kernels after the first count
-    const int fills = a.accumulate ? 0 : 2 * l.passes - 1;
-    int filled = 0;
-    auto sorted = [&](auto kernel, bool fill) {
-        s.fills = fill ? fills : 0;
-        s.fill = filled;
-        filled += fill;
-        ++*launches;
-        return launch_after(kernel, l.tiles + (s.fills ? kFillBlocks : 0), kSortThreads, 0, st, a, s);
+    auto fill_blocks = [&](int warps) {  // for the share f0 .. f1
+        return (int)std::min<int64_t>(2 * kSMs, (a.vocab * (f.f1 - f.f0) / kShares + warps - 1) / warps);
     };
     auto sort = [&](auto per_thread) {
         constexpr int ITEMS = decltype(per_thread)::value;
+        const size_t words = s.present ? (size_t)((a.vocab + 31) / 32) : 0;
+        HISS_TRY(launch_after(k_sort_count<ITEMS>, l.tiles, kSortThreads, words <= kBitmapWords ? 4 * words : 0, st, a, s));
+        ++*launches;
         for (int i = 0; i < l.passes; ++i) {
             s.shift = i * s.bits;
             s.in = i ? items[(i - 1) & 1] : nullptr;
             s.out = items[i & 1];
-            HISS_TRY(sorted(k_sort_count<ITEMS>, i > 0));
+            if (i) s.counts = s.counts_out;
+            s.counts_out = i + 1 < l.passes ? s.clear + (size_t)l.bins * (l.tiles + 1) * i : nullptr;
             if (s.scanned) {
                 HISS_TRY(launch_after(k_sort_scan, (l.bins + 31) / 32, 1024, 0, st, s));
                 ++*launches;
             }
-            HISS_TRY(sorted(k_sort_scatter<ITEMS>, true));
+            f.f0 = f.f1;
+            f.f1 = f.f0 + kScatterShare;
+            f.blocks = s.present ? fill_blocks(kSortWarps) : 0;
+            HISS_TRY(launch_after(k_sort_scatter<ITEMS>, l.tiles + f.blocks, kSortThreads, 0, st, a, s, f));
+            ++*launches;
         }
         return cudaSuccess;
     };
@@ -754,18 +803,23 @@ cudaError_t embed_grad(const EmbedArgs &a, void *tmp, cudaStream_t st, int64_t *
         m.last = (uint32_t *)(p + l.last);
         m.units = l.units;
         lanes_of(a.width, &m.lanes, &m.tiles);
-        const int64_t blocks = (l.units * m.tiles * m.lanes + kThreads - 1) / kThreads;
+        m.present = s.present;
+        m.blocks = (int)((l.units * m.tiles * m.lanes + kThreads - 1) / kThreads);
+        f.f0 = f.f1;
+        f.f1 = kShares;
+        f.blocks = s.present && f.f0 < f.f1 ? fill_blocks(kThreads / 32) : 0;
         using TI = decltype(ti);
-        auto sum = k_sum<TI, TO, E>;
-        constexpr size_t smem = sum_bytes<TI, E>();
-        if (smem > 48 * 1024) {
-            static std::atomic<bool> allowed{false};
-            if (!allowed.load(std::memory_order_acquire)) {
-                HISS_TRY(cudaFuncSetAttribute(sum, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
+        auto sum = [&](auto full) {
+            auto kernel = k_sum<TI, TO, E, decltype(full)::value>;
+            constexpr size_t smem = sum_bytes<TI, E>();
+            static std::atomic<bool> allowed{false};  // of this kernel
+            if (smem > 48 * 1024 && !allowed.load(std::memory_order_acquire)) {
+                HISS_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
                 allowed.store(true, std::memory_order_release);
             }
-        }
-        HISS_TRY(launch_after(sum, (unsigned)blocks, kThreads, smem, st, a, m));
+            return launch_after(kernel, m.blocks + f.blocks, kThreads, smem, st, a, m, f);
+        };
+        HISS_TRY(m.lanes == 32 ? sum(std::true_type{}) : sum(std::false_type{}));
         HISS_TRY(launch_after(k_join<TO, E>, kJoinBlocks, kJoinThreads, 0, st, a, m));
         *launches += 2;
         return cudaSuccess;

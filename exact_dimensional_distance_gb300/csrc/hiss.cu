@@ -90,10 +90,10 @@ struct hiss_ctx {
     // exact kNN: per-batch pair scratch, done flags, active query ids
     DBuf k_keys, k_vals, k_keys_alt, k_vals_alt, k_sort_tmp, k_d2, k_prow, k_done, k_active;
 
-    // operators on parameters and activations: workspace, what the clipping
-    // kernels keep from call to call, and a device int that records an
-    // out-of-range token until hiss_finish reads it
-    DBuf op_tmp, op_clip, op_bad;
+    // operators on parameters and activations: workspace, counters of the
+    // clipping and flags of the embedding gradient that every call leaves zero, and
+    // a device int that records an out-of-range token until hiss_finish reads it
+    DBuf op_tmp, op_clip, op_present, op_bad;
 
     hiss_stats st{};
     cudaEvent_t ev[8] = {};
@@ -1259,9 +1259,9 @@ int embed_args_ok(const EmbedArgs &a, int64_t rows_n, int64_t out_n)
 // A buffer that is zero when it is new.
 int ensure_zeroed(hiss_ctx *ctx, DBuf &b, size_t bytes)
 {
-    if (b.p) return HISS_OK;
+    if (b.cap >= bytes) return HISS_OK;
     ST(ensure(ctx, b, bytes));
-    CK(cudaMemsetAsync(b.p, 0, bytes, ctx->stream));
+    CK(cudaMemsetAsync(b.p, 0, b.cap, ctx->stream));
     return HISS_OK;
 }
 
@@ -1315,7 +1315,7 @@ void hiss_destroy(hiss_ctx *ctx)
                    &ctx->q_bound, &ctx->q_work_key, &ctx->q_cell_idx, &ctx->q_work, &ctx->k_keys,
                    &ctx->k_vals, &ctx->k_keys_alt, &ctx->k_vals_alt, &ctx->k_sort_tmp, &ctx->k_d2, &ctx->k_prow,
                    &ctx->k_done, &ctx->k_active, &ctx->row_ptr2, &ctx->cols2, &ctx->row_ptr_sub, &ctx->unit_tile, &ctx->unit_chunk,
-                   &ctx->query_ids2, &ctx->query_rows2, &ctx->op_tmp, &ctx->op_clip, &ctx->op_bad};
+                   &ctx->query_ids2, &ctx->query_rows2, &ctx->op_tmp, &ctx->op_clip, &ctx->op_present, &ctx->op_bad};
     if (ctx->copy_stream) cudaStreamSynchronize(ctx->copy_stream);
     for (DBuf *b : all) release(ctx, *b);
     cudaStreamSynchronize(ctx->stream);
@@ -1601,7 +1601,8 @@ int hiss_embed_grad(hiss_ctx *ctx, const void *d_dy, int32_t dy_dtype, int64_t d
     ST(ensure_zeroed(ctx, ctx->op_bad, sizeof(int)));
     ST(ensure(ctx, ctx->op_tmp, embed_grad_tmp_bytes(a)));
     a.bad = as<int>(ctx->op_bad);
-    CK(embed_grad(a, ctx->op_tmp.p, ctx->stream, &ctx->launches));
+    ST(ensure_zeroed(ctx, ctx->op_present, embed_grad_present_bytes(a)));
+    CK(embed_grad(a, ctx->op_tmp.p, as<uint32_t>(ctx->op_present), ctx->stream, &ctx->launches));
     return HISS_OK;
 }
 

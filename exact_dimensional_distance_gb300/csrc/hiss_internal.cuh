@@ -247,9 +247,11 @@ struct EmbedArgs {
     int *bad;              // device int, set to 1 when a token is out of range
 };
 cudaError_t embed(const EmbedArgs &a, cudaStream_t s, int64_t *launches);
-// Workspace of embed_grad in bytes.
+// Workspace of embed_grad in bytes, and the bytes of a second one that is zero
+// before the first call and that each call leaves zero.
 size_t embed_grad_tmp_bytes(const EmbedArgs &a);
-cudaError_t embed_grad(const EmbedArgs &a, void *tmp, cudaStream_t s, int64_t *launches);
+size_t embed_grad_present_bytes(const EmbedArgs &a);
+cudaError_t embed_grad(const EmbedArgs &a, void *tmp, uint32_t *present, cudaStream_t s, int64_t *launches);
 
 struct NormArgs {
     const void *x, *dy;    // dy: backward only
