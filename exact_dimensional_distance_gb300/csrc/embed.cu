@@ -10,7 +10,7 @@
 //   1. the positions are sorted by token (stable LSD radix sort, up to 9 bits
 //      per pass; tokens of a vocabulary below 2^18 take two), while the SMs that the sort
 //      leaves idle write the zeros of the rows without positions;
-//   2. k_sum cuts the sorted positions into units of kUnit and sums runs of equal
+//   2. k_sum cuts the sorted positions into units of 16 or 32 and sums runs of equal
 //      tokens: a run belongs to the unit it begins in, which follows it
 //      into the next unit.  A run that goes on past that one leaves a float32 partial
 //      sum per unit, so the work of a unit is bounded however often a token occurs;
@@ -29,7 +29,6 @@ namespace hiss {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kCols = 16;  // columns per lane of the sums
 
 // The table row of position i; kPadRow for padding and kBadRow for a token
 // outside the table, both rows of zeros.  The caller raises *a.bad once it has
@@ -84,12 +83,12 @@ constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kMaxItems = 8;  // positions per thread
 constexpr int kMaxBits = 9;  // one bin per thread
 constexpr int kMaxBins = 1 << kMaxBits;
-// The sort is a chain of latencies.  Tiles are as small as kManyTiles
-// allows: few large ones leave it on few SMs.  Up to kSumTiles each block of the
+// The sort is a chain of latencies.  Up to kSumTiles tiles each block of the
 // scatter adds up the tiles' counts itself; above, their prefix sums are a kernel of
-// their own.
+// their own, and tiles are as small as kManyTiles allows (few large ones leave
+// the sort on few SMs: 262,144 positions in 64 tiles 6 us more than in 128).
+constexpr int kSumTiles = 32, kSumItems = 4;
 constexpr int kManyTiles = 128;
-constexpr int kSumTiles = 32;
 constexpr int kBitmapWords = 8192;  // of a block's bitmap of tokens (32 KB: a vocabulary of 262,144)
 
 struct SortArgs {
@@ -315,8 +314,6 @@ __global__ void __launch_bounds__(kSortThreads) k_sort_scatter(EmbedArgs a, Sort
 
 // ---- the sums ---------------------------------------------------------------------
 
-constexpr int kUnit = 32;  // sorted positions per unit
-
 struct SumArgs {
     const uint2 *items;           // sorted (token, position)
     float *part;                  // [units][2][width]: sum of the long run that comes in from the unit
@@ -325,19 +322,40 @@ struct SumArgs {
     uint32_t *last;               // [vocab]: last unit of a long run
     uint32_t *present;            // cleared at the end
     int64_t units;
-    int lanes, tiles;             // lanes * kCols columns per tile
+    int unit;                     // positions per unit
+    int lanes, tiles;             // lanes per unit and tile; tiles of a row
     int blocks;                   // of k_sum that sum (the others write empty rows)
 };
 
+// How a group of lanes takes a tile of lanes * C columns of a row.
+//   packed: packs of E elements, pack k of lane l at column (k lanes + l) E of the tile;
+//           each lane copies its own packs to shared memory, ahead of their sum;
+//   raw (E <= 2): rows that are not aligned to 16 bytes.  The group copies the 16-byte
+//           lines that hold the tile and each lane reads its single elements or pairs.
+// BIG tiles (32 lanes of 16 columns) cost the fewest instructions per element, small
+// ones spread a narrow row, or few positions, over more lanes.
+template <typename TI, int E, bool BIG>
+struct SumShape {
+    static constexpr bool RAW = E <= 2;
+    static constexpr int C = BIG ? 16 : RAW ? 2 * E : E;   // columns per lane
+    static constexpr int kAhead = BIG ? 4 : 8;             // rows in the ring
+    // bytes of a row of the ring: a raw tile begins at its offset in a line
+    __host__ __device__ static constexpr int row_bytes(int lanes)
+    {
+        return RAW ? (lanes * C * (int)sizeof(TI) + 16 + 15) / 16 * 16 : lanes * C * (int)sizeof(TI);
+    }
+    static constexpr size_t smem(int lanes) { return (size_t)(kThreads / lanes) * kAhead * row_bytes(lanes); }
+};
+
 // Write (or add) a finished row's columns.
-template <typename TO, int E, int NV>
-__device__ __forceinline__ void write_row(const EmbedArgs &a, uint32_t v, int c0, int lanes, const float (&s)[kCols])
+template <typename TO, int E, int C>
+__device__ __forceinline__ void write_row(const EmbedArgs &a, uint32_t v, int c0, int lanes, const float (&s)[C])
 {
     TO *p = static_cast<TO *>(a.out) + (int64_t)v * a.out_stride;
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
+    for (int k = 0; k < C / E; ++k) {
         const int c = c0 + k * lanes * E;
-        if (c >= a.width) continue;
+        if (c >= a.width) break;
         Pack<TO, E> o;
         if (a.accumulate) o = load_pack<TO, E>(p + c);
 #pragma unroll
@@ -350,13 +368,13 @@ __device__ __forceinline__ void write_row(const EmbedArgs &a, uint32_t v, int c0
     }
 }
 
-template <int E, int NV>
-__device__ __forceinline__ void write_part(const EmbedArgs &a, float *p, int c0, int lanes, const float (&s)[kCols])
+template <int E, int C>
+__device__ __forceinline__ void write_part(const EmbedArgs &a, float *p, int c0, int lanes, const float (&s)[C])
 {
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
+    for (int k = 0; k < C / E; ++k) {
         const int c = c0 + k * lanes * E;
-        if (c >= a.width) continue;
+        if (c >= a.width) break;
         Pack<float, E> o;
 #pragma unroll
         for (int e = 0; e < E; ++e) o.v[e] = s[k * E + e];
@@ -364,18 +382,13 @@ __device__ __forceinline__ void write_part(const EmbedArgs &a, float *p, int c0,
     }
 }
 
-constexpr int kAhead = 4;  // rows in flight per lane
-
-template <typename TI, int E>
-constexpr size_t sum_bytes() { return (size_t)kThreads * kAhead * kCols * sizeof(TI); }
-
-// FULL: 32 lanes, so that a lane's packs are a constant distance apart.
-template <typename TI, typename TO, int E, bool FULL>
+template <typename TI, typename TO, int E, bool BIG>
 __global__ void __launch_bounds__(kThreads) k_sum(EmbedArgs a, SumArgs s, Fill f)
 {
-    constexpr int NV = kCols / E;
+    using S = SumShape<TI, E, BIG>;
+    constexpr bool RAW = S::RAW;
+    constexpr int C = S::C, A = S::kAhead, NV = C / E;
     using P = Pack<TI, E>;
-    constexpr bool kAsync = sizeof(TI) * E >= 4;  // single 16-bit elements cannot be copied asynchronously
     extern __shared__ __align__(16) char ring[];
     wait_for_previous();
     if ((int)blockIdx.x >= s.blocks) {
@@ -383,21 +396,21 @@ __global__ void __launch_bounds__(kThreads) k_sum(EmbedArgs a, SumArgs s, Fill f
                    (int64_t)f.blocks * (kThreads / 32));
         return;
     }
-    const int lanes = FULL ? 32 : s.lanes;
-    const int64_t item = ((int64_t)blockIdx.x * kThreads + threadIdx.x) / lanes;
+    const int lanes = BIG ? 32 : s.lanes;
+    const int64_t item = (int64_t)blockIdx.x * (kThreads / lanes) + threadIdx.x / lanes;
     const int lane = threadIdx.x & (lanes - 1);
     if (item >= s.units * s.tiles) return;
     // tiles of a unit are neighbours: they read the same rows of dy
     const int64_t unit = item / s.tiles;
     const int tile = (int)(item - unit * s.tiles);
-    const int c0 = (tile * lanes * NV + lane) * E;
-    const int packs = min(NV, (a.width - tile * lanes * kCols + lanes * E - 1) / (lanes * E));  // of a row in this tile
-    const int n = (int)a.n, i0 = (int)unit * kUnit, i1 = min(i0 + kUnit, n);
+    const int t0 = tile * lanes * C, cols = min(lanes * C, a.width - t0);  // the tile's columns
+    const int c0 = t0 + lane * E;
+    const int n = (int)a.n, i0 = (int)unit * s.unit, i1 = min(i0 + s.unit, n);
     const uint32_t vocab = (uint32_t)a.vocab, none = ~0u;
     auto key_of = [&](int i) { return i >= 0 && i < n ? s.items[i].x : none; };
     const uint32_t k0 = key_of(i0), k1 = key_of(i1 - 1);
-    const uint32_t prev = key_of(i0 - 1), prev_unit = key_of(i0 - kUnit), prev_unit2 = key_of(i0 - kUnit - 1);
-    const uint32_t next = key_of(i1), next_unit = key_of(i1 + kUnit);
+    const uint32_t prev = key_of(i0 - 1), prev_unit = key_of(i0 - s.unit), prev_unit2 = key_of(i0 - s.unit - 1);
+    const uint32_t next = key_of(i1), next_unit = key_of(i1 + s.unit);
     if (k0 >= vocab) return;  // only positions without a row from here on
     // the run that comes in: summed by the unit before when it began there and
     // ends here, a part of a long run otherwise
@@ -421,114 +434,119 @@ __global__ void __launch_bounds__(kThreads) k_sum(EmbedArgs a, SumArgs s, Fill f
     if (long_in && (next != k0 || k1 != k0) && tile == 0 && lane == 0) s.last[k0] = (uint32_t)unit;
     if (i >= end) return;
 
-    P *slot = reinterpret_cast<P *>(ring) + threadIdx.x;
-    const TI *rows = static_cast<const TI *>(a.rows) + c0;
+    const uint32_t mask = lanes == 32 ? 0xffffffffu : ((1u << lanes) - 1u) << (threadIdx.x & 31 & ~(lanes - 1));
+    const int row_bytes = S::row_bytes(lanes);
+    char *group_ring = ring + (threadIdx.x / lanes) * (A * row_bytes);
+    const TI *rows = static_cast<const TI *>(a.rows) + t0;
+    // lines that reach outside the matrix are copied by element
+    const uintptr_t lo = reinterpret_cast<uintptr_t>(a.rows), hi = lo + ((a.n - 1) * a.rows_stride + a.width) * sizeof(TI);
     auto fetch = [&](int j) {
         if (j < end) {
             const TI *p = rows + (int64_t)s.items[j].y * a.rows_stride;
-            P *d = slot + (j & (kAhead - 1)) * (NV * kThreads);
+            char *d = group_ring + (j & (A - 1)) * row_bytes;
+            if constexpr (RAW) {
+                const uintptr_t b0 = reinterpret_cast<uintptr_t>(p), b1 = b0 + cols * sizeof(TI), line0 = b0 & ~(uintptr_t)15;
+                for (uintptr_t b = line0 + 16 * lane; b < b1; b += 16 * lanes) {
+                    if (b >= lo && b + 16 <= hi) {
+                        cp_async16(d + (b - line0), reinterpret_cast<const void *>(b));
+                    } else {
+                        for (uintptr_t e = max(b, b0); e < min(b + 16, b1); e += sizeof(TI))
+                            *reinterpret_cast<TI *>(d + (e - line0)) = *reinterpret_cast<const TI *>(e);
+                    }
+                }
+            } else {
 #pragma unroll
-            for (int q = 0; q < NV; ++q) {
-                if (q >= packs) break;
-                if (q == packs - 1 && c0 + q * lanes * E >= a.width) break;
-                if constexpr (kAsync) copy_pack_async<TI, E>(d + q * kThreads, p + q * lanes * E);
-                else d[q * kThreads] = load_pack<TI, E>(p + q * lanes * E);
+                for (int k = 0; k < NV; ++k) {
+                    const int c = (k * lanes + lane) * E;
+                    if (c >= cols) break;
+                    copy_pack_async<TI, E>(reinterpret_cast<P *>(d) + k * lanes + lane, p + c);
+                }
             }
         }
         cp_async_commit();
     };
-    for (int k = 0; k < kAhead - 1; ++k) fetch(i + k);
-    float acc[kCols];
+    for (int k = 0; k < A - 1; ++k) fetch(i + k);
+    float acc[C];
 #pragma unroll
-    for (int c = 0; c < kCols; ++c) acc[c] = 0.0f;
+    for (int c = 0; c < C; ++c) acc[c] = 0.0f;
     float *part = s.part + unit * 2 * a.width;
     bool head = long_in;  // the current run is the long one that came in
-    uint32_t key = s.items[i].x;
+    uint2 it = s.items[i];
     while (i < end) {
-        fetch(i + kAhead - 1);
-        cp_async_wait<kAhead - 1>();
+        cp_async_wait<A - 2>();
+        // raw: the row was copied by the whole group, and the row before it has been read
+        // by the whole group before its place in the ring is filled again
+        if (RAW) __syncwarp(mask);
+        fetch(i + A - 1);
+        const char *d = group_ring + (i & (A - 1)) * row_bytes;
+        if constexpr (RAW) d += reinterpret_cast<uintptr_t>(rows + (int64_t)it.y * a.rows_stride) & 15;
 #pragma unroll
-        for (int q = 0; q < NV; ++q) {
-            if (q >= packs) break;
-            const P v = slot[((i & (kAhead - 1)) * NV + q) * kThreads];
+        for (int k = 0; k < NV; ++k) {
+            if (k * lanes * E >= cols) break;
+            // what lies beyond the tile's columns is not written
+            const P v = reinterpret_cast<const P *>(d)[k * lanes + lane];
             if constexpr (E == 1) {
-                acc[q] += to_f32(v.v[0]);
+                acc[k] += to_f32(v.v[0]);
             } else {
 #pragma unroll
                 for (int e = 0; e < E; e += 2) {
-                    const float2 p = __fadd2_rn(make_float2(acc[q * E + e], acc[q * E + e + 1]), pair_of(v.v + e));
-                    acc[q * E + e] = p.x;
-                    acc[q * E + e + 1] = p.y;
+                    const float2 p = __fadd2_rn(make_float2(acc[k * E + e], acc[k * E + e + 1]), pair_of(v.v + e));
+                    acc[k * E + e] = p.x;
+                    acc[k * E + e + 1] = p.y;
                 }
             }
         }
+        const uint32_t key = it.x;
         ++i;
-        const uint32_t k = i < end ? s.items[i].x : none;
-        if (k == key) continue;
+        it = i < end ? s.items[i] : make_uint2(none, 0);
+        if (it.x == key) continue;
         const bool tail = i >= end && long_out;
-        if (head || tail) write_part<E, NV>(a, head ? part : part + a.width, c0, lanes, acc);
-        else write_row<TO, E, NV>(a, key, c0, lanes, acc);
-        key = k;
+        if (head || tail) write_part<E, C>(a, head ? part : part + a.width, c0, lanes, acc);
+        else write_row<TO, E, C>(a, key, c0, lanes, acc);
         head = false;
 #pragma unroll
-        for (int c = 0; c < kCols; ++c) acc[c] = 0.0f;
+        for (int c = 0; c < C; ++c) acc[c] = 0.0f;
     }
     let_next_start();
 }
 
 constexpr int kJoinThreads = 512;
-constexpr int kJoinBlocks = 2 * kSMs;
+constexpr int kJoinCols = 64;      // columns per tile
+constexpr int kJoinBlocks = 4 * kSMs;
 
 // The row of each long run: the second part of the unit it begins in and the
 // first parts of the units up to its last.  One block per run and tile at a
-// time; its groups of lanes each take a stretch of the units, and a thread per
-// column adds the groups up in order.
-template <typename TO, int E>
+// time: a thread per column and stretch of units, the stretches added up in order.
+template <typename TO>
 __global__ void __launch_bounds__(kJoinThreads) k_join(EmbedArgs a, SumArgs s)
 {
-    constexpr int NV = kCols / E;
-    __shared__ float sh[kJoinThreads * kCols];  // [group][column of the tile]
+    constexpr int G = kJoinThreads / kJoinCols;
+    __shared__ float sh[G][kJoinCols];
     wait_for_previous();
-    const int lanes = s.lanes, groups = kJoinThreads / lanes, cols = lanes * kCols;
-    const int group = threadIdx.x / lanes, lane = threadIdx.x & (lanes - 1);
     if (s.present)
         for (int64_t i = (int64_t)blockIdx.x * kJoinThreads + threadIdx.x; i < (a.vocab + 31) / 32; i += (int64_t)gridDim.x * kJoinThreads)
             s.present[i] = 0;
-    const int64_t items = (int64_t)s.runs[0] * s.tiles;
+    const int group = threadIdx.x / kJoinCols, lane = threadIdx.x % kJoinCols;
+    const int tiles = (a.width + kJoinCols - 1) / kJoinCols;
+    const int64_t items = (int64_t)s.runs[0] * tiles;
     for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
-        const int64_t run = it / s.tiles;
-        const int tile0 = (int)(it - run * s.tiles) * cols;
+        const int64_t run = it / tiles;
+        const int c = (int)(it - run * tiles) * kJoinCols + lane;
         const uint32_t key = s.runs[1 + 2 * run];
         const int64_t first = s.runs[2 + 2 * run], count = (int64_t)s.last[key] - first + 1;
-        float acc[kCols];
-#pragma unroll
-        for (int c = 0; c < kCols; ++c) acc[c] = 0.0f;
-        const int64_t to = first + count * (group + 1) / groups;
-#pragma unroll 4
-        for (int64_t u = first + count * group / groups; u < to; ++u) {
-            const float *p = s.part + (u * 2 + (u == first)) * a.width + tile0;
-#pragma unroll
-            for (int q = 0; q < NV; ++q) {
-                const int c = (q * lanes + lane) * E;
-                if (tile0 + c >= a.width) continue;
-                const auto v = load_pack<float, E>(p + c);
-#pragma unroll
-                for (int e = 0; e < E; ++e) acc[q * E + e] += v.v[e];
-            }
+        const int64_t to = first + count * (group + 1) / G;
+        float x = 0.0f;
+        if (c < a.width) {
+#pragma unroll 8
+            for (int64_t u = first + count * group / G; u < to; ++u) x += s.part[(u * 2 + (u == first)) * a.width + c];
         }
-#pragma unroll
-        for (int q = 0; q < NV; ++q) {
-            Pack<float, E> v;
-#pragma unroll
-            for (int e = 0; e < E; ++e) v.v[e] = acc[q * E + e];
-            store_pack<float, E>(sh + group * cols + (q * lanes + lane) * E, v);
-        }
+        sh[group][lane] = x;
         __syncthreads();
-        for (int c = threadIdx.x; c < cols && tile0 + c < a.width; c += kJoinThreads) {
-            float x = 0.0f;
-            for (int g = 0; g < groups; ++g) x += sh[g * cols + c];
+        if (group == 0 && c < a.width) {
+#pragma unroll
+            for (int g = 1; g < G; ++g) x += sh[g][lane];
             x *= a.scale;
-            TO *p = static_cast<TO *>(a.out) + (int64_t)key * a.out_stride + tile0 + c;
+            TO *p = static_cast<TO *>(a.out) + (int64_t)key * a.out_stride + c;
             if (a.accumulate) x += to_f32(*p);
             *p = from_f32<TO>(x);
         }
@@ -538,94 +556,132 @@ __global__ void __launch_bounds__(kJoinThreads) k_join(EmbedArgs a, SumArgs s)
 
 // ---- few positions -------------------------------------------------------------------
 
-constexpr int64_t kFew = 1024;
-constexpr int kFewThreads = 256;
-constexpr int kFewFloats = 8192;  // accumulators of a block
+constexpr int kFew = 2048;
+constexpr int kFewRound = kFew / kThreads;  // tokens per thread
+constexpr int kFewPacks = 4;                // packs per lane
+constexpr int kFewRows = 8192;              // most rows of a fill block
 
-// One kernel without a sort: a block owns some rows and a range of columns (its
-// accumulators in shared memory), picks the positions whose token is one of
-// its rows, in order, and adds them up; every one of its rows is written.
+struct FewArgs {
+    int lanes, tiles;    // lanes (a power of two) per row and tile; tiles of a row
+    int sums;            // blocks that sum: one per position and tile
+    int rows;            // rows of a fill block (the blocks behind those)
+    int store;           // bytes per store that the gradient's rows allow
+};
+
+// One kernel without a sort.  A block per position (and tile of columns): the
+// first position of a token collects the token's other positions, in order,
+// and writes the row; the others leave.  Further blocks write zeros to the rows of
+// their range that no position holds.
 template <typename TI, typename TO, int E>
-__global__ void __launch_bounds__(kFewThreads) k_grad_few(EmbedArgs a, int rows, int lanes)
+__global__ void __launch_bounds__(kThreads) k_grad_few(EmbedArgs a, FewArgs f)
 {
-    __shared__ float acc[kFewFloats];
-    __shared__ uint32_t found[kFew];     // (row in the range) << 10 | position
-    __shared__ uint32_t warp_count[kFewThreads / 32];
-    __shared__ uint8_t touched[kFewFloats];
+    constexpr int U = 8;  // rows in flight
+    __shared__ uint16_t found[kFew];
+    __shared__ uint32_t warp_count[kThreads / 32];
+    __shared__ union {
+        float part[kThreads * E];
+        uint32_t held[kFewRows / 32];
+    } sh;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    // row i of the block is row i * blocks + block of the table: frequent
-    // tokens, which a vocabulary often has next to one another, go to different blocks
-    const uint32_t blocks = gridDim.x, block = blockIdx.x;
-    const int nrows = (int)((a.vocab - block + blocks - 1) / blocks);
-    const int cols = lanes * E;              // columns of the tile
-    const int c0 = blockIdx.y * cols;
-    for (int i = threadIdx.x; i < rows; i += kFewThreads) touched[i] = 0;
-    constexpr int R = kFew / kFewThreads;
-    int r[R];  // row in the block, -1: another block's or none
-    bool bad = false;
+    int64_t r[kFewRound];
 #pragma unroll
-    for (int k = 0; k < R; ++k) {
-        const int64_t i = k * kFewThreads + threadIdx.x;
-        const int64_t v = i < a.n ? row_of(a, i) : kPadRow;
-        bad = bad || v == kBadRow;
-        r[k] = v >= 0 && (uint32_t)v % blocks == block ? (int)((uint32_t)v / blocks) : -1;
+    for (int k = 0; k < kFewRound; ++k) {
+        const int i = k * kThreads + threadIdx.x;
+        r[k] = i < a.n ? row_of(a, i) : kPadRow;
     }
-    if (bad) *a.bad = 1;
-    __syncthreads();
-    uint32_t count = 0;
-    for (int k = 0; k < R; ++k) {
-        const bool hit = r[k] >= 0;
+    if ((int)blockIdx.x >= f.sums) {
+        const int64_t v0 = (int64_t)(blockIdx.x - f.sums) * f.rows, v1 = min(v0 + f.rows, a.vocab);
+        for (int i = threadIdx.x; i < (f.rows + 31) / 32; i += kThreads) sh.held[i] = 0;
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < kFewRound; ++k)
+            if (r[k] >= v0 && r[k] < v1) atomicOr(&sh.held[(r[k] - v0) >> 5], 1u << ((r[k] - v0) & 31));
+        __syncthreads();
+        const int size = sizeof(TO);
+        for (int64_t v = v0 + warp; v < v1; v += kThreads / 32) {
+            if (sh.held[(v - v0) >> 5] >> ((v - v0) & 31) & 1u) continue;
+            char *p = static_cast<char *>(a.out) + v * a.out_stride * size;
+            if (f.store == 16) zero_row<uint4>(p, (int64_t)a.width * size, lane);
+            else if (f.store == 4) zero_row<uint32_t>(p, (int64_t)a.width * size, lane);
+            else zero_row<uint16_t>(p, (int64_t)a.width * size, lane);
+        }
+        return;
+    }
+    const int pos = blockIdx.x / f.tiles, tile = blockIdx.x - pos * f.tiles;
+    const int64_t row = row_of(a, pos);
+    if (row < 0) {
+        if (row == kBadRow && threadIdx.x == 0) *a.bad = 1;
+        return;
+    }
+    bool earlier = false;
+#pragma unroll
+    for (int k = 0; k < kFewRound; ++k) earlier = earlier || (r[k] == row && k * kThreads + (int)threadIdx.x < pos);
+    if (__syncthreads_or(earlier)) return;
+    int count = 0;
+    for (int k = 0; k * kThreads < a.n; ++k) {
+        bool hit = false;
+#pragma unroll
+        for (int q = 0; q < kFewRound; ++q) hit = hit || (q == k && r[q] == row);
         const uint32_t m = __ballot_sync(0xffffffffu, hit);
         if (lane == 0) warp_count[warp] = __popc(m);
         __syncthreads();
-        uint32_t at = count;
-        for (int w = 0; w < kFewThreads / 32; ++w) {
+        int at = count;
+        for (int w = 0; w < kThreads / 32; ++w) {
             if (w < warp) at += warp_count[w];
             count += warp_count[w];
         }
-        if (hit) {
-            found[at + __popc(m & ((1u << lane) - 1u))] = (uint32_t)r[k] << 10 | (uint32_t)(k * kFewThreads + threadIdx.x);
-            touched[r[k]] = 1;
-        }
+        if (hit) found[at + __popc(m & ((1u << lane) - 1u))] = (uint16_t)(k * kThreads + threadIdx.x);
         __syncthreads();
     }
-    // a group of lanes takes the rows of its residue: rows of other groups are not its concern
-    const int group = threadIdx.x / lanes, groups = kFewThreads / lanes, gl = threadIdx.x - group * lanes;
-    const int c = c0 + gl * E;
-    if (group >= groups || c >= a.width) return;
-    for (int i = group; i < nrows; i += groups)
-        if (touched[i])
+    // each group of lanes takes a stretch of the positions
+    const int group = threadIdx.x / f.lanes, groups = kThreads / f.lanes, l = threadIdx.x & (f.lanes - 1);
+    const int c0 = (tile * f.lanes * kFewPacks + l) * E;
+    float acc[kFewPacks][E];
 #pragma unroll
-            for (int e = 0; e < E; ++e) acc[i * cols + gl * E + e] = 0.0f;
-    constexpr int U = 8;  // rows in flight
-    for (uint32_t j = 0; j < count; j += U) {
-        Pack<TI, E> v[U];
-        int at[U];
+    for (int q = 0; q < kFewPacks; ++q)
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const uint32_t f = j + u < count ? found[j + u] : 0u;
-            at[u] = j + u < count && (int)((f >> 10) % groups) == group ? (int)(f >> 10) * cols + gl * E : -1;
-            if (at[u] >= 0)
-                v[u] = load_pack<TI, E>(static_cast<const TI *>(a.rows) + (int64_t)(f & 1023u) * a.rows_stride + c);
+        for (int e = 0; e < E; ++e) acc[q][e] = 0.0f;
+    const int to = count * (group + 1) / groups;
+#pragma unroll
+    for (int q = 0; q < kFewPacks; ++q) {
+        const int c = c0 + q * f.lanes * E;
+        if (c >= a.width) break;
+        const TI *p = static_cast<const TI *>(a.rows) + c;
+        for (int j = count * group / groups; j < to; j += U) {
+            Pack<TI, E> v[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (j + u < to) v[u] = load_pack<TI, E>(p + (int64_t)found[j + u] * a.rows_stride);
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (j + u < to)
+#pragma unroll
+                    for (int e = 0; e < E; ++e) acc[q][e] += to_f32(v[u].v[e]);
         }
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (at[u] >= 0)
-#pragma unroll
-                for (int e = 0; e < E; ++e) acc[at[u] + e] += to_f32(v[u].v[e]);
     }
-    for (int i = group; i < nrows; i += groups) {
-        if (a.accumulate && !touched[i]) continue;
-        TO *p = static_cast<TO *>(a.out) + ((int64_t)i * blocks + block) * a.out_stride + c;
+    if (groups > 1) {  // then a row is one pack per lane: the groups' sums are added up in order
+#pragma unroll
+        for (int e = 0; e < E; ++e) sh.part[(group * E + e) * f.lanes + l] = acc[0][e];
+        __syncthreads();
+        if (group > 0) return;
+        for (int g = 1; g < groups; ++g)
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[0][e] += sh.part[(g * E + e) * f.lanes + l];
+    }
+    TO *p = static_cast<TO *>(a.out) + row * a.out_stride;
+#pragma unroll
+    for (int q = 0; q < kFewPacks; ++q) {
+        const int c = c0 + q * f.lanes * E;
+        if (c >= a.width) break;
         Pack<TO, E> o;
-        if (a.accumulate) o = load_pack<TO, E>(p);
+        if (a.accumulate) o = load_pack<TO, E>(p + c);
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-            float x = touched[i] ? a.scale * acc[i * cols + gl * E + e] : 0.0f;
+            float x = a.scale * acc[q][e];
             if (a.accumulate) x += to_f32(o.v[e]);
             o.v[e] = from_f32<TO>(x);
         }
-        store_pack<TO, E>(p, o);
+        store_pack<TO, E>(p + c, o);
     }
 }
 
@@ -669,17 +725,19 @@ cudaError_t with_types(const EmbedArgs &a, F &&f)
     });
 }
 
-// Lanes (a power of two up to 32) for a row at kCols columns per lane, and the
-// tiles a wider row takes.
-void lanes_of(int width, int *lanes, int *tiles)
+// Bytes per store (16, 4 or 2) that the gradient's rows allow.
+int store_bytes(const EmbedArgs &a)
 {
-    *lanes = 1;
-    while (*lanes < 32 && *lanes * kCols < width) *lanes <<= 1;
-    *tiles = (width + *lanes * kCols - 1) / (*lanes * kCols);
+    for (int b : {16, 4}) {
+        const int e = b / (int)dtype_bytes(a.out_dtype);
+        if (a.width % e == 0 && rows_aligned(a.out, a.out_stride, a.out_dtype, e)) return b;
+    }
+    return 2;
 }
 
 struct GradLayout {
     int passes = 0, items = 1, tiles = 0, bins = 0;
+    int unit = 0;
     int64_t units = 0;
     size_t sorted[2] = {}, counts = 0, counts_later = 0, later_n = 0, part = 0, runs = 0, last = 0, bytes = 0;
 };
@@ -691,9 +749,11 @@ GradLayout layout(const EmbedArgs &a)
     const int bits = bits_of(a.vocab);  // keys 0 .. vocab
     l.passes = (bits + kMaxBits - 1) / kMaxBits;
     l.bins = 1 << ((bits + l.passes - 1) / l.passes);
-    while (l.items < kMaxItems && a.n > (int64_t)kManyTiles * kSortThreads * l.items) l.items <<= 1;
+    const int64_t tiles = a.n <= (int64_t)kSumTiles * kSortThreads * kSumItems ? kSumTiles : kManyTiles;
+    while (l.items < kMaxItems && a.n > tiles * kSortThreads * l.items) l.items <<= 1;
     l.tiles = (int)((a.n + kSortThreads * l.items - 1) / (kSortThreads * l.items));
-    l.units = (a.n + kUnit - 1) / kUnit;
+    l.unit = a.n < 32 * 8 * kSMs ? 16 : 32;  // at least 8 units per SM, where there are that many
+    l.units = (a.n + l.unit - 1) / l.unit;
     size_t at = 0;
     auto take = [&](size_t b) { const size_t p = at; at += up(b); return p; };
     for (size_t &p : l.sorted) p = take(8 * (size_t)a.n);
@@ -735,14 +795,17 @@ cudaError_t embed_grad(const EmbedArgs &a, void *tmp, uint32_t *present, cudaStr
     if (!l.passes) {
         return with_types(a, [&](auto ti, auto to, auto e) {
             constexpr int E = decltype(e)::value;
-            // up to 32 lanes of columns; as many rows as the accumulators
-            // hold, fewer when that leaves SMs without a block
-            const int lanes = std::min((a.width + E - 1) / E, 64);
-            const int tiles = (a.width + lanes * E - 1) / (lanes * E);
-            int64_t rows = std::min<int64_t>(kFewFloats / (lanes * E), a.vocab);
-            while (rows > 8 && (a.vocab + rows - 1) / rows * tiles < 4 * kSMs) rows >>= 1;
-            const dim3 grid((unsigned)((a.vocab + rows - 1) / rows), tiles);
-            k_grad_few<decltype(ti), decltype(to), E><<<grid, kFewThreads, 0, st>>>(a, (int)rows, lanes);
+            FewArgs f{};
+            for (f.lanes = 1; f.lanes < kThreads && f.lanes * E < a.width;) f.lanes <<= 1;
+            const int packs = f.lanes < kThreads ? 1 : kFewPacks;
+            f.tiles = (a.width + f.lanes * E * packs - 1) / (f.lanes * E * packs);
+            f.sums = (int)a.n * f.tiles;
+            f.store = store_bytes(a);
+            // at least 4 fill blocks per SM
+            f.rows = (int)std::min<int64_t>(kFewRows, std::max<int64_t>(1, a.vocab / (4 * kSMs)));
+            const int64_t fills = a.accumulate ? 0 : (a.vocab + f.rows - 1) / f.rows;
+            if (f.sums + fills == 0) return cudaSuccess;
+            k_grad_few<decltype(ti), decltype(to), E><<<(unsigned)(f.sums + fills), kThreads, 0, st>>>(a, f);
             ++*launches;
             return cudaGetLastError();
         });
@@ -762,10 +825,7 @@ cudaError_t embed_grad(const EmbedArgs &a, void *tmp, uint32_t *present, cudaStr
     // memory idle, and the rest beside the sums
     Fill f{};
     f.present = s.present;
-    for (f.store = 16; f.store > 2; f.store = f.store == 4 ? 2 : 4) {
-        const int e = f.store / (int)dtype_bytes(a.out_dtype);
-        if (a.width % e == 0 && rows_aligned(a.out, a.out_stride, a.out_dtype, e)) break;
-    }
+    f.store = store_bytes(a);
     auto fill_blocks = [&](int warps) {  // for the share f0 .. f1
         return (int)std::min<int64_t>(2 * kSMs, (a.vocab * (f.f1 - f.f0) / kShares + warps - 1) / warps);
     };
@@ -793,36 +853,43 @@ cudaError_t embed_grad(const EmbedArgs &a, void *tmp, uint32_t *present, cudaStr
         return cudaSuccess;
     };
     HISS_TRY(l.items == 1 ? sort(Int<1>{}) : l.items == 2 ? sort(Int<2>{}) : l.items == 4 ? sort(Int<4>{}) : sort(Int<8>{}));
-    return with_types(a, [&](auto ti, auto to, auto e) {
+    SumArgs m{};
+    m.items = s.out;
+    m.part = (float *)(p + l.part);
+    m.runs = s.runs;
+    m.last = (uint32_t *)(p + l.last);
+    m.present = s.present;
+    m.units = l.units;
+    m.unit = l.unit;
+    f.f0 = f.f1;
+    f.f1 = kShares;
+    f.blocks = s.present && f.f0 < f.f1 ? fill_blocks(kThreads / 32) : 0;
+    HISS_TRY(with_types(a, [&](auto ti, auto to, auto e) {
+        using TI = decltype(ti);
         using TO = decltype(to);
         constexpr int E = decltype(e)::value;
-        SumArgs m{};
-        m.items = s.out;
-        m.part = (float *)(p + l.part);
-        m.runs = s.runs;
-        m.last = (uint32_t *)(p + l.last);
-        m.units = l.units;
-        lanes_of(a.width, &m.lanes, &m.tiles);
-        m.present = s.present;
-        m.blocks = (int)((l.units * m.tiles * m.lanes + kThreads - 1) / kThreads);
-        f.f0 = f.f1;
-        f.f1 = kShares;
-        f.blocks = s.present && f.f0 < f.f1 ? fill_blocks(kThreads / 32) : 0;
-        using TI = decltype(ti);
-        auto sum = [&](auto full) {
-            auto kernel = k_sum<TI, TO, E, decltype(full)::value>;
-            constexpr size_t smem = sum_bytes<TI, E>();
+        auto sum = [&](auto shape) {
+            constexpr bool BIG = decltype(shape)::value;
+            using S = SumShape<TI, E, BIG>;
+            auto kernel = k_sum<TI, TO, E, BIG>;
+            for (m.lanes = BIG ? 32 : 1; m.lanes < 32 && m.lanes * S::C < a.width;) m.lanes <<= 1;
+            m.tiles = (a.width + m.lanes * S::C - 1) / (m.lanes * S::C);
+            m.blocks = (int)((l.units * m.tiles + kThreads / m.lanes - 1) / (kThreads / m.lanes));
             static std::atomic<bool> allowed{false};  // of this kernel
-            if (smem > 48 * 1024 && !allowed.load(std::memory_order_acquire)) {
-                HISS_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
+            if (!allowed.load(std::memory_order_acquire)) {
+                HISS_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 128 * 1024));
                 allowed.store(true, std::memory_order_release);
             }
-            return launch_after(kernel, m.blocks + f.blocks, kThreads, smem, st, a, m, f);
+            ++*launches;
+            return launch_after(kernel, m.blocks + f.blocks, kThreads, S::smem(m.lanes), st, a, m, f);
         };
-        HISS_TRY(m.lanes == 32 ? sum(std::true_type{}) : sum(std::false_type{}));
-        HISS_TRY(launch_after(k_join<TO, E>, kJoinBlocks, kJoinThreads, 0, st, a, m));
-        *launches += 2;
-        return cudaSuccess;
+        // big tiles where they still give 16 warps per SM
+        if (a.width > 256 && l.units * ((a.width + 511) / 512) >= 16 * kSMs) return sum(std::true_type{});
+        return sum(std::false_type{});
+    }));
+    ++*launches;
+    return with_dtype(a.out_dtype, [&](auto to) {
+        return launch_after(k_join<decltype(to)>, kJoinBlocks, kJoinThreads, 0, st, a, m);
     });
 }
 
