@@ -10,7 +10,7 @@
 //   1. the positions are sorted by token (stable LSD radix sort, up to 9 bits
 //      per pass; tokens of a vocabulary below 2^18 take two), while the SMs that the sort
 //      leaves idle write the zeros of the rows without positions;
-//   2. k_sum cuts the sorted positions into units of 16 or 32 and sums runs of equal
+//   2. k_sum cuts the sorted positions into units of 8 to 32 and sums runs of equal
 //      tokens: a run belongs to the unit it begins in, which follows it
 //      into the next unit.  A run that goes on past that one leaves a float32 partial
 //      sum per unit, so the work of a unit is bounded however often a token occurs;
@@ -98,7 +98,7 @@ struct SortArgs {
                          // tiles once scanned; then [bins] totals
     uint32_t *counts_out;  // the next digit's counts of the output's tiles (NULL: last pass)
     uint32_t *present;   // [ceil(vocab / 32)] bit: the token occurs (NULL: not wanted); 0 between calls
-    uint32_t *runs;      // number of long runs (SumArgs), set to 0 by the first kernel
+    uint32_t *runs;      // numbers of long runs (SumArgs), set to 0 by the first kernel
     uint32_t *clear;     // the later passes' counts, set to 0 by the first kernel
     int64_t clear_n;
     int tiles, shift, bits, scanned;
@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(kSortThreads) k_sort_count(EmbedArgs a, SortAr
     hist[threadIdx.x] = 0;
     if (merge)
         for (int i = threadIdx.x; i < words; i += kSortThreads) bitmap[i] = 0;
-    if (blockIdx.x == 0 && threadIdx.x == 0) *s.runs = 0;
+    if (blockIdx.x == 0 && threadIdx.x < 2) s.runs[threadIdx.x] = 0;
     for (int64_t i = (int64_t)blockIdx.x * kSortThreads + threadIdx.x; i < s.clear_n; i += (int64_t)gridDim.x * kSortThreads)
         s.clear[i] = 0;
     __syncthreads();
@@ -205,18 +205,32 @@ __global__ void __launch_bounds__(1024) k_sort_scan(SortArgs s)
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const int bins = 1 << s.bits, bin = blockIdx.x * 32 + lane;
     const int t0 = (int)((int64_t)s.tiles * w / 32), t1 = (int)((int64_t)s.tiles * (w + 1) / 32);
-    uint32_t v = 0;
+    constexpr int B = 4;  // counts held per thread: up to 128 tiles in one batch
+    uint32_t c[B], v = 0;
     if (bin < bins)
-        for (int t = t0; t < t1; ++t) v += s.counts[(int64_t)t * bins + bin];
+        for (int t = t0; t < t1; t += B) {
+#pragma unroll
+            for (int u = 0; u < B; ++u) c[u] = t + u < t1 ? s.counts[(int64_t)(t + u) * bins + bin] : 0u;
+#pragma unroll
+            for (int u = 0; u < B; ++u) v += c[u];
+        }
     sum[w][lane] = v;
     __syncthreads();
     uint32_t run = 0;
-    for (int i = 0; i < w; ++i) run += sum[i][lane];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) run += i < w ? sum[i][lane] : 0u;
     if (bin >= bins) return;
-    for (int t = t0; t < t1; ++t) {
-        const uint32_t c = s.counts[(int64_t)t * bins + bin];
-        s.counts[(int64_t)t * bins + bin] = run;
-        run += c;
+    for (int t = t0; t < t1; t += B) {
+        if (t1 - t0 > B) {
+#pragma unroll
+            for (int u = 0; u < B; ++u) c[u] = t + u < t1 ? s.counts[(int64_t)(t + u) * bins + bin] : 0u;
+        }
+#pragma unroll
+        for (int u = 0; u < B; ++u)
+            if (t + u < t1) {
+                s.counts[(int64_t)(t + u) * bins + bin] = run;
+                run += c[u];
+            }
     }
     if (w == 31) s.counts[(int64_t)s.tiles * bins + bin] = run;
     let_next_start();
@@ -254,11 +268,17 @@ __global__ void __launch_bounds__(kSortThreads) k_sort_scatter(EmbedArgs a, Sort
             before = s.counts[(int64_t)blockIdx.x * bins + bin];
             total = s.counts[(int64_t)s.tiles * bins + bin];
         } else {
-#pragma unroll 32
-            for (int t = 0; t < s.tiles; ++t) {
-                const uint32_t c = s.counts[(int64_t)t * bins + bin];
-                total += c;
-                if (t < (int)blockIdx.x) before += c;
+            // in batches: the loads of a loop of unknown length wait for one another
+            constexpr int B = 16;
+            for (int t0 = 0; t0 < s.tiles; t0 += B) {
+                uint32_t c[B];
+#pragma unroll
+                for (int u = 0; u < B; ++u) c[u] = t0 + u < s.tiles ? s.counts[(int64_t)(t0 + u) * bins + bin] : 0u;
+#pragma unroll
+                for (int u = 0; u < B; ++u) {
+                    total += c[u];
+                    if (t0 + u < (int)blockIdx.x) before += c[u];
+                }
             }
         }
     }
@@ -318,8 +338,9 @@ struct SumArgs {
     const uint2 *items;           // sorted (token, position)
     float *part;                  // [units][2][width]: sum of the long run that comes in from the unit
                                   // before, and of the long run that begins here
-    uint32_t *runs;               // [0]: number of long runs; then (key, first unit) of each
-    uint32_t *last;               // [vocab]: last unit of a long run
+    uint32_t *runs;               // [0]: number of long runs; then (key, last unit) of each, those of many
+                                  // units from the end of the list backwards, counted in [1]
+    uint32_t *first;              // [vocab]: first unit of a long run
     uint32_t *present;            // cleared at the end
     int64_t units;
     int unit;                     // positions per unit
@@ -382,6 +403,8 @@ __device__ __forceinline__ void write_part(const EmbedArgs &a, float *p, int c0,
     }
 }
 
+constexpr int kManyUnits = 16;  // a run over more units is summed by a whole block
+
 template <typename TI, typename TO, int E, bool BIG>
 __global__ void __launch_bounds__(kThreads) k_sum(EmbedArgs a, SumArgs s, Fill f)
 {
@@ -426,12 +449,12 @@ __global__ void __launch_bounds__(kThreads) k_sum(EmbedArgs a, SumArgs s, Fill f
     if (goes_out && !long_out)
         while (end < n && s.items[end].x == k1) ++end;
     while (end > i && s.items[end - 1].x >= vocab) --end;
-    if (long_out && begins && tile == 0 && lane == 0) {
-        const uint32_t at = atomicAdd(s.runs, 1u);
-        s.runs[1 + 2 * at] = k1;
-        s.runs[2 + 2 * at] = (uint32_t)unit;
+    if (long_out && begins && tile == 0 && lane == 0) s.first[k1] = (uint32_t)unit;
+    if (long_in && (next != k0 || k1 != k0) && tile == 0 && lane == 0) {
+        const bool many = key_of(i0 - kManyUnits * s.unit) == k0;
+        const uint32_t at = atomicAdd(s.runs + many, 1u);
+        *reinterpret_cast<uint2 *>(s.runs + 2 * (many ? s.units - at : 1 + at)) = make_uint2(k0, (uint32_t)unit);
     }
-    if (long_in && (next != k0 || k1 != k0) && tile == 0 && lane == 0) s.last[k0] = (uint32_t)unit;
     if (i >= end) return;
 
     const uint32_t mask = lanes == 32 ? 0xffffffffu : ((1u << lanes) - 1u) << (threadIdx.x & 31 & ~(lanes - 1));
@@ -511,12 +534,15 @@ __global__ void __launch_bounds__(kThreads) k_sum(EmbedArgs a, SumArgs s, Fill f
 }
 
 constexpr int kJoinThreads = 512;
-constexpr int kJoinCols = 64;      // columns per tile
-constexpr int kJoinBlocks = 4 * kSMs;
+constexpr int kJoinWarps = kJoinThreads / 32;
+constexpr int kJoinCols = 64;      // columns per tile of a run of many units
+constexpr int kJoinBlocks = 2 * kSMs;
 
 // The row of each long run: the second part of the unit it begins in and the
-// first parts of the units up to its last.  One block per run and tile at a
-// time: a thread per column and stretch of units, the stretches added up in order.
+// first parts of the units up to its last.  The first half of the blocks takes the
+// runs of many units, a run and tile at a time: a thread per column and stretch of
+// units, the stretches added up in order.  In the other half each warp
+// takes a run and 128 columns.
 template <typename TO>
 __global__ void __launch_bounds__(kJoinThreads) k_join(EmbedArgs a, SumArgs s)
 {
@@ -526,31 +552,70 @@ __global__ void __launch_bounds__(kJoinThreads) k_join(EmbedArgs a, SumArgs s)
     if (s.present)
         for (int64_t i = (int64_t)blockIdx.x * kJoinThreads + threadIdx.x; i < (a.vocab + 31) / 32; i += (int64_t)gridDim.x * kJoinThreads)
             s.present[i] = 0;
-    const int group = threadIdx.x / kJoinCols, lane = threadIdx.x % kJoinCols;
-    const int tiles = (a.width + kJoinCols - 1) / kJoinCols;
-    const int64_t items = (int64_t)s.runs[0] * tiles;
-    for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
-        const int64_t run = it / tiles;
-        const int c = (int)(it - run * tiles) * kJoinCols + lane;
-        const uint32_t key = s.runs[1 + 2 * run];
-        const int64_t first = s.runs[2 + 2 * run], count = (int64_t)s.last[key] - first + 1;
-        const int64_t to = first + count * (group + 1) / G;
-        float x = 0.0f;
-        if (c < a.width) {
-#pragma unroll 8
-            for (int64_t u = first + count * group / G; u < to; ++u) x += s.part[(u * 2 + (u == first)) * a.width + c];
-        }
-        sh[group][lane] = x;
-        __syncthreads();
-        if (group == 0 && c < a.width) {
+    const bool many = blockIdx.x < gridDim.x / 2;
+    const int64_t runs = s.runs[many];
+    auto record = [&](int64_t run) { return *reinterpret_cast<const uint2 *>(s.runs + 2 * (many ? s.units - run : 1 + run)); };
+    auto finish = [&](uint32_t key, int c, float x) {
+        x *= a.scale;
+        TO *p = static_cast<TO *>(a.out) + (int64_t)key * a.out_stride + c;
+        if (a.accumulate) x += to_f32(*p);
+        *p = from_f32<TO>(x);
+    };
+    constexpr int U = 8;  // parts in flight
+    if (many) {
+        const int group = threadIdx.x / kJoinCols, lane = threadIdx.x % kJoinCols;
+        const int tiles = (a.width + kJoinCols - 1) / kJoinCols;
+        for (int64_t it = blockIdx.x; it < runs * tiles; it += gridDim.x / 2) {
+            const int64_t run = it / tiles;
+            const int c = (int)(it - run * tiles) * kJoinCols + lane;
+            const uint2 r = record(run);
+            const int64_t first = s.first[r.x], count = (int64_t)r.y - first + 1;
+            const int64_t to = first + count * (group + 1) / G;
+            float x = 0.0f;
+            for (int64_t u = first + count * group / G; u < to; u += U) {
+                float v[U];
 #pragma unroll
-            for (int g = 1; g < G; ++g) x += sh[g][lane];
-            x *= a.scale;
-            TO *p = static_cast<TO *>(a.out) + (int64_t)key * a.out_stride + c;
-            if (a.accumulate) x += to_f32(*p);
-            *p = from_f32<TO>(x);
+                for (int k = 0; k < U; ++k)
+                    v[k] = u + k < to && c < a.width ? s.part[((u + k) * 2 + (u + k == first)) * a.width + c] : 0.0f;
+#pragma unroll
+                for (int k = 0; k < U; ++k) x += v[k];
+            }
+            sh[group][lane] = x;
+            __syncthreads();
+            if (group == 0 && c < a.width) {
+#pragma unroll
+                for (int g = 1; g < G; ++g) x += sh[g][lane];
+                finish(r.x, c, x);
+            }
+            __syncthreads();
         }
-        __syncthreads();
+    } else {
+        constexpr int N = 4;
+        const int lane = threadIdx.x & 31;
+        const int tiles = (a.width + 32 * N - 1) / (32 * N);
+        const int64_t warp = (int64_t)(blockIdx.x - gridDim.x / 2) * kJoinWarps + (threadIdx.x >> 5);
+        for (int64_t it = warp; it < runs * tiles; it += (int64_t)(gridDim.x - gridDim.x / 2) * kJoinWarps) {
+            const int64_t run = it / tiles;
+            const int c = (int)(it - run * tiles) * 32 * N + lane;
+            const uint2 r = record(run);
+            const int64_t first = s.first[r.x], to = (int64_t)r.y + 1;
+            float x[N] = {};
+            for (int64_t u = first; u < to; u += U) {
+                float v[U][N];
+#pragma unroll
+                for (int k = 0; k < U; ++k)
+#pragma unroll
+                    for (int q = 0; q < N; ++q)
+                        v[k][q] = u + k < to && c + 32 * q < a.width ? s.part[((u + k) * 2 + (u + k == first)) * a.width + c + 32 * q] : 0.0f;
+#pragma unroll
+                for (int k = 0; k < U; ++k)
+#pragma unroll
+                    for (int q = 0; q < N; ++q) x[q] += v[k][q];
+            }
+#pragma unroll
+            for (int q = 0; q < N; ++q)
+                if (c + 32 * q < a.width) finish(r.x, c + 32 * q, x[q]);
+        }
     }
 }
 
@@ -739,7 +804,7 @@ struct GradLayout {
     int passes = 0, items = 1, tiles = 0, bins = 0;
     int unit = 0;
     int64_t units = 0;
-    size_t sorted[2] = {}, counts = 0, counts_later = 0, later_n = 0, part = 0, runs = 0, last = 0, bytes = 0;
+    size_t sorted[2] = {}, counts = 0, counts_later = 0, later_n = 0, part = 0, runs = 0, first = 0, bytes = 0;
 };
 
 GradLayout layout(const EmbedArgs &a)
@@ -752,7 +817,11 @@ GradLayout layout(const EmbedArgs &a)
     const int64_t tiles = a.n <= (int64_t)kSumTiles * kSortThreads * kSumItems ? kSumTiles : kManyTiles;
     while (l.items < kMaxItems && a.n > tiles * kSortThreads * l.items) l.items <<= 1;
     l.tiles = (int)((a.n + kSortThreads * l.items - 1) / (kSortThreads * l.items));
-    l.unit = a.n < 32 * 8 * kSMs ? 16 : 32;  // at least 8 units per SM, where there are that many
+    // positions per unit: 32, fewer where that gives less than 16 warps per SM
+    // (a narrow row takes only some of a warp's lanes)
+    const int64_t per = std::max<int64_t>(1, (int64_t)a.width / 256 * 32 + (a.width % 256 + 7) / 8);  // lanes of a row
+    l.unit = 32;
+    while (l.unit > 8 && a.n / l.unit * per < 32 * 16 * kSMs) l.unit /= 2;
     l.units = (a.n + l.unit - 1) / l.unit;
     size_t at = 0;
     auto take = [&](size_t b) { const size_t p = at; at += up(b); return p; };
@@ -762,8 +831,8 @@ GradLayout layout(const EmbedArgs &a)
     l.later_n = counts_n * (l.passes - 1);
     l.counts_later = take(4 * l.later_n);
     l.part = take(8 * (size_t)l.units * a.width);
-    l.runs = take(8 * (size_t)l.units + 4);  // a long run begins in a unit of its own
-    l.last = take(4 * (size_t)a.vocab);
+    l.runs = take(8 * (size_t)(l.units + 1));  // a long run ends in a unit of its own
+    l.first = take(4 * (size_t)a.vocab);
     l.bytes = at;
     return l;
 }
@@ -857,7 +926,7 @@ cudaError_t embed_grad(const EmbedArgs &a, void *tmp, uint32_t *present, cudaStr
     m.items = s.out;
     m.part = (float *)(p + l.part);
     m.runs = s.runs;
-    m.last = (uint32_t *)(p + l.last);
+    m.first = (uint32_t *)(p + l.first);
     m.present = s.present;
     m.units = l.units;
     m.unit = l.unit;

@@ -10,10 +10,11 @@
 // a power of two of lanes inside a warp (narrow rows, several per warp), or
 // whole warps that meet at a named barrier once per row.  Blocks are persistent:
 // the weights (and in the backward pass each lane's column sums of dw and
-// db) stay in registers from row to row.  Each thread copies its own packs
-// of the rows to come into its own slots of a shared-memory ring
-// (cp.async), so no barrier guards the ring and the loads in flight cost no
-// registers.  Rows too wide for a group of kMaxLanes go through the looping
+// db) stay in registers from row to row.  The rows to come are copied
+// into a shared-memory ring (cp.async), so the loads in flight cost no
+// registers: each thread copies its own packs where rows are aligned to 16
+// bytes, and no barrier guards the ring; a group copies the 16-byte lines that
+// hold a row of any other alignment.  Rows too wide for a group of kMaxLanes go through the looping
 // kernels at the end of the file.
 #include <algorithm>
 #include <atomic>
@@ -110,59 +111,99 @@ constexpr int kChunks = E == 1 ? NV / 2 : NV;
 
 // ---- the rows to come -------------------------------------------------------------
 
-// S rows ahead of one operand in this thread's slots of shared memory.  Packs
-// below 4 bytes (16-bit elements of rows without 4-byte alignment) cannot be
-// copied asynchronously and are held in registers, one row ahead.
-template <typename T, int E, int NV, int S>
-struct Stream {
+// Whether rows are copied by lines (they are not aligned to 16 bytes).
+template <int E>
+constexpr bool kRaw = E <= 2;
+
+// Rows of one operand, S of them in shared memory.
+//   packed: pack v of this thread at slot v of the thread;
+//   raw:    the group's copy of the lines that hold the row, which begins at
+//           the row's offset in its first line.
+template <typename T, int E, int NV, int S, bool NARROW>
+struct Ring {
     using P = Pack<T, E>;
-    static constexpr bool kAsync = sizeof(T) * E >= 4;
-    static constexpr size_t kThreadBytes = kAsync ? sizeof(P) * NV * S : 0;
-    P *slot;
-    P cur[kAsync ? 1 : NV], next[kAsync ? 1 : NV];
+    char *base;
+    int stage;           // bytes from one row to the next
+    uintptr_t lo, hi;    // the matrix: lines that reach outside are copied by element
 
-    // base: the block's part of shared memory for this operand
-    __device__ __forceinline__ void open(char *base) { slot = reinterpret_cast<P *>(base) + threadIdx.x; }
-
-    // Start the copy of pack v of a row into stage st.
-    __device__ __forceinline__ void fetch(int st, int v, const T *p)
+    static __host__ __device__ int line_bytes(int width) { return (width * (int)sizeof(T) + 15 + 15) / 16 * 16; }
+    static size_t bytes(int threads, int lanes, int width)
     {
-        if constexpr (kAsync) {
-            copy_pack_async<T, E>(slot + (st * NV + v) * blockDim.x, p);
+        return kRaw<E> ? (size_t)(threads / lanes) * S * line_bytes(width) : (size_t)threads * S * NV * sizeof(P);
+    }
+    // at: the block's part of shared memory for this operand
+    __device__ __forceinline__ void open(char *at, const Group &g, const void *p, int64_t n, int64_t stride, int width)
+    {
+        if constexpr (kRaw<E>) {
+            stage = line_bytes(width);
+            base = at + g.id * (S * stage);
+            lo = reinterpret_cast<uintptr_t>(p);
+            hi = lo + ((n - 1) * stride + width) * sizeof(T);
         } else {
-            next[v] = load_pack<T, E>(p);
+            stage = blockDim.x * NV * (int)sizeof(P);
+            base = at + threadIdx.x * sizeof(P);
+        }
+    }
+    // Start copying a row into stage st.
+    __device__ __forceinline__ void fetch(int st, const T *row, const Group &g, int col, int vs, int width)
+    {
+        char *d = base + st * stage;
+        if constexpr (kRaw<E>) {
+            const uintptr_t b0 = reinterpret_cast<uintptr_t>(row), b1 = b0 + width * sizeof(T), line0 = b0 & ~(uintptr_t)15;
+            const int bytes = (int)(b1 - line0);
+            const char *q = reinterpret_cast<const char *>(line0);
+            if (line0 >= lo && line0 + (bytes + 15) / 16 * 16 <= hi) {
+#pragma unroll 2
+                for (int b = 16 * g.lane; b < bytes; b += 16 * g.lanes) cp_async16(d + b, q + b);
+            } else {  // the first and last rows
+                for (int b = 16 * g.lane; b < bytes; b += 16 * g.lanes) {
+                    if (line0 + b >= lo && line0 + b + 16 <= hi) {
+                        cp_async16(d + b, q + b);
+                    } else {
+                        for (uintptr_t e = max(line0 + b, b0); e < min(line0 + b + 16, b1); e += sizeof(T))
+                            *reinterpret_cast<T *>(d + (e - line0)) = *reinterpret_cast<const T *>(e);
+                    }
+                }
+            }
+        } else {
+#pragma unroll
+            for (int v = 0; v < NV; ++v)
+                if (col + v * vs < width)
+                    copy_pack_async<T, E>(reinterpret_cast<P *>(d + v * blockDim.x * sizeof(P)), row + col + v * vs);
         }
     }
     // Chunk c of the row in stage st: a pack as float32 pairs, or two packs of
     // one element as a pair, the second 0 unless the row reaches it.
-    __device__ __forceinline__ void get(int st, int c, bool second, float2 (&x)[kPairs<E>]) const
+    __device__ __forceinline__ void get(int st, const T *row, int col, int vs, int c, bool second, float2 (&x)[kPairs<E>]) const
     {
-        auto pack = [&](int v) {
-            if constexpr (kAsync) return slot[(st * NV + v) * blockDim.x];
-            else return cur[v];
-        };
+        const char *d = base + st * stage;
         if constexpr (E == 1) {
-            x[0] = make_float2(to_f32(pack(2 * c).v[0]), second ? to_f32(pack(2 * c + 1).v[0]) : 0.0f);
+            const T *v = reinterpret_cast<const T *>(d + (reinterpret_cast<uintptr_t>(row) & 15)) + col;
+            x[0] = make_float2(to_f32(v[2 * c * vs]), second ? to_f32(v[(2 * c + 1) * vs]) : 0.0f);
         } else {
-            const P p = pack(c);
+            P p;
+            if constexpr (kRaw<E>) p = load_pack<T, E>(reinterpret_cast<const T *>(d + (reinterpret_cast<uintptr_t>(row) & 15)) + col + c * vs);
+            else p = *reinterpret_cast<const P *>(d + c * blockDim.x * sizeof(P));
 #pragma unroll
             for (int h = 0; h < E / 2; ++h) x[h] = pair_of(p.v + 2 * h);
         }
     }
-    // Make the row fetched last the current one (register form).
-    __device__ __forceinline__ void turn()
-    {
-        if constexpr (!kAsync)
-#pragma unroll
-            for (int v = 0; v < NV; ++v) cur[v] = next[v];
-    }
 };
+
+// Before a raw row is read, and before the place of the row before it is
+// filled again.
+template <bool NARROW>
+__device__ __forceinline__ void group_sync(const Group &g)
+{
+    if (NARROW || g.warps == 1) __syncwarp();
+    else group_barrier(g);
+}
 
 // Rows in the ring: at most 4, so many that a block of kMaxLanes threads fits
 // with other bytes per lane beside the ring.
 constexpr int stages(size_t row_bytes, size_t other)
 {
-    const int s = (int)((kSharedBytes / kMaxLanes - other) / row_bytes);
+    const int s = (int)(((kSharedBytes - 1024) / kMaxLanes - other) / row_bytes);  // lines: up to 30 bytes more per row
     return s > 4 ? 4 : s;
 }
 
@@ -175,9 +216,10 @@ struct Rows {
 };
 
 // The widest pack that the width and every row's alignment allow; 16 elements
-// per lane, or 32 where that is too few and the caller has such a kernel; as
-// many groups per block as reach the given threads without leaving SMs idle.
-Rows plan_rows(const NormArgs &a, bool has32, int threads)
+// per lane, or 32 where that is too few and the caller has such a kernel for
+// the pack; as many groups per block as reach the given threads without leaving
+// SMs idle.
+Rows plan_rows(const NormArgs &a, bool has32, bool has32_wide, int threads)
 {
     const bool half = a.x_dtype != HISS_F32;
     auto fits = [&](int e) {
@@ -193,7 +235,8 @@ Rows plan_rows(const NormArgs &a, bool has32, int threads)
     Rows r;
     const int e = fits(wide) ? wide : half && fits(2) ? 2 : 1;
     int per = 16;
-    if (has32 && e == wide && (a.width > per * kMaxLanes || (half && a.width >= 1024))) per = 32;
+    const bool can = e == wide ? has32_wide : has32;
+    if (can && (a.width > per * kMaxLanes || (half && a.width > 512))) per = 32;
     const int lanes = (a.width + per - 1) / per;
     if (lanes > kMaxLanes) return r;
     r.e = e;
@@ -207,12 +250,17 @@ Rows plan_rows(const NormArgs &a, bool has32, int threads)
         r.lanes = (lanes + 31) & ~31;
         r.groups = 1;
     }
-    while (2 * r.groups * r.lanes <= threads && (int64_t)r.groups * kSMs < a.n) r.groups <<= 1;
+    // a raw row takes up to 30 bytes more than its elements, which counts for very narrow ones
+    const size_t row = 4 * (a.width * (dtype_bytes(a.x_dtype) + (a.dy ? dtype_bytes(a.y_dtype) : 0)) + 60);
+    while (2 * r.groups * r.lanes <= threads && (int64_t)r.groups * kSMs < a.n &&
+           (!r.narrow || 2 * r.groups * row <= kSharedBytes))
+        r.groups <<= 1;
     return r;
 }
 
-// Resident blocks per SM of a kernel at a block size and its shared memory,
-// asked for once (and the kernel is allowed that much shared memory).
+// Resident blocks per SM of a kernel: those that its registers allow at a block
+// size, asked for once (and the kernel is allowed its shared memory), and those
+// that its shared memory leaves.
 struct Residency {
     std::atomic<int> blocks[kMaxWarps + 1];
 };
@@ -223,44 +271,50 @@ int resident(K kernel, int threads, size_t smem, Residency &cache)
     int v = c.load(std::memory_order_acquire);
     if (v == 0) {
         if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSharedBytes) != cudaSuccess ||
-            cudaOccupancyMaxActiveBlocksPerMultiprocessor(&v, kernel, threads, smem) != cudaSuccess || v < 1)
+            cudaOccupancyMaxActiveBlocksPerMultiprocessor(&v, kernel, threads, 0) != cudaSuccess || v < 1)
             v = 1;
         c.store(v, std::memory_order_release);
     }
-    return v;
+    const int fit = (int)(227 * 1024 / (smem + sizeof(Exchange) * kMaxWarps + 1024));  // 1 KB per block is the system's
+    return std::max(1, std::min(v, fit));
 }
 
 // ---- parameters -----------------------------------------------------------------
 
 // The weights (or biases) of a lane's columns, as float32 pairs, for every row
-// the block takes: in registers, or with four packs of 8 elements in shared
-// memory (one copy per block, 16-byte accesses without bank conflicts): 64
-// registers of them would halve the warps per SM.
+// the block takes: in registers, or with 32 16-bit elements per lane in shared
+// memory (one copy per block, accesses without bank conflicts): 64 registers of
+// them would halve the warps per SM.
 template <bool NARROW, int E, int NV>
 struct Params {
-    static constexpr bool kShared = E == 8 && NV == 4;
+    static constexpr bool kShared = E * NV == 32 && E != 4;
     static constexpr size_t kLaneBytes = kShared ? 4 * E * NV : 0;  // of shared memory
     float2 held[kShared ? 1 : kChunks<E, NV>][kPairs<E>];
-    float4 *sh;
+    char *sh;
     int lanes;
 
     // Called by every thread; the block synchronises before the first get.
     __device__ __forceinline__ void open(const Group &g, const void *p, int dtype, float none, int col, int vs, int width,
                                          char *base)
     {
-        sh = reinterpret_cast<float4 *>(base) + g.lane;
+        sh = base + g.lane * (E == 8 ? 16 : 8);
         lanes = g.lanes;
+        float first = none;  // E = 1: of a chunk's two elements
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
             float t[E];
 #pragma unroll
             for (int e = 0; e < E; ++e) t[e] = none;
             if (p && col + v * vs < width) load_params<E>(p, dtype, col + v * vs, t);
-            if constexpr (kShared) {
+            if constexpr (kShared && E == 8) {
                 if (g.id == 0)
 #pragma unroll
                     for (int e = 0; e < E; e += 4)
-                        sh[(v * (E / 4) + e / 4) * lanes] = make_float4(t[e], t[e + 1], t[e + 2], t[e + 3]);
+                        *reinterpret_cast<float4 *>(sh + 16 * (v * 2 + e / 4) * lanes) = make_float4(t[e], t[e + 1], t[e + 2], t[e + 3]);
+            } else if constexpr (kShared) {
+                if (E == 2 && g.id == 0) *reinterpret_cast<float2 *>(sh + 8 * v * lanes) = make_float2(t[0], t[E - 1]);
+                if (E == 1 && (v & 1) && g.id == 0) *reinterpret_cast<float2 *>(sh + 8 * (v / 2) * lanes) = make_float2(first, t[0]);
+                first = t[0];
             } else if constexpr (E == 1) {
                 if (v & 1) held[v / 2][0].y = t[0];
                 else held[v / 2][0].x = t[0];
@@ -272,13 +326,15 @@ struct Params {
     }
     __device__ __forceinline__ void get(int c, float2 (&t)[kPairs<E>]) const
     {
-        if constexpr (kShared) {
+        if constexpr (kShared && E == 8) {
 #pragma unroll
-            for (int q = 0; q < E / 4; ++q) {
-                const float4 f = sh[(c * (E / 4) + q) * lanes];
+            for (int q = 0; q < 2; ++q) {
+                const float4 f = *reinterpret_cast<const float4 *>(sh + 16 * (c * 2 + q) * lanes);
                 t[2 * q] = make_float2(f.x, f.y);
                 t[2 * q + 1] = make_float2(f.z, f.w);
             }
+        } else if constexpr (kShared) {
+            t[0] = *reinterpret_cast<const float2 *>(sh + 8 * c * lanes);
         } else {
 #pragma unroll
             for (int h = 0; h < kPairs<E>; ++h) t[h] = held[c][h];
@@ -303,19 +359,19 @@ __device__ __forceinline__ void store_chunk(T *p, int c, int vs, bool second, co
 
 // ---- forward --------------------------------------------------------------------
 
-template <typename TX, int E, int NV>
+template <typename TX, int E, int NV, bool NARROW>
 struct Forward {
-    static constexpr size_t kParamBytes = 2 * Params<false, E, NV>::kLaneBytes;
+    static constexpr size_t kParamBytes = 2 * Params<NARROW, E, NV>::kLaneBytes;
     static constexpr int kStages = stages(sizeof(TX) * E * NV, kParamBytes);
     static_assert(kStages >= 2, "a row ahead");
-    using X = Stream<TX, E, NV, kStages>;
-    static size_t smem(int threads, int lanes) { return X::kThreadBytes * threads + kParamBytes * lanes; }
+    using X = Ring<TX, E, NV, kStages, NARROW>;
+    static size_t smem(int threads, int lanes, int width) { return X::bytes(threads, lanes, width) + kParamBytes * lanes; }
 };
 
 template <typename TX, typename TY, int E, int NV, bool NARROW>
 __global__ void __launch_bounds__(kMaxLanes) k_norm(NormArgs a, int lanes, int groups)
 {
-    using F = Forward<TX, E, NV>;
+    using F = Forward<TX, E, NV, NARROW>;
     using PA = Params<NARROW, E, NV>;
     constexpr int S = F::kStages, C = NV * E, H = kPairs<E>, NC = kChunks<E, NV>;
     extern __shared__ __align__(16) char ring[];
@@ -323,32 +379,28 @@ __global__ void __launch_bounds__(kMaxLanes) k_norm(NormArgs a, int lanes, int g
     const Group g = group_of<NARROW>(lanes);
     const int col = column_of<NARROW, E, NV>(g);
     const int vs = E * (NARROW ? lanes : 32);
-    // the row reaches chunk c, and (packs of one element) its second half
+    // the row reaches chunk c of this lane, (packs of one element) its second
+    // half, and chunk c of any lane of the warp; full: every chunk of every lane
     auto has = [&](int c) { return col + (E == 1 ? 2 * c : c) * vs < a.width; };
     auto has_second = [&](int c) { return E > 1 || col + (2 * c + 1) * vs < a.width; };
+    const int warp_col = NARROW ? 0 : g.warp * 32 * NV * E;
+    auto any = [&](int c) { return warp_col + (E == 1 ? 2 * c : c) * vs < a.width; };
+    const bool full = warp_col + NV * vs <= a.width;
     const int64_t step = (int64_t)gridDim.x * groups;
     int64_t row = (int64_t)blockIdx.x * groups + g.id;
     // the loop runs for whole warps: as long as the warp's first row exists
     int64_t first = row - (NARROW ? (threadIdx.x & 31) / lanes : 0);
     typename F::X xs;
-    xs.open(ring);
+    char *params = ring;  // first: their accesses need the alignment
+    xs.open(ring + F::kParamBytes * lanes, g, a.x, a.n, a.x_stride, a.width);
+    const TX *x0 = static_cast<const TX *>(a.x);
     auto fetch = [&](int st, int64_t r) {
-        if (r < a.n) {
-            const TX *p = static_cast<const TX *>(a.x) + r * a.x_stride + col;
-#pragma unroll
-            for (int v = 0; v < NV; ++v)
-                if (col + v * vs < a.width) xs.fetch(st, v, p + v * vs);
-        }
+        if (r < a.n) xs.fetch(st, x0 + r * a.x_stride, g, col, vs, a.width);
         cp_async_commit();
     };
-    if constexpr (F::X::kAsync) {
 #pragma unroll
-        for (int i = 0; i < S - 1; ++i) fetch(i, row + i * step);
-    } else {
-        fetch(0, row);
-    }
+    for (int i = 0; i < S - 1; ++i) fetch(i, row + i * step);
     PA w, b;
-    char *params = ring + F::X::kThreadBytes * blockDim.x;
     w.open(g, a.weight, a.p_dtype, 1.0f, col, vs, a.width, params);
     b.open(g, a.bias, a.p_dtype, 0.0f, col, vs, a.width, params + PA::kLaneBytes * lanes);
     if constexpr (PA::kShared) __syncthreads();
@@ -358,36 +410,46 @@ __global__ void __launch_bounds__(kMaxLanes) k_norm(NormArgs a, int lanes, int g
     const float my_n = NARROW ? (float)a.width : columns(g.warp), inv_my_n = my_n > 0.0f ? 1.0f / my_n : 0.0f;
     const float lane_n = NARROW ? 0.0f : columns(threadIdx.x & 31);
     int st = 0;
-    for (int parity = 0; first < a.n; first += step, row += step, parity ^= 1) {
-        if constexpr (F::X::kAsync) {
-            fetch(st == 0 ? S - 1 : st - 1, row + (S - 1) * step);
-            cp_async_wait<S - 1>();
+    int parity = 0;
+    // one row; FULL: no column to be left out
+    auto body = [&](auto is_full) {
+        constexpr bool FULL = decltype(is_full)::value;
+        const int before = st == 0 ? S - 1 : st - 1;
+        const TX *x_row = x0 + row * a.x_stride;
+        if constexpr (kRaw<E>) {
+            cp_async_wait<S - 2>();
+            group_sync<NARROW>(g);
+            fetch(before, row + (S - 1) * step);
         } else {
-            xs.turn();
-            fetch(0, row + step);
+            fetch(before, row + (S - 1) * step);
+            cp_async_wait<S - 1>();
         }
         float2 x[NC][H];
         float2 s2 = both(0.0f);
 #pragma unroll
-        for (int c = 0; c < NC; ++c)
-            if (has(c)) {
-                xs.get(st, c, has_second(c), x[c]);
+        for (int c = 0; c < NC; ++c) {
+            if (!FULL && !any(c)) break;
+            if (FULL || has(c)) {
+                xs.get(st, x_row, col, vs, c, FULL || has_second(c), x[c]);
 #pragma unroll
                 for (int h = 0; h < H; ++h) s2 = __fadd2_rn(s2, x[c][h]);
             }
+        }
         // mean and sum of squared differences of the warp's columns, then of the
         // row from those of its warps: M2 = sum of (M2_w + n_w (m_w - m)^2)
         float mean = warp_sum<NARROW>(g, s2.x + s2.y) * inv_my_n;
         float2 q2 = both(0.0f);
 #pragma unroll
-        for (int c = 0; c < NC; ++c)
-            if (has(c))
+        for (int c = 0; c < NC; ++c) {
+            if (!FULL && !any(c)) break;
+            if (FULL || has(c))
 #pragma unroll
                 for (int h = 0; h < H; ++h) {
                     float2 d = __fadd2_rn(x[c][h], both(-mean));
-                    if (!has_second(c)) d.y = 0.0f;
+                    if (!FULL && !has_second(c)) d.y = 0.0f;
                     q2 = __ffma2_rn(d, d, q2);
                 }
+        }
         float q = warp_sum<NARROW>(g, q2.x + q2.y);
         if (!NARROW && g.warps > 1) {
             float2 *slot = ex[g.id].slot[parity];
@@ -403,14 +465,15 @@ __global__ void __launch_bounds__(kMaxLanes) k_norm(NormArgs a, int lanes, int g
             TY *y = static_cast<TY *>(a.y) + row * a.y_stride + col;
 #pragma unroll
             for (int c = 0; c < NC; ++c) {
-                if (!has(c)) continue;
+                if (!FULL && !any(c)) break;
+                if (!FULL && !has(c)) continue;
                 float2 tw[H], tb[H], r[H];
                 w.get(c, tw);
                 b.get(c, tb);
 #pragma unroll
                 for (int h = 0; h < H; ++h)
                     r[h] = __ffma2_rn(__fmul2_rn(__fadd2_rn(x[c][h], both(-mean)), both(rstd)), tw[h], tb[h]);
-                store_chunk<TY, E>(y, c, vs, has_second(c), r);
+                store_chunk<TY, E>(y, c, vs, FULL || has_second(c), r);
             }
             if (g.lane == 0) {
                 if (a.mean) a.mean[row] = mean;
@@ -418,33 +481,42 @@ __global__ void __launch_bounds__(kMaxLanes) k_norm(NormArgs a, int lanes, int g
             }
         }
         st = st == S - 1 ? 0 : st + 1;
-    }
+        parity ^= 1;
+    };
+    // a body of its own for full warps where the checks cost most: one per
+    // element, or 32 elements (65,536 x 4096 bfloat16 204 -> 176 us, 47,397 x 2569
+    // float16 249 -> 177); with four packs of four float32 it costs 7%
+    constexpr bool kTwo = kRaw<E> || C == 32;
+    if (kTwo && full)
+        for (; first < a.n; first += step, row += step) body(std::integral_constant<bool, kTwo>{});
+    else
+        for (; first < a.n; first += step, row += step) body(std::false_type{});
 }
 
 // ---- backward -------------------------------------------------------------------
 
-template <typename TX, typename TY, int E, int NV>
+template <typename TX, typename TY, int E, int NV, bool NARROW>
 struct Backward {
-    static constexpr size_t kParamBytes = Params<false, E, NV>::kLaneBytes;
+    static constexpr size_t kParamBytes = Params<NARROW, E, NV>::kLaneBytes;
     static constexpr int kStages = stages((sizeof(TX) + sizeof(TY)) * E * NV, kParamBytes);
     static_assert(kStages >= 2, "a row ahead");
-    using X = Stream<TX, E, NV, kStages>;
-    using Y = Stream<TY, E, NV, kStages>;
-    static constexpr size_t kThreadBytes = X::kThreadBytes + Y::kThreadBytes;
-    // the ring and the weights; the ring's memory holds the column sums of half of the
-    // block's threads at the end
-    static size_t smem(int threads, int lanes, bool many)
+    using X = Ring<TX, E, NV, kStages, NARROW>;
+    using Y = Ring<TY, E, NV, kStages, NARROW>;
+    // the rings and the weights; their memory holds the column sums of half of
+    // the block's threads at the end
+    static size_t smem(int threads, int lanes, int width, bool many)
     {
-        return std::max(kThreadBytes * threads + kParamBytes * lanes, many ? 4 * (size_t)threads * E * NV : 0);
+        return std::max(X::bytes(threads, lanes, width) + Y::bytes(threads, lanes, width) + kParamBytes * lanes,
+                        many ? 4 * (size_t)threads * E * NV : 0);
     }
 };
 
 // Each block leaves its column sums in part[block][0 .. width) (dw) and
-// [width .. 2 width) (db): k_norm_param adds the blocks up.
+// [width .. 2 width) (db): k_norm_param adds the blocks up.  x_bytes: of x's ring.
 template <typename TX, typename TY, int E, int NV, bool NARROW>
-__global__ void __launch_bounds__(kMaxLanes) k_norm_grad(NormArgs a, int lanes, int groups, float *part)
+__global__ void __launch_bounds__(kMaxLanes) k_norm_grad(NormArgs a, int lanes, int groups, int x_bytes, float *part)
 {
-    using B = Backward<TX, TY, E, NV>;
+    using B = Backward<TX, TY, E, NV, NARROW>;
     using PA = Params<NARROW, E, NV>;
     constexpr int S = B::kStages, H = kPairs<E>, NC = kChunks<E, NV>;
     extern __shared__ __align__(16) char ring[];
@@ -452,37 +524,33 @@ __global__ void __launch_bounds__(kMaxLanes) k_norm_grad(NormArgs a, int lanes, 
     const Group g = group_of<NARROW>(lanes);
     const int col = column_of<NARROW, E, NV>(g);
     const int vs = E * (NARROW ? lanes : 32);
-    // the row reaches chunk c, and (packs of one element) its second half
+    // the row reaches chunk c of this lane, (packs of one element) its second
+    // half, and chunk c of any lane of the warp; full: every chunk of every lane
     auto has = [&](int c) { return col + (E == 1 ? 2 * c : c) * vs < a.width; };
     auto has_second = [&](int c) { return E > 1 || col + (2 * c + 1) * vs < a.width; };
+    const int warp_col = NARROW ? 0 : g.warp * 32 * NV * E;
+    auto any = [&](int c) { return warp_col + (E == 1 ? 2 * c : c) * vs < a.width; };
+    const bool full = warp_col + NV * vs <= a.width;
     const int64_t step = (int64_t)gridDim.x * groups;
     int64_t row = (int64_t)blockIdx.x * groups + g.id;
     int64_t first = row - (NARROW ? (threadIdx.x & 31) / lanes : 0);
     typename B::X xs;
     typename B::Y ys;
-    xs.open(ring);
-    ys.open(ring + B::X::kThreadBytes * blockDim.x);
+    xs.open(ring + B::kParamBytes * lanes, g, a.x, a.n, a.x_stride, a.width);
+    ys.open(ring + B::kParamBytes * lanes + x_bytes, g, a.dy, a.n, a.y_stride, a.width);
+    const TX *x0 = static_cast<const TX *>(a.x);
+    const TY *y0 = static_cast<const TY *>(a.dy);
     auto fetch = [&](int st, int64_t r) {
         if (r < a.n) {
-            const TX *p = static_cast<const TX *>(a.x) + r * a.x_stride + col;
-            const TY *q = static_cast<const TY *>(a.dy) + r * a.y_stride + col;
-#pragma unroll
-            for (int v = 0; v < NV; ++v)
-                if (col + v * vs < a.width) {
-                    xs.fetch(st, v, p + v * vs);
-                    ys.fetch(st, v, q + v * vs);
-                }
+            xs.fetch(st, x0 + r * a.x_stride, g, col, vs, a.width);
+            ys.fetch(st, y0 + r * a.y_stride, g, col, vs, a.width);
         }
         cp_async_commit();
     };
-    // a pair of operands of which only one can be copied asynchronously
-    // (16-bit x, float32 dy, odd rows) moves in step: one row ahead
-    constexpr bool kAhead = B::X::kAsync && B::Y::kAsync;
-    constexpr int A = kAhead ? S - 1 : 1;  // rows fetched before the loop
 #pragma unroll
-    for (int i = 0; i < A; ++i) fetch(i, row + i * step);
+    for (int i = 0; i < S - 1; ++i) fetch(i, row + i * step);
     PA w;
-    w.open(g, a.weight, a.p_dtype, 1.0f, col, vs, a.width, ring + B::kThreadBytes * blockDim.x);
+    w.open(g, a.weight, a.p_dtype, 1.0f, col, vs, a.width, ring);
     if constexpr (PA::kShared) __syncthreads();
     float2 dw[NC][H], db[NC][H];
 #pragma unroll
@@ -492,15 +560,19 @@ __global__ void __launch_bounds__(kMaxLanes) k_norm_grad(NormArgs a, int lanes, 
     const float inv_width = 1.0f / (float)a.width;
     float mean_n = row < a.n ? a.mean[row] : 0.0f, rstd_n = row < a.n ? a.rstd[row] : 0.0f;
     int st = 0;
-    for (int parity = 0; first < a.n; first += step, row += step, parity ^= 1) {
-        if constexpr (kAhead) {
-            fetch(st == 0 ? S - 1 : st - 1, row + (S - 1) * step);
-            cp_async_wait<S - 1>();
+    int parity = 0;
+    auto body = [&](auto is_full) {
+        constexpr bool FULL = decltype(is_full)::value;
+        const int before = st == 0 ? S - 1 : st - 1;
+        const TX *x_row = x0 + row * a.x_stride;
+        const TY *y_row = y0 + row * a.y_stride;
+        if constexpr (kRaw<E>) {
+            cp_async_wait<S - 2>();
+            group_sync<NARROW>(g);
+            fetch(before, row + (S - 1) * step);
         } else {
-            xs.turn();
-            ys.turn();
-            fetch(st ^ 1, row + step);
-            cp_async_wait<1>();
+            fetch(before, row + (S - 1) * step);
+            cp_async_wait<S - 1>();
         }
         const float mean = mean_n, rstd = rstd_n;
         if (row + step < a.n) {
@@ -511,15 +583,16 @@ __global__ void __launch_bounds__(kMaxLanes) k_norm_grad(NormArgs a, int lanes, 
         if (row < a.n) {
 #pragma unroll
             for (int c = 0; c < NC; ++c) {
-                if (!has(c)) continue;
+                if (!FULL && !any(c)) break;
+                if (!FULL && !has(c)) continue;
                 float2 x[H], d[H], t[H];
-                xs.get(st, c, has_second(c), x);
-                ys.get(st, c, has_second(c), d);
+                xs.get(st, x_row, col, vs, c, FULL || has_second(c), x);
+                ys.get(st, y_row, col, vs, c, FULL || has_second(c), d);
                 w.get(c, t);
 #pragma unroll
                 for (int h = 0; h < H; ++h) {
                     float2 n = __fmul2_rn(__fadd2_rn(x[h], both(-mean)), both(rstd));
-                    if (!has_second(c)) n.y = 0.0f;  // dy is 0 there
+                    if (!FULL && !has_second(c)) n.y = 0.0f;  // dy is 0 there
                     const float2 gr = __fmul2_rn(d[h], t[h]);
                     db[c][h] = __fadd2_rn(db[c][h], d[h]);
                     dw[c][h] = __ffma2_rn(d[h], n, dw[c][h]);
@@ -544,25 +617,31 @@ __global__ void __launch_bounds__(kMaxLanes) k_norm_grad(NormArgs a, int lanes, 
                 TX *dx = static_cast<TX *>(a.dx) + row * a.dx_stride + col;
 #pragma unroll
                 for (int c = 0; c < NC; ++c) {
-                    if (!has(c)) continue;
+                    if (!FULL && !any(c)) break;
+                    if (!FULL && !has(c)) continue;
                     // read and computed again: holding h and g from above would
                     // take 2 registers per element
                     float2 x[H], d[H], t[H], r[H];
-                    xs.get(st, c, has_second(c), x);
-                    ys.get(st, c, has_second(c), d);
+                    xs.get(st, x_row, col, vs, c, FULL || has_second(c), x);
+                    ys.get(st, y_row, col, vs, c, FULL || has_second(c), d);
                     w.get(c, t);
 #pragma unroll
                     for (int h = 0; h < H; ++h) {
                         const float2 n = __fmul2_rn(__fadd2_rn(x[h], both(-mean)), both(rstd));
                         r[h] = __ffma2_rn(__fmul2_rn(d[h], t[h]), both(rstd), __ffma2_rn(n, mgh, mg));
                     }
-                    store_chunk<TX, E>(dx, c, vs, has_second(c), r);
+                    store_chunk<TX, E>(dx, c, vs, FULL || has_second(c), r);
                 }
             }
         }
-        if constexpr (kAhead) st = st == S - 1 ? 0 : st + 1;
-        else st ^= 1;
-    }
+        st = st == S - 1 ? 0 : st + 1;
+        parity ^= 1;
+    };
+    // with packs the checks cost less than the registers of a second body
+    if (kRaw<E> && full)
+        for (; first < a.n; first += step, row += step) body(std::integral_constant<bool, kRaw<E>>{});
+    else
+        for (; first < a.n; first += step, row += step) body(std::false_type{});
     if (!part) return;
     // the block's column sums: over the groups of a warp, then over the warps (or
     // groups of warps) in a fixed tree, through the ring's memory
@@ -737,13 +816,13 @@ template <int V>
 using Int = std::integral_constant<int, V>;
 
 // f(E, NV, NARROW) for the packs of r.
-template <typename TX, bool HAS32, typename F>
+template <typename TX, bool HAS32, bool HAS32_WIDE, typename F>
 cudaError_t with_packs(const Rows &r, F &&f)
 {
     constexpr int W = 16 / (int)sizeof(TX);
     auto with_width = [&](auto e) {
         constexpr int E = decltype(e)::value;
-        if constexpr (HAS32 && E == W)
+        if constexpr (E == W ? HAS32_WIDE : HAS32)
             if (r.e * r.nv == 32) return f(e, Int<32 / E>{}, std::false_type{});
         if (r.narrow) return f(e, Int<16 / E>{}, std::true_type{});
         return f(e, Int<16 / E>{}, std::false_type{});
@@ -760,11 +839,11 @@ unsigned grid_for(const NormArgs &a, const Rows &r, int per_sm)
     return (unsigned)(want < (int64_t)kSMs * per_sm ? want : (int64_t)kSMs * per_sm);
 }
 
-Rows plan_forward(const NormArgs &a) { return plan_rows(a, true, 256); }
+Rows plan_forward(const NormArgs &a) { return plan_rows(a, a.x_dtype != HISS_F32, true, 256); }
 
 // 32 elements per lane with a float32 operand would not leave room for two
 // rows in the ring.
-Rows plan_backward(const NormArgs &a) { return plan_rows(a, a.y_dtype != HISS_F32, kMaxLanes); }
+Rows plan_backward(const NormArgs &a) { return plan_rows(a, a.y_dtype != HISS_F32, a.y_dtype != HISS_F32, kMaxLanes); }
 
 // Blocks (and parts) of the backward pass: one per SM, so that there are few
 // parts to add up.
@@ -783,13 +862,13 @@ cudaError_t layer_norm(const NormArgs &a, cudaStream_t s, int64_t *launches)
             k_norm_loop<TX, TY><<<(unsigned)a.n, kLoopThreads, 0, s>>>(a);
             return cudaGetLastError();
         }
-        return with_packs<TX, true>(r, [&](auto e, auto nv, auto narrow) {
+        return with_packs<TX, sizeof(TX) == 2, true>(r, [&](auto e, auto nv, auto narrow) {
             constexpr int E = decltype(e)::value, NV = decltype(nv)::value;
             constexpr bool NARROW = decltype(narrow)::value;
             static Residency cache;
             auto kernel = k_norm<TX, TY, E, NV, NARROW>;
             const int threads = r.lanes * r.groups;
-            const size_t smem = Forward<TX, E, NV>::smem(threads, r.lanes);
+            const size_t smem = Forward<TX, E, NV, NARROW>::smem(threads, r.lanes, a.width);
             const unsigned grid = grid_for(a, r, resident(kernel, threads, smem, cache));
             kernel<<<grid, threads, smem, s>>>(a, r.lanes, r.groups);
             return cudaGetLastError();
@@ -826,16 +905,17 @@ cudaError_t layer_norm_grad(const NormArgs &a, void *tmp, cudaStream_t s, int64_
                 }
                 return cudaGetLastError();
             }
-            return with_packs<TX, sizeof(TY) == 2>(r, [&](auto e, auto nv, auto narrow) {
+            return with_packs<TX, sizeof(TY) == 2, sizeof(TY) == 2>(r, [&](auto e, auto nv, auto narrow) {
                 constexpr int E = decltype(e)::value, NV = decltype(nv)::value;
                 static Residency cache;
                 auto kernel = k_norm_grad<TX, TY, E, NV, decltype(narrow)::value>;
                 const int threads = r.lanes * r.groups;
                 const bool many = threads > (r.narrow ? 32 : r.lanes);  // sums of several warps or groups to add up
-                const size_t smem = Backward<TX, TY, E, NV>::smem(threads, r.lanes, many);
+                using B = Backward<TX, TY, E, NV, decltype(narrow)::value>;
+                const size_t smem = B::smem(threads, r.lanes, a.width, many);
                 resident(kernel, threads, smem, cache);
                 parts = grad_grid(a, r);
-                kernel<<<parts, threads, smem, s>>>(a, r.lanes, r.groups, part);
+                kernel<<<parts, threads, smem, s>>>(a, r.lanes, r.groups, (int)B::X::bytes(threads, r.lanes, a.width), part);
                 ++*launches;
                 return cudaGetLastError();
             });
