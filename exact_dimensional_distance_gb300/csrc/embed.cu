@@ -403,7 +403,7 @@ __device__ __forceinline__ void write_part(const EmbedArgs &a, float *p, int c0,
     }
 }
 
-constexpr int kManyUnits = 16;  // a run over more units is summed by a whole block
+constexpr int kManyUnits = 64;  // a run over more units is summed by a whole block
 
 template <typename TI, typename TO, int E, bool BIG>
 __global__ void __launch_bounds__(kThreads) k_sum(EmbedArgs a, SumArgs s, Fill f)
@@ -461,20 +461,31 @@ __global__ void __launch_bounds__(kThreads) k_sum(EmbedArgs a, SumArgs s, Fill f
     const int row_bytes = S::row_bytes(lanes);
     char *group_ring = ring + (threadIdx.x / lanes) * (A * row_bytes);
     const TI *rows = static_cast<const TI *>(a.rows) + t0;
-    // lines that reach outside the matrix are copied by element
+    // lines that reach outside the matrix are copied by element: they belong to
+    // the first and last rows
     const uintptr_t lo = reinterpret_cast<uintptr_t>(a.rows), hi = lo + ((a.n - 1) * a.rows_stride + a.width) * sizeof(TI);
+    const uint32_t edge = a.rows_stride > 0 ? (uint32_t)((15 + a.rows_stride) / a.rows_stride) : 0x7fffffffu;
+    const uint32_t rows_at = (uint32_t)reinterpret_cast<uintptr_t>(rows), rows_by = (uint32_t)a.rows_stride * (uint32_t)sizeof(TI);
     auto fetch = [&](int j) {
         if (j < end) {
-            const TI *p = rows + (int64_t)s.items[j].y * a.rows_stride;
+            const uint32_t y = s.items[j].y;
+            const TI *p = rows + (int64_t)y * a.rows_stride;
             char *d = group_ring + (j & (A - 1)) * row_bytes;
             if constexpr (RAW) {
-                const uintptr_t b0 = reinterpret_cast<uintptr_t>(p), b1 = b0 + cols * sizeof(TI), line0 = b0 & ~(uintptr_t)15;
-                for (uintptr_t b = line0 + 16 * lane; b < b1; b += 16 * lanes) {
-                    if (b >= lo && b + 16 <= hi) {
-                        cp_async16(d + (b - line0), reinterpret_cast<const void *>(b));
-                    } else {
-                        for (uintptr_t e = max(b, b0); e < min(b + 16, b1); e += sizeof(TI))
-                            *reinterpret_cast<TI *>(d + (e - line0)) = *reinterpret_cast<const TI *>(e);
+                const int off = (int)((rows_at + y * rows_by) & 15), bytes = off + cols * (int)sizeof(TI);
+                const char *q = reinterpret_cast<const char *>(p) - off;
+                if (y >= edge && y + edge < (uint32_t)n) {
+#pragma unroll 2
+                    for (int b = 16 * lane; b < bytes; b += 16 * lanes) cp_async16(d + b, q + b);
+                } else {
+                    const uintptr_t b0 = reinterpret_cast<uintptr_t>(p), b1 = b0 + cols * sizeof(TI), line0 = b0 - off;
+                    for (int b = 16 * lane; b < bytes; b += 16 * lanes) {
+                        if (line0 + b >= lo && line0 + b + 16 <= hi) {
+                            cp_async16(d + b, q + b);
+                        } else {
+                            for (uintptr_t e = max(line0 + b, b0); e < min(line0 + b + 16, b1); e += sizeof(TI))
+                                *reinterpret_cast<TI *>(d + (e - line0)) = *reinterpret_cast<const TI *>(e);
+                        }
                     }
                 }
             } else {
@@ -502,7 +513,7 @@ __global__ void __launch_bounds__(kThreads) k_sum(EmbedArgs a, SumArgs s, Fill f
         if (RAW) __syncwarp(mask);
         fetch(i + A - 1);
         const char *d = group_ring + (i & (A - 1)) * row_bytes;
-        if constexpr (RAW) d += reinterpret_cast<uintptr_t>(rows + (int64_t)it.y * a.rows_stride) & 15;
+        if constexpr (RAW) d += (rows_at + it.y * rows_by) & 15;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             if (k * lanes * E >= cols) break;
