@@ -206,6 +206,13 @@ def _matrix(t, name):
     return t, n, d, row if n > 1 else d
 
 
+def _vector(t, width):
+    """The address of a contiguous vector of width entries."""
+    if t.shape != (width,) or not t.is_contiguous():
+        raise ValueError("weight and bias: contiguous vectors of %d entries expected" % width)
+    return t.data_ptr()
+
+
 def _out_matrix(t, name):
     """As _matrix without a copy (t is written)."""
     m = t
@@ -259,7 +266,7 @@ class Gradients:
         for a, b in zip(spans, spans[1:]):
             if b[0] < a[1]:
                 raise ValueError("the tensors overlap")
-        self.grads, self.out = grads, out
+        self.grads, self.out, self.all = grads, out, [t for t in grads + out if t.numel()]
 
     @staticmethod
     def _dense(t):
@@ -288,6 +295,7 @@ class Join:
         self._raw = self.stream.cuda_stream
         # the same value without building a Stream object, where torch has it
         self._current = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)
+        self._scalar = None  # a model of clip_grads' result
         h = _p()
         _check(hiss_create(ctypes.byref(h), _p(self.stream.cuda_stream)), None, "hiss_create")
         self._h = h
@@ -529,12 +537,10 @@ class Join:
     # its later work waits for the call.
 
     def _enqueue(self, fn, args, what, tensors):
-        for t in tensors:
-            if t is not None and t.get_device() != self._index:
-                raise ValueError("%s: CUDA tensors on the context's device expected" % what)
+        """fn(context, *args): tensors are those that it reads or writes."""
         if self._current(self._index) == self._raw:
             rc = fn(self._h, *args)
-            if rc != HISS_OK:
+            if rc:
                 raise HissError(rc, self._h, what)
             return
         cur = self._torch.cuda.current_stream(self._index)
@@ -546,21 +552,30 @@ class Join:
         cur.wait_stream(self.stream)
         _check(rc, self._h, what)
 
+    def _here(self, what, *tensors):
+        for t in tensors:
+            if t is not None and t.get_device() != self._index:
+                raise ValueError("%s: CUDA tensors on the context's device expected" % what)
+
     def _tokens(self, tokens):
         """(contiguous tokens, bits)."""
         if tokens.dtype == self._torch.int64:
-            return tokens.contiguous(), 64
+            return tokens if tokens.is_contiguous() else tokens.contiguous(), 64
         if tokens.dtype == self._torch.int32:
-            return tokens.contiguous(), 32
+            return tokens if tokens.is_contiguous() else tokens.contiguous(), 32
         raise ValueError("int32 or int64 tokens expected, not %s" % tokens.dtype)
 
-    def _out(self, out, shape, dtype, name="out"):
-        """out, checked, or a new tensor."""
+    def _out(self, out, shape, dtype, default, width, what):
+        """(out checked, or a new tensor; its rows; their stride; their hiss_dtype)."""
         if out is None:
-            return self._torch.empty(shape, dtype=dtype, device=self._device)
+            dtype = dtype or default
+            code = _dtype(dtype)
+            out = self._torch.empty(*shape, dtype=dtype, device=self._device)  # sizes apart: parsed faster than a Size
+            return out, out, width, code
         if out.shape != shape or (dtype is not None and out.dtype != dtype):
-            raise ValueError("%s: shape or type differs from the result's" % name)
-        return out
+            raise ValueError("out: shape or type differs from the result's")
+        self._here(what, out)
+        return (out, *_out_matrix(out, "out"), _dtype(out.dtype))
 
     def embed(self, tokens, table, scale=1.0, pad=None, dtype=None, out=None):
         """scale * table[tokens] (hiss_embed): tokens int32 or int64 of any
@@ -571,11 +586,13 @@ class Join:
         if table.dim() != 2:
             raise ValueError("table: (vocab, width) expected")
         w, vocab, width, stride = _matrix(table, "table")
-        out = self._out(out, (*tokens.shape, width), dtype if out is not None else dtype or table.dtype)
-        o, o_stride = _out_matrix(out, "out")
-        self._enqueue(hiss_embed, (w.data_ptr(), _dtype(w.dtype), vocab, width, stride, t.data_ptr(), bits, t.numel(),
-                                   HISS_NO_PAD if pad is None else pad, scale, o.data_ptr(), _dtype(o.dtype),
-                                   o_stride), "hiss_embed", (t, w, o))
+        kind = table.dtype
+        code = _dtype(kind)
+        self._here("hiss_embed", t, w)
+        out, o, o_stride, o_code = self._out(out, (*t.shape, width), dtype, kind, width, "hiss_embed")
+        self._enqueue(hiss_embed, (w.data_ptr(), code, vocab, width, stride, t.data_ptr(), bits, t.numel(),
+                                   HISS_NO_PAD if pad is None else pad, scale, o.data_ptr(), o_code, o_stride),
+                      "hiss_embed", (t, w, o))
         return out
 
     def embed_grad(self, tokens, dy, vocab, scale=1.0, pad=None, dtype=None, out=None, accumulate=False):
@@ -583,17 +600,18 @@ class Join:
         dy (*tokens.shape, width); returns (vocab, width) of the given dtype
         (default: dy's), or out, to which it is added with accumulate."""
         t, bits = self._tokens(tokens)
-        g, _, width, stride = _matrix(dy, "dy")
-        if dy.shape[:-1] != tokens.shape:
+        g, n, width, stride = _matrix(dy, "dy")
+        if dy.shape[:-1] != t.shape:
             raise ValueError("dy: shape (*tokens.shape, width) expected")
         if out is None and accumulate:
             raise ValueError("accumulate needs out")
-        vocab = int(vocab)
-        out = self._out(out, (max(vocab, 0), width), dtype if out is not None else dtype or dy.dtype)
-        o, o_stride = _out_matrix(out, "out")
-        self._enqueue(hiss_embed_grad, (g.data_ptr(), _dtype(g.dtype), stride, t.data_ptr(), bits, t.numel(),
+        kind = dy.dtype
+        code = _dtype(kind)
+        self._here("hiss_embed_grad", t, g)
+        out, o, o_stride, o_code = self._out(out, (max(vocab, 0), width), dtype, kind, width, "hiss_embed_grad")
+        self._enqueue(hiss_embed_grad, (g.data_ptr(), code, stride, t.data_ptr(), bits, n,
                                         HISS_NO_PAD if pad is None else pad, scale, vocab, width,
-                                        1 if accumulate else 0, o.data_ptr(), _dtype(o.dtype), o_stride),
+                                        1 if accumulate else 0, o.data_ptr(), o_code, o_stride),
                       "hiss_embed_grad", (t, g, o))
         return out
 
@@ -602,17 +620,16 @@ class Join:
         rstd), the statistics float32 of shape x.shape[:-1].  dtype: y's type, x's
         (default) or float32."""
         m, n, width, stride = _matrix(x, "x")
-        p = self._params(width, weight, bias)
-        shape = x.shape
-        out = self._out(out, shape, dtype if out is not None else dtype or x.dtype)
-        o, o_stride = _out_matrix(out, "out")
-        torch = self._torch
-        mean = torch.empty(shape[:-1], dtype=torch.float32, device=self._device)
-        rstd = torch.empty(shape[:-1], dtype=torch.float32, device=self._device)
-        self._enqueue(hiss_layer_norm, (m.data_ptr(), _dtype(m.dtype), stride, n, width,
-                                        None if weight is None else weight.data_ptr(),
-                                        None if bias is None else bias.data_ptr(), p, eps, o.data_ptr(),
-                                        _dtype(o.dtype), o_stride, mean.data_ptr(), rstd.data_ptr()),
+        kind, shape, torch = x.dtype, x.shape, self._torch
+        code = _dtype(kind)
+        p, w_ptr, b_ptr = self._params(width, weight, bias)
+        self._here("hiss_layer_norm", m, weight, bias)
+        out, o, o_stride, o_code = self._out(out, shape, dtype, kind, width, "hiss_layer_norm")
+        rows = shape[:-1]
+        mean = torch.empty(*rows or ((),), dtype=torch.float32, device=self._device)
+        rstd = torch.empty_like(mean)
+        self._enqueue(hiss_layer_norm, (m.data_ptr(), code, stride, n, width, w_ptr, b_ptr, p, eps, o.data_ptr(),
+                                        o_code, o_stride, mean.data_ptr(), rstd.data_ptr()),
                       "hiss_layer_norm", (m, weight, bias, o, mean, rstd))
         return out, mean, rstd
 
@@ -620,26 +637,31 @@ class Join:
         """Gradient of ``layer_norm`` (hiss_layer_norm_grad): (dx, dweight,
         dbias).  dweight and dbias have the weight's type, or param_dtype
         (default: float32) without a weight."""
-        torch = self._torch
+        torch, shape, kind = self._torch, x.shape, x.dtype
         m, n, width, stride = _matrix(x, "x")
         g, _, _, g_stride = _matrix(dy, "dy")
-        shape = x.shape
-        if dy.shape != shape or mean.shape != shape[:-1] or rstd.shape != shape[:-1]:
+        rows = shape[:-1]
+        if dy.shape != shape or mean.shape != rows or rstd.shape != rows:
             raise ValueError("dy, mean and rstd do not match x")
-        if mean.dtype != torch.float32 or rstd.dtype != torch.float32:
+        f32 = torch.float32
+        if mean.dtype != f32 or rstd.dtype != f32:
             raise ValueError("mean and rstd: float32 expected")
-        p = self._params(width, weight, None)
-        pt = weight.dtype if weight is not None else param_dtype or torch.float32
+        code, g_code = _dtype(kind), _dtype(dy.dtype)
+        p, w_ptr, _ = self._params(width, weight, None)
+        pt = weight.dtype if weight is not None else param_dtype or f32
         if weight is None:
             p = _dtype(pt)
-        dx = torch.empty(shape, dtype=x.dtype, device=self._device)
+        if not mean.is_contiguous():
+            mean = mean.contiguous()
+        if not rstd.is_contiguous():
+            rstd = rstd.contiguous()
+        self._here("hiss_layer_norm_grad", g, m, mean, rstd, weight)
+        dx = torch.empty(*shape, dtype=kind, device=self._device)
         dw = torch.empty(width, dtype=pt, device=self._device)
-        db = torch.empty(width, dtype=pt, device=self._device)
-        mean, rstd = mean.contiguous(), rstd.contiguous()
-        self._enqueue(hiss_layer_norm_grad, (g.data_ptr(), _dtype(g.dtype), g_stride, m.data_ptr(), _dtype(m.dtype),
-                                             stride, mean.data_ptr(), rstd.data_ptr(),
-                                             None if weight is None else weight.data_ptr(), p, n, width,
-                                             dx.data_ptr(), width, dw.data_ptr(), db.data_ptr()),
+        db = torch.empty_like(dw)
+        self._enqueue(hiss_layer_norm_grad, (g.data_ptr(), g_code, g_stride, m.data_ptr(), code, stride,
+                                             mean.data_ptr(), rstd.data_ptr(), w_ptr, p, n, width, dx.data_ptr(), width,
+                                             dw.data_ptr(), db.data_ptr()),
                       "hiss_layer_norm_grad", (g, m, mean, rstd, weight, dx, dw, db))
         return dx, dw, db
 
@@ -648,11 +670,12 @@ class Join:
         or a sequence of tensors, clipped in place.  Returns the norm before
         clipping (float32 CUDA scalar)."""
         g = grads if isinstance(grads, Gradients) else Gradients(grads)
-        norm = self._torch.empty((), dtype=self._torch.float32, device=self._device)
-        # one device for all (checked by Gradients); all are recorded on another stream
-        same = self._current(self._index) == self._raw
+        self._here("hiss_clip_grads", *g.grads[:1])  # one device for all: checked by Gradients
+        if self._scalar is None:
+            self._scalar = self._torch.empty((), dtype=self._torch.float32, device=self._device)
+        norm = self._torch.empty_like(self._scalar)
         self._enqueue(hiss_clip_grads, (g.array, len(g.grads), max_norm, norm.data_ptr()), "hiss_clip_grads",
-                      (norm, *g.grads[:1]) if same else (norm, *g.grads, *g.out))
+                      g.all + [norm])
         return norm
 
     def finish(self):
@@ -662,14 +685,13 @@ class Join:
 
     @staticmethod
     def _params(width, weight, bias):
-        """The hiss_dtype of weight and bias."""
-        kind = None
-        for t in (weight, bias):
-            if t is None:
-                continue
-            if t.dim() != 1 or t.shape[0] != width or (width > 1 and t.stride(0) != 1):
-                raise ValueError("weight and bias: contiguous vectors of %d entries expected" % width)
-            if kind is not None and t.dtype != kind:
-                raise ValueError("weight and bias of one type expected")
-            kind = t.dtype
-        return HISS_F32 if kind is None else _dtype(kind)
+        """(hiss_dtype, pointer, pointer) of weight and bias."""
+        if weight is None:
+            if bias is None:
+                return HISS_F32, None, None
+            return _dtype(bias.dtype), None, _vector(bias, width)
+        if bias is None:
+            return _dtype(weight.dtype), _vector(weight, width), None
+        if weight.dtype != bias.dtype:
+            raise ValueError("weight and bias of one type expected")
+        return _dtype(weight.dtype), _vector(weight, width), _vector(bias, width)

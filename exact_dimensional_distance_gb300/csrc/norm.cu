@@ -213,13 +213,14 @@ struct Rows {
     int e = 0, nv = 0;     // elements per pack, packs per lane; e = 0: looping kernels
     int lanes = 0, groups = 0;
     bool narrow = false;
+    bool one_block = false;
 };
 
 // The widest pack that the width and every row's alignment allow; 16 elements
 // per lane, or 32 where that is too few and the caller has such a kernel for
 // the pack; as many groups per block as reach the given threads without leaving
 // SMs idle.
-Rows plan_rows(const NormArgs &a, bool has32, bool has32_wide, int threads)
+Rows plan_rows(const NormArgs &a, bool has32, bool has32_wide, int threads, bool one_block)
 {
     const bool half = a.x_dtype != HISS_F32;
     auto fits = [&](int e) {
@@ -252,9 +253,21 @@ Rows plan_rows(const NormArgs &a, bool has32, bool has32_wide, int threads)
     }
     // a raw row takes up to 30 bytes more than its elements, which counts for very narrow ones
     const size_t row = 4 * (a.width * (dtype_bytes(a.x_dtype) + (a.dy ? dtype_bytes(a.y_dtype) : 0)) + 60);
-    while (2 * r.groups * r.lanes <= threads && (int64_t)r.groups * kSMs < a.n &&
-           (!r.narrow || 2 * r.groups * row <= kSharedBytes))
-        r.groups <<= 1;
+    const auto fits_block = [&](int groups) {
+        return groups * r.lanes <= threads && (!r.narrow || groups * row <= kSharedBytes);
+    };
+    // the backward pass of at most two rows per group of one block: a second
+    // launch to add up the blocks' sums takes longer than the second row
+    if (one_block) {
+        int groups = r.groups;
+        while (groups < a.n && fits_block(2 * groups)) groups <<= 1;
+        if (a.n <= 2 * groups) {
+            r.groups = groups;
+            r.one_block = true;
+            return r;
+        }
+    }
+    while ((int64_t)r.groups * kSMs < a.n && fits_block(2 * r.groups)) r.groups <<= 1;
     return r;
 }
 
@@ -512,9 +525,10 @@ struct Backward {
 };
 
 // Each block leaves its column sums in part[block][0 .. width) (dw) and
-// [width .. 2 width) (db): k_norm_param adds the blocks up.  x_bytes: of x's ring.
+// [width .. 2 width) (db): k_norm_param adds the blocks up.  direct: the only block
+// writes dweight and dbias itself.  x_bytes: of x's ring.
 template <typename TX, typename TY, int E, int NV, bool NARROW>
-__global__ void __launch_bounds__(kMaxLanes) k_norm_grad(NormArgs a, int lanes, int groups, int x_bytes, float *part)
+__global__ void __launch_bounds__(kMaxLanes) k_norm_grad(NormArgs a, int lanes, int groups, int x_bytes, float *part, bool direct)
 {
     using B = Backward<TX, TY, E, NV, NARROW>;
     using PA = Params<NARROW, E, NV>;
@@ -642,7 +656,7 @@ __global__ void __launch_bounds__(kMaxLanes) k_norm_grad(NormArgs a, int lanes, 
         for (; first < a.n; first += step, row += step) body(std::integral_constant<bool, kRaw<E>>{});
     else
         for (; first < a.n; first += step, row += step) body(std::false_type{});
-    if (!part) return;
+    if (!part && !direct) return;
     // the block's column sums: over the groups of a warp, then over the warps (or
     // groups of warps) in a fixed tree, through the ring's memory
     cp_async_wait<0>();
@@ -677,7 +691,18 @@ __global__ void __launch_bounds__(kMaxLanes) k_norm_grad(NormArgs a, int lanes, 
                 q += o.y;
             });
     }
-    if (unit == 0 && lane < lanes) {
+    if (unit == 0 && lane < lanes && direct) {
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+#pragma unroll
+            for (int h = 0; h < H; ++h) {
+                const int c0 = col + (E == 1 ? 2 * c : c) * vs + 2 * h, c1 = E == 1 ? c0 + vs : c0 + 1;
+                if (c0 < a.width && a.dweight) store_any(a.dweight, a.p_dtype, c0, dw[c][h].x);
+                if (c0 < a.width && a.dbias) store_any(a.dbias, a.p_dtype, c0, db[c][h].x);
+                if (c1 < a.width && a.dweight) store_any(a.dweight, a.p_dtype, c1, dw[c][h].y);
+                if (c1 < a.width && a.dbias) store_any(a.dbias, a.p_dtype, c1, db[c][h].y);
+            }
+    } else if (unit == 0 && lane < lanes) {
         float *p = part + (int64_t)blockIdx.x * 2 * a.width + col;
 #pragma unroll
         for (int c = 0; c < NC; ++c)
@@ -839,15 +864,19 @@ unsigned grid_for(const NormArgs &a, const Rows &r, int per_sm)
     return (unsigned)(want < (int64_t)kSMs * per_sm ? want : (int64_t)kSMs * per_sm);
 }
 
-Rows plan_forward(const NormArgs &a) { return plan_rows(a, a.x_dtype != HISS_F32, true, 256); }
+Rows plan_forward(const NormArgs &a) { return plan_rows(a, a.x_dtype != HISS_F32, true, 256, false); }
 
 // 32 elements per lane with a float32 operand would not leave room for two
 // rows in the ring.
-Rows plan_backward(const NormArgs &a) { return plan_rows(a, a.y_dtype != HISS_F32, a.y_dtype != HISS_F32, kMaxLanes); }
+Rows plan_backward(const NormArgs &a)
+{
+    const bool both16 = a.y_dtype != HISS_F32;
+    return plan_rows(a, both16, both16, kMaxLanes, a.dweight || a.dbias);
+}
 
 // Blocks (and parts) of the backward pass: one per SM, so that there are few
 // parts to add up.
-unsigned grad_grid(const NormArgs &a, const Rows &r) { return grid_for(a, r, 1); }
+unsigned grad_grid(const NormArgs &a, const Rows &r) { return r.one_block ? 1 : grid_for(a, r, 1); }
 
 }  // namespace
 
@@ -887,6 +916,7 @@ cudaError_t layer_norm_grad(const NormArgs &a, void *tmp, cudaStream_t s, int64_
     const bool params = a.dweight || a.dbias;
     float *part = params ? static_cast<float *>(tmp) : nullptr;
     unsigned parts = 0;
+    bool direct = false;
     if (a.n > 0) {
         const Rows r = plan_backward(a);
         HISS_TRY(with_xy(a, [&](auto tx, auto ty) {
@@ -915,13 +945,15 @@ cudaError_t layer_norm_grad(const NormArgs &a, void *tmp, cudaStream_t s, int64_
                 const size_t smem = B::smem(threads, r.lanes, a.width, many);
                 resident(kernel, threads, smem, cache);
                 parts = grad_grid(a, r);
-                kernel<<<parts, threads, smem, s>>>(a, r.lanes, r.groups, (int)B::X::bytes(threads, r.lanes, a.width), part);
+                direct = r.one_block;
+                kernel<<<parts, threads, smem, s>>>(a, r.lanes, r.groups, (int)B::X::bytes(threads, r.lanes, a.width),
+                                                  r.one_block ? nullptr : part, r.one_block);
                 ++*launches;
                 return cudaGetLastError();
             });
         }));
     }
-    if (!params) return cudaSuccess;
+    if (!params || direct) return cudaSuccess;
     ++*launches;
     return launch_after(k_norm_param, (unsigned)((2 * a.width + 31) / 32), 1024, 0, s, a, part, (int)parts);
 }
