@@ -51,10 +51,14 @@ __global__ void __launch_bounds__(kThreads) k_embed(EmbedArgs a, int lanes, int 
     const int per_block = kThreads / lanes;
     const int lane = threadIdx.x & (lanes - 1);
     const int64_t items = a.n * tiles, step = (int64_t)gridDim.x * per_block;
-    for (int64_t it = (int64_t)blockIdx.x * per_block + threadIdx.x / lanes; it < items; it += step) {
-        const int64_t i = tiles == 1 ? it : it / tiles;
+    int64_t it = (int64_t)blockIdx.x * per_block + threadIdx.x / lanes;
+    auto position = [&](int64_t item) { return tiles == 1 ? item : item / tiles; };
+    int64_t next = it < items ? row_of(a, position(it)) : kPadRow;
+    bool bad = false;
+    for (; it < items; it += step) {
+        const int64_t i = position(it);
         const int c0 = ((int)(it - i * tiles) * lanes * NV + lane) * E;
-        const int64_t r = row_of(a, i);
+        const int64_t r = next;
         const TI *p = static_cast<const TI *>(a.rows) + r * a.rows_stride;
         TO *q = static_cast<TO *>(a.out) + i * a.out_stride;
         Pack<TI, E> v[NV];
@@ -63,6 +67,9 @@ __global__ void __launch_bounds__(kThreads) k_embed(EmbedArgs a, int lanes, int 
             const int c = c0 + k * lanes * E;
             if (r >= 0 && c < a.width) v[k] = load_pack<TI, E>(p + c);
         }
+        // the next position's token is on its way while this row is
+        if (it + step < items) next = row_of(a, position(it + step));
+        bad = bad || r == kBadRow;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             const int c = c0 + k * lanes * E;
@@ -72,8 +79,92 @@ __global__ void __launch_bounds__(kThreads) k_embed(EmbedArgs a, int lanes, int 
             for (int e = 0; e < E; ++e) o.v[e] = from_f32<TO>(r >= 0 ? a.scale * to_f32(v[k].v[e]) : 0.0f);
             store_pack<TO, E>(q + c, o);
         }
-        if (r == kBadRow) *a.bad = 1;
     }
+    if (bad) *a.bad = 1;
+}
+
+// E elements from any address: the 16-byte lines that hold them, shifted into
+// place.  The lines are inside the matrix.
+template <typename T, int E>
+__device__ __forceinline__ void load_shifted(const T *p, Pack<T, E> &v)
+{
+    constexpr int W = E * sizeof(T) / 4, L = E * sizeof(T) / 16 + 1;  // words; lines they can lie in
+    const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+    const uint4 *line = reinterpret_cast<const uint4 *>(at & ~(uintptr_t)15);
+    const uint32_t off = (uint32_t)at & 15;
+    uint32_t w[4 * L + 1];
+    w[4 * L] = 0;
+#pragma unroll
+    for (int i = 0; i < L; ++i) {
+        uint4 q = make_uint4(0, 0, 0, 0);
+        if (i + 1 < L || off) q = line[i];
+        w[4 * i] = q.x, w[4 * i + 1] = q.y, w[4 * i + 2] = q.z, w[4 * i + 3] = q.w;
+    }
+    // the offset is the same for all lanes of a row, so these do not diverge
+    if (off & 8)
+#pragma unroll
+        for (int i = 0; i + 2 <= 4 * L; ++i) w[i] = w[i + 2 <= 4 * L ? i + 2 : 4 * L];
+    if (off & 4)
+#pragma unroll
+        for (int i = 0; i < 4 * L; ++i) w[i] = w[i + 1];
+    if (sizeof(T) == 2 && (off & 2))
+#pragma unroll
+        for (int i = 0; i < W; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
+    uint32_t *o = reinterpret_cast<uint32_t *>(&v);
+#pragma unroll
+    for (int i = 0; i < W; ++i) o[i] = w[i];
+}
+
+// Rows that are not aligned to 16 bytes, in or out: a lane writes the E
+// elements of an aligned 16-byte line (two for float32 from 16-bit rows) of the output,
+// at column E k - s for line k of a row that begins s elements into its first line.
+// A row's first and last line, and elements whose input lines reach outside
+// the table, go one by one.
+template <typename TI, typename TO, int E>
+__global__ void __launch_bounds__(kThreads) k_embed_raw(EmbedArgs a, int lanes, int tiles)
+{
+    constexpr int NV = 2;  // lines per lane
+    const int per_block = kThreads / lanes;
+    const int lane = threadIdx.x & (lanes - 1);
+    const int64_t items = a.n * tiles, step = (int64_t)gridDim.x * per_block;
+    const uintptr_t lo = reinterpret_cast<uintptr_t>(a.rows), hi = lo + ((a.vocab - 1) * a.rows_stride + a.width) * sizeof(TI);
+    int64_t it = (int64_t)blockIdx.x * per_block + threadIdx.x / lanes;
+    auto position = [&](int64_t item) { return tiles == 1 ? item : item / tiles; };
+    int64_t next = it < items ? row_of(a, position(it)) : kPadRow;
+    bool bad = false;
+    for (; it < items; it += step) {
+        const int64_t i = position(it), r = next;
+        const TI *p = static_cast<const TI *>(a.rows) + r * a.rows_stride;
+        TO *q = static_cast<TO *>(a.out) + i * a.out_stride;
+        const int s = (int)((reinterpret_cast<uintptr_t>(q) & 15) / sizeof(TO));
+        const int c0 = ((int)(it - i * tiles) * lanes * NV + lane) * E - s;
+        Pack<TI, E> v[NV];
+        bool whole[NV];
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int c = c0 + k * lanes * E;
+            const uintptr_t from = reinterpret_cast<uintptr_t>(p + c) & ~(uintptr_t)15;
+            const uintptr_t to = (reinterpret_cast<uintptr_t>(p + c + E) + 15) & ~(uintptr_t)15;
+            whole[k] = c >= 0 && c + E <= a.width && (r < 0 || (from >= lo && to <= hi));
+            if (whole[k] && r >= 0) load_shifted<TI, E>(p + c, v[k]);
+        }
+        if (it + step < items) next = row_of(a, position(it + step));
+        bad = bad || r == kBadRow;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int c = c0 + k * lanes * E;
+            if (whole[k]) {
+                Pack<TO, E> o;
+#pragma unroll
+                for (int e = 0; e < E; ++e) o.v[e] = from_f32<TO>(r >= 0 ? a.scale * to_f32(v[k].v[e]) : 0.0f);
+                store_pack<TO, E>(q + c, o);
+            } else {
+                for (int e = max(c, 0); e < min(c + E, a.width); ++e)
+                    q[e] = from_f32<TO>(r >= 0 ? a.scale * to_f32(p[e]) : 0.0f);
+            }
+        }
+    }
+    if (bad) *a.bad = 1;
 }
 
 // ---- the sort ---------------------------------------------------------------------
@@ -649,9 +740,9 @@ struct FewArgs {
 // and writes the row; the others leave.  Further blocks write zeros to the rows of
 // their range that no position holds.
 template <typename TI, typename TO, int E>
-__global__ void __launch_bounds__(kThreads) k_grad_few(EmbedArgs a, FewArgs f)
+__global__ void __launch_bounds__(kThreads, 4) k_grad_few(EmbedArgs a, FewArgs f)
 {
-    constexpr int U = 8;  // rows in flight
+    constexpr int U = E == 8 ? 4 : 8;  // rows in flight
     __shared__ uint16_t found[kFew];
     __shared__ uint32_t warp_count[kThreads / 32];
     __shared__ union {
@@ -659,11 +750,11 @@ __global__ void __launch_bounds__(kThreads) k_grad_few(EmbedArgs a, FewArgs f)
         uint32_t held[kFewRows / 32];
     } sh;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int64_t r[kFewRound];
+    int r[kFewRound];  // a row is below 2^31
 #pragma unroll
     for (int k = 0; k < kFewRound; ++k) {
         const int i = k * kThreads + threadIdx.x;
-        r[k] = i < a.n ? row_of(a, i) : kPadRow;
+        r[k] = i < a.n ? (int)row_of(a, i) : (int)kPadRow;
     }
     if ((int)blockIdx.x >= f.sums) {
         const int64_t v0 = (int64_t)(blockIdx.x - f.sums) * f.rows, v1 = min(v0 + f.rows, a.vocab);
@@ -684,7 +775,7 @@ __global__ void __launch_bounds__(kThreads) k_grad_few(EmbedArgs a, FewArgs f)
         return;
     }
     const int pos = blockIdx.x / f.tiles, tile = blockIdx.x - pos * f.tiles;
-    const int64_t row = row_of(a, pos);
+    const int row = (int)row_of(a, pos);
     if (row < 0) {
         if (row == kBadRow && threadIdx.x == 0) *a.bad = 1;
         return;
@@ -712,18 +803,13 @@ __global__ void __launch_bounds__(kThreads) k_grad_few(EmbedArgs a, FewArgs f)
     // each group of lanes takes a stretch of the positions
     const int group = threadIdx.x / f.lanes, groups = kThreads / f.lanes, l = threadIdx.x & (f.lanes - 1);
     const int c0 = (tile * f.lanes * kFewPacks + l) * E;
-    float acc[kFewPacks][E];
-#pragma unroll
-    for (int q = 0; q < kFewPacks; ++q)
-#pragma unroll
-        for (int e = 0; e < E; ++e) acc[q][e] = 0.0f;
-    const int to = count * (group + 1) / groups;
-#pragma unroll
-    for (int q = 0; q < kFewPacks; ++q) {
-        const int c = c0 + q * f.lanes * E;
-        if (c >= a.width) break;
+    const int from = count * group / groups, to = count * (group + 1) / groups;
+    TO *out = static_cast<TO *>(a.out) + row * a.out_stride;
+    auto add = [&](int c, float(&acc)[E]) {
         const TI *p = static_cast<const TI *>(a.rows) + c;
-        for (int j = count * group / groups; j < to; j += U) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = 0.0f;
+        for (int j = from; j < to; j += U) {
             Pack<TI, E> v[U];
 #pragma unroll
             for (int u = 0; u < U; ++u)
@@ -732,32 +818,39 @@ __global__ void __launch_bounds__(kThreads) k_grad_few(EmbedArgs a, FewArgs f)
             for (int u = 0; u < U; ++u)
                 if (j + u < to)
 #pragma unroll
-                    for (int e = 0; e < E; ++e) acc[q][e] += to_f32(v[u].v[e]);
+                    for (int e = 0; e < E; ++e) acc[e] += to_f32(v[u].v[e]);
         }
-    }
-    if (groups > 1) {  // then a row is one pack per lane: the groups' sums are added up in order
-#pragma unroll
-        for (int e = 0; e < E; ++e) sh.part[(group * E + e) * f.lanes + l] = acc[0][e];
-        __syncthreads();
-        if (group > 0) return;
-        for (int g = 1; g < groups; ++g)
-#pragma unroll
-            for (int e = 0; e < E; ++e) acc[0][e] += sh.part[(g * E + e) * f.lanes + l];
-    }
-    TO *p = static_cast<TO *>(a.out) + row * a.out_stride;
-#pragma unroll
-    for (int q = 0; q < kFewPacks; ++q) {
-        const int c = c0 + q * f.lanes * E;
-        if (c >= a.width) break;
+    };
+    auto write = [&](int c, const float(&acc)[E]) {
         Pack<TO, E> o;
-        if (a.accumulate) o = load_pack<TO, E>(p + c);
+        if (a.accumulate) o = load_pack<TO, E>(out + c);
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-            float x = a.scale * acc[q][e];
+            float x = a.scale * acc[e];
             if (a.accumulate) x += to_f32(o.v[e]);
             o.v[e] = from_f32<TO>(x);
         }
-        store_pack<TO, E>(p + c, o);
+        store_pack<TO, E>(out + c, o);
+    };
+    float acc[E];
+    if (groups > 1) {  // a row is one pack per lane; the groups' sums are added up in order
+        if (c0 < a.width) {
+            add(c0, acc);
+#pragma unroll
+            for (int e = 0; e < E; ++e) sh.part[(group * E + e) * f.lanes + l] = acc[e];
+        }
+        __syncthreads();
+        if (group > 0 || c0 >= a.width) return;
+        for (int g = 1; g < groups; ++g)
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[e] += sh.part[(g * E + e) * f.lanes + l];
+        write(c0, acc);
+        return;
+    }
+#pragma unroll 1
+    for (int c = c0; c < min(c0 + f.lanes * kFewPacks * E, a.width); c += f.lanes * E) {
+        add(c, acc);
+        write(c, acc);
     }
 }
 
@@ -785,14 +878,17 @@ int pack_of(const EmbedArgs &a, int wide)
 template <int V>
 using Int = std::integral_constant<int, V>;
 
+// Elements per access where rows are aligned: 16 bytes of the narrower type.
+template <typename TI, typename TO>
+constexpr int kWide = sizeof(TI) == 4 && sizeof(TO) == 4 ? 4 : 8;
+
 // f(TI{}, TO{}, E) for the accesses of a.
 template <typename F>
 cudaError_t with_types(const EmbedArgs &a, F &&f)
 {
     return with_dtype(a.rows_dtype, [&](auto ti) {
         return with_dtype(a.out_dtype, [&](auto to) {
-            // 16 bytes of the narrower type
-            constexpr int W = sizeof(ti) == 4 && sizeof(to) == 4 ? 4 : 8;
+            constexpr int W = kWide<decltype(ti), decltype(to)>;
             const int e = pack_of(a, W);
             if (e == W) return f(ti, to, Int<W>{});
             if (e == 2) return f(ti, to, Int<2>{});
@@ -852,16 +948,24 @@ GradLayout layout(const EmbedArgs &a)
 
 cudaError_t embed(const EmbedArgs &a, cudaStream_t s, int64_t *launches)
 {
-    return with_types(a, [&](auto ti, auto to, auto e) {
-        constexpr int E = decltype(e)::value, NV = E >= 8 ? 4 : 16 / E;
-        int lanes = 1;
-        while (lanes < 32 && lanes * E * NV < a.width) lanes <<= 1;
-        const int tiles = (a.width + lanes * E * NV - 1) / (lanes * E * NV);
-        const int64_t want = (a.n * tiles * lanes + kThreads - 1) / kThreads;
-        const unsigned grid = (unsigned)std::min<int64_t>(want, 16 * kSMs);
-        k_embed<decltype(ti), decltype(to), E, NV><<<grid, kThreads, 0, s>>>(a, lanes, tiles);
-        ++*launches;
-        return cudaGetLastError();
+    ++*launches;
+    return with_dtype(a.rows_dtype, [&](auto ti) {
+        return with_dtype(a.out_dtype, [&](auto to) {
+            using TI = decltype(ti);
+            using TO = decltype(to);
+            constexpr int E = kWide<TI, TO>;
+            const bool raw = pack_of(a, E) != E;
+            const int packs = raw ? 2 : 4;  // per lane
+            const int cols = a.width + (raw ? E - 1 : 0);  // a raw row begins inside its first line
+            int lanes = 1;
+            while (lanes < 32 && lanes * E * packs < cols) lanes <<= 1;
+            const int tiles = (cols + lanes * E * packs - 1) / (lanes * E * packs);
+            const int64_t want = (a.n * tiles * lanes + kThreads - 1) / kThreads;
+            const unsigned grid = (unsigned)std::min<int64_t>(want, 16 * kSMs);
+            if (raw) k_embed_raw<TI, TO, E><<<grid, kThreads, 0, s>>>(a, lanes, tiles);
+            else k_embed<TI, TO, E, 4><<<grid, kThreads, 0, s>>>(a, lanes, tiles);
+            return cudaGetLastError();
+        });
     });
 }
 
