@@ -270,6 +270,8 @@ class Gradients:
 
     @staticmethod
     def _dense(t):
+        if t.is_contiguous():
+            return True
         want = 1
         for size, stride in sorted(((n, s) for n, s in zip(t.shape, t.stride()) if n != 1), key=lambda p: p[1]):
             if stride != want:
