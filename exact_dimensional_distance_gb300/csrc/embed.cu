@@ -1059,11 +1059,8 @@ cudaError_t embed_grad(const EmbedArgs &a, void *tmp, uint32_t *present, cudaStr
             for (m.lanes = BIG ? 32 : 1; m.lanes < 32 && m.lanes * S::C < a.width;) m.lanes <<= 1;
             m.tiles = (a.width + m.lanes * S::C - 1) / (m.lanes * S::C);
             m.blocks = (int)((l.units * m.tiles + kThreads / m.lanes - 1) / (kThreads / m.lanes));
-            static std::atomic<bool> allowed{false};  // of this kernel
-            if (!allowed.load(std::memory_order_acquire)) {
-                HISS_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 128 * 1024));
-                allowed.store(true, std::memory_order_release);
-            }
+            static std::atomic<uint64_t> allowed{0};
+            HISS_TRY(allow_shared(kernel, 128 * 1024, allowed));
             ++*launches;
             return launch_after(kernel, m.blocks + f.blocks, kThreads, S::smem(m.lanes), st, a, m, f);
         };

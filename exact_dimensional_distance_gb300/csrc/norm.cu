@@ -17,7 +17,6 @@
 // hold a row of any other alignment.  Rows too wide for a group of kMaxLanes go through the looping
 // kernels at the end of the file.
 #include <algorithm>
-#include <atomic>
 
 #include "hiss_internal.cuh"
 #include "numeric.cuh"
@@ -272,24 +271,24 @@ Rows plan_rows(const NormArgs &a, bool has32, bool has32_wide, int threads, bool
 }
 
 // Resident blocks per SM of a kernel: those that its registers allow at a block
-// size, asked for once (and the kernel is allowed its shared memory), and those
-// that its shared memory leaves.
+// size, asked for once, and those that its shared memory leaves.
 struct Residency {
-    std::atomic<int> blocks[kMaxWarps + 1];
+    std::atomic<uint64_t> allowed{0};  // devices on which it may use kSharedBytes
+    std::atomic<int> blocks[kMaxWarps + 1] = {};
 };
 template <typename K>
-int resident(K kernel, int threads, size_t smem, Residency &cache)
+cudaError_t resident(K kernel, int threads, size_t smem, Residency &cache, int *blocks)
 {
+    HISS_TRY(allow_shared(kernel, kSharedBytes, cache.allowed));
     std::atomic<int> &c = cache.blocks[threads / 32];
-    int v = c.load(std::memory_order_acquire);
+    int v = c.load(std::memory_order_relaxed);
     if (v == 0) {
-        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSharedBytes) != cudaSuccess ||
-            cudaOccupancyMaxActiveBlocksPerMultiprocessor(&v, kernel, threads, 0) != cudaSuccess || v < 1)
-            v = 1;
-        c.store(v, std::memory_order_release);
+        HISS_TRY(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&v, kernel, threads, 0));
+        c.store(v, std::memory_order_relaxed);
     }
     const int fit = (int)(227 * 1024 / (smem + sizeof(Exchange) * kMaxWarps + 1024));  // 1 KB per block is the system's
-    return std::max(1, std::min(v, fit));
+    *blocks = std::max(1, std::min(v, fit));
+    return cudaSuccess;
 }
 
 // ---- parameters -----------------------------------------------------------------
@@ -898,7 +897,9 @@ cudaError_t layer_norm(const NormArgs &a, cudaStream_t s, int64_t *launches)
             auto kernel = k_norm<TX, TY, E, NV, NARROW>;
             const int threads = r.lanes * r.groups;
             const size_t smem = Forward<TX, E, NV, NARROW>::smem(threads, r.lanes, a.width);
-            const unsigned grid = grid_for(a, r, resident(kernel, threads, smem, cache));
+            int per_sm = 1;
+            HISS_TRY(resident(kernel, threads, smem, cache, &per_sm));
+            const unsigned grid = grid_for(a, r, per_sm);
             kernel<<<grid, threads, smem, s>>>(a, r.lanes, r.groups);
             return cudaGetLastError();
         });
@@ -937,13 +938,13 @@ cudaError_t layer_norm_grad(const NormArgs &a, void *tmp, cudaStream_t s, int64_
             }
             return with_packs<TX, sizeof(TY) == 2, sizeof(TY) == 2>(r, [&](auto e, auto nv, auto narrow) {
                 constexpr int E = decltype(e)::value, NV = decltype(nv)::value;
-                static Residency cache;
+                static std::atomic<uint64_t> allowed{0};
                 auto kernel = k_norm_grad<TX, TY, E, NV, decltype(narrow)::value>;
                 const int threads = r.lanes * r.groups;
                 const bool many = threads > (r.narrow ? 32 : r.lanes);  // sums of several warps or groups to add up
                 using B = Backward<TX, TY, E, NV, decltype(narrow)::value>;
                 const size_t smem = B::smem(threads, r.lanes, a.width, many);
-                resident(kernel, threads, smem, cache);
+                HISS_TRY(allow_shared(kernel, kSharedBytes, allowed));
                 parts = grad_grid(a, r);
                 direct = r.one_block;
                 kernel<<<parts, threads, smem, s>>>(a, r.lanes, r.groups, (int)B::X::bytes(threads, r.lanes, a.width),

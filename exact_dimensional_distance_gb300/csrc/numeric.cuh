@@ -7,6 +7,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <atomic>
 #include <type_traits>
 
 #include "hiss.h"
@@ -131,6 +132,21 @@ inline bool rows_aligned(const void *p, int64_t stride, int dtype, int e)
 {
     const size_t b = dtype_bytes(dtype) * e < 16 ? dtype_bytes(dtype) * e : 16;
     return reinterpret_cast<uintptr_t>(p) % b == 0 && (stride * dtype_bytes(dtype)) % b == 0;
+}
+
+// Lets a kernel use bytes of dynamic shared memory, once per device (done: a bit
+// for each, of this kernel alone).
+template <typename K>
+cudaError_t allow_shared(K kernel, size_t bytes, std::atomic<uint64_t> &done)
+{
+    int device = 0;
+    cudaError_t e = cudaGetDevice(&device);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = uint64_t(1) << (device & 63);
+    if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+    return e;
 }
 
 // ---- launches that overlap the kernel before them ---------------------------

@@ -352,7 +352,8 @@ int hiss_gram_tf32(hiss_ctx *ctx, const float *d_a, const float *d_b, int32_t k,
  *     >= 0 for what is only read (0 repeats one row).  Pointers are aligned to
  *     their element.  Any alignment and width is accepted; 16-byte aligned
  *     rows are read and written with 16-byte accesses.
- *   - What is written must not overlap anything else of the same call
+ *   - What is written must not overlap anything else of the same call, from
+ *     the first element to the last, the gaps between rows included
  *     (HISS_E_ARG), unless a call says otherwise.
  *   - Sums, means and norms are held in float32 or wider whatever the types,
  *     and each result is rounded once, to nearest even, when it is stored.

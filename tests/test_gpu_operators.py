@@ -224,6 +224,85 @@ def test_embed_grad_broadcast_and_order(lib):
     lib.finish()
 
 
+@pytest.mark.parametrize("n", [1, 700, 2048, 2049, 40000])
+def test_embed_grad_all_padding(lib, n):
+    t = torch.full((n,), -7, dtype=torch.int32, device="cuda")
+    dy = torch.full((n, 40), float("nan"), device="cuda")  # what is masked is not read
+    got = lib.embed_grad(t, dy, 333, pad=-7, out=torch.full((333, 40), 9.0, device="cuda"))
+    assert not got.any()
+    kept = torch.full((333, 40), 9.0, device="cuda")
+    lib.embed_grad(t, dy, 333, pad=-7, out=kept, accumulate=True)
+    assert bool((kept == 9.0).all())
+    # one position left: its row alone, whatever the padding holds
+    t[n // 2] = 5
+    dy[n // 2] = 1.5
+    got = lib.embed_grad(t, dy, 333, pad=-7)
+    assert bool((got[5] == 1.5).all()) and int((got != 0).any(1).sum()) == 1
+    lib.finish()
+
+
+@pytest.mark.parametrize("vocab", [511, 512, (1 << 18) - 1, 1 << 18, 300007, (1 << 20) + 3])
+def test_embed_grad_large_vocabularies(lib, vocab):
+    # one, two and three sort passes; more tokens than a tile's bitmap holds
+    g = _gen(vocab)
+    n = 30000
+    t = _tokens(n, vocab, g, "zipf", 64, -1)
+    dy = torch.randint(-8, 9, (n, 6), generator=g, device="cuda").float()  # integers: exact in any order
+    want = torch.zeros((vocab, 6), dtype=torch.float64, device="cuda")
+    keep = t >= 0
+    want.index_put_((t[keep],), dy[keep].double(), accumulate=True)
+    for _ in range(2):  # the second call finds what the first left in the workspace
+        assert torch.equal(lib.embed_grad(t, dy, vocab, pad=-1).double(), want)
+    lib.finish()
+
+
+def test_embed_grad_many_positions(lib):
+    # more than 128 tiles of the largest size
+    g = _gen(99)
+    n, vocab = 700_001, 1000
+    t = _tokens(n, vocab, g, "zipf", 32, 3)
+    dy = torch.randint(-2, 3, (n, 3), generator=g, device="cuda").to(BF16)
+    want = torch.zeros((vocab, 3), dtype=torch.float64, device="cuda")
+    keep = t != 3
+    want.index_put_((t[keep].long(),), dy[keep].double(), accumulate=True)
+    assert torch.equal(lib.embed_grad(t, dy, vocab, pad=3, dtype=F32).double(), want)
+    lib.finish()
+
+
+def test_offsets_beyond_32_bits(edd, lib):
+    """Matrices and tensors of more than 2^31 elements."""
+    rows, width = (1 << 21) + 5, 1040
+    assert rows * width > 1 << 31
+    x = torch.empty((rows, width), dtype=BF16, device="cuda")
+    step = 1 << 18
+    for i in range(0, rows, step):
+        x[i:i + step] = (torch.arange(i, min(i + step, rows), device="cuda") % 251).to(BF16)[:, None]
+    x += (torch.arange(width, device="cuda") % 2).to(BF16)
+    last = torch.tensor([0, 1, rows - 1, rows - 2, (1 << 31) // width + 1], device="cuda")
+    assert torch.equal(lib.embed(last, x), x[last])
+    y, mean, rstd = lib.layer_norm(x)
+    want = lib.layer_norm(x[last].contiguous())
+    assert torch.equal(y[last], want[0]) and torch.equal(mean[last], want[1]) and torch.equal(rstd[last], want[2])
+    dx, _, _ = lib.layer_norm_grad(x, y, mean, rstd)
+    assert torch.equal(dx[last], lib.layer_norm_grad(x[last].contiguous(), y[last].contiguous(), mean[last], rstd[last])[0])
+    del y, dx
+    # the gradient of a table of as many elements, and as many elements of dy
+    dy = torch.ones((5, width), dtype=BF16, device="cuda")
+    grad = lib.embed_grad(last, dy, rows)
+    assert torch.equal(grad.sum(1, dtype=torch.float32).nonzero().flatten(), last.sort().values)
+    assert bool((grad[last] == 1).all())
+    del grad
+    t = torch.full((rows,), -1, device="cuda")
+    t[last] = torch.arange(5, device="cuda")
+    assert torch.equal(lib.embed_grad(t, x, 7, pad=-1)[:5], x[last])
+    norm = lib.clip_grads(edd.Gradients([x.view(-1)]), float("inf"))
+    assert abs(float(norm) - math.sqrt(sum(float((x[i:i + step].double() ** 2).sum()) for i in range(0, rows, step)))) <= \
+        1e-5 * float(norm)
+    lib.clip_grads([x], float(norm) / 2)
+    assert torch.equal(x[-1, :2], torch.tensor([(rows - 1) % 251 / 2, ((rows - 1) % 251 + 1) / 2], device="cuda").to(BF16))
+    lib.finish()
+
+
 def test_embed_grad_against_differences(lib):
     # L = sum(dy * embed(E)) is linear in E: the difference along V is <grad, V>
     g = _gen(9)
