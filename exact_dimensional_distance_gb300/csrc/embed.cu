@@ -548,63 +548,58 @@ __global__ void __launch_bounds__(kThreads) k_sum(EmbedArgs a, SumArgs s, Fill f
     }
     if (i >= end) return;
 
-    const uint32_t mask = lanes == 32 ? 0xffffffffu : ((1u << lanes) - 1u) << (threadIdx.x & 31 & ~(lanes - 1));
     const int row_bytes = S::row_bytes(lanes);
     char *group_ring = ring + (threadIdx.x / lanes) * (A * row_bytes);
     const TI *rows = static_cast<const TI *>(a.rows) + t0;
-    // lines that reach outside the matrix are copied by element: they belong to
-    // the first and last rows
-    const uintptr_t lo = reinterpret_cast<uintptr_t>(a.rows), hi = lo + ((a.n - 1) * a.rows_stride + a.width) * sizeof(TI);
+    // raw: lines that reach outside the matrix are copied by element: they belong
+    // to the first and last rows
     const uint32_t edge = a.rows_stride > 0 ? (uint32_t)((15 + a.rows_stride) / a.rows_stride) : 0x7fffffffu;
     const uint32_t rows_at = (uint32_t)reinterpret_cast<uintptr_t>(rows), rows_by = (uint32_t)a.rows_stride * (uint32_t)sizeof(TI);
-    auto fetch = [&](int j) {
-        if (j < end) {
-            const uint32_t y = s.items[j].y;
-            const TI *p = rows + (int64_t)y * a.rows_stride;
-            char *d = group_ring + (j & (A - 1)) * row_bytes;
-            if constexpr (RAW) {
-                const int off = (int)((rows_at + y * rows_by) & 15), bytes = off + cols * (int)sizeof(TI);
-                const char *q = reinterpret_cast<const char *>(p) - off;
-                if (y >= edge && y + edge < (uint32_t)n) {
-#pragma unroll 2
-                    for (int b = 16 * lane; b < bytes; b += 16 * lanes) cp_async16(d + b, q + b);
-                } else {
-                    const uintptr_t b0 = reinterpret_cast<uintptr_t>(p), b1 = b0 + cols * sizeof(TI), line0 = b0 - off;
-                    for (int b = 16 * lane; b < bytes; b += 16 * lanes) {
-                        if (line0 + b >= lo && line0 + b + 16 <= hi) {
-                            cp_async16(d + b, q + b);
-                        } else {
-                            for (uintptr_t e = max(line0 + b, b0); e < min(line0 + b + 16, b1); e += sizeof(TI))
-                                *reinterpret_cast<TI *>(d + (e - line0)) = *reinterpret_cast<const TI *>(e);
-                        }
+    // start copying row y into place st of the ring
+    auto copy = [&](uint32_t y, int st) {
+        const TI *p = rows + (int64_t)y * a.rows_stride;
+        char *d = group_ring + st * row_bytes;
+        if constexpr (RAW) {
+            const int off = (int)((rows_at + y * rows_by) & 15), bytes = off + cols * (int)sizeof(TI);
+            const char *q = reinterpret_cast<const char *>(p) - off;
+            if (y >= edge && y + edge < (uint32_t)n) {
+                if constexpr (BIG) {
+#pragma unroll
+                    for (int k = 0; k < (512 * (int)sizeof(TI) + 15 + 511) / 512; ++k) {
+                        if (512 * k >= bytes) break;
+                        if (512 * k + 16 * lane < bytes) cp_async16(d + 512 * k + 16 * lane, q + 512 * k + 16 * lane);
                     }
+                } else {
+                    for (int b = 16 * lane; b < bytes; b += 16 * lanes) cp_async16(d + b, q + b);
                 }
             } else {
-#pragma unroll
-                for (int k = 0; k < NV; ++k) {
-                    const int c = (k * lanes + lane) * E;
-                    if (c >= cols) break;
-                    copy_pack_async<TI, E>(reinterpret_cast<P *>(d) + k * lanes + lane, p + c);
+                const uintptr_t lo = reinterpret_cast<uintptr_t>(a.rows), hi = lo + ((a.n - 1) * a.rows_stride + a.width) * sizeof(TI);
+                const uintptr_t b0 = reinterpret_cast<uintptr_t>(p), b1 = b0 + cols * sizeof(TI), line0 = b0 - off;
+                for (int b = 16 * lane; b < bytes; b += 16 * lanes) {
+                    if (line0 + b >= lo && line0 + b + 16 <= hi) {
+                        cp_async16(d + b, q + b);
+                    } else {
+                        for (uintptr_t e = max(line0 + b, b0); e < min(line0 + b + 16, b1); e += sizeof(TI))
+                            *reinterpret_cast<TI *>(d + (e - line0)) = *reinterpret_cast<const TI *>(e);
+                    }
                 }
             }
+        } else {
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                const int c = (k * lanes + lane) * E;
+                if (c >= cols) break;
+                copy_pack_async<TI, E>(reinterpret_cast<P *>(d) + k * lanes + lane, p + c);
+            }
         }
-        cp_async_commit();
     };
-    for (int k = 0; k < A - 1; ++k) fetch(i + k);
     float acc[C];
 #pragma unroll
     for (int c = 0; c < C; ++c) acc[c] = 0.0f;
-    float *part = s.part + unit * 2 * a.width;
-    bool head = long_in;  // the current run is the long one that came in
-    uint2 it = s.items[i];
-    while (i < end) {
-        cp_async_wait<A - 2>();
-        // raw: the row was copied by the whole group, and the row before it has been read
-        // by the whole group before its place in the ring is filled again
-        if (RAW) __syncwarp(mask);
-        fetch(i + A - 1);
-        const char *d = group_ring + (i & (A - 1)) * row_bytes;
-        if constexpr (RAW) d += (rows_at + it.y * rows_by) & 15;
+    // add row y, which is in place st
+    auto add = [&](uint32_t y, int st) {
+        const char *d = group_ring + st * row_bytes;
+        if constexpr (RAW) d += (rows_at + y * rows_by) & 15;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             if (k * lanes * E >= cols) break;
@@ -621,16 +616,68 @@ __global__ void __launch_bounds__(kThreads) k_sum(EmbedArgs a, SumArgs s, Fill f
                 }
             }
         }
-        const uint32_t key = it.x;
-        ++i;
-        it = i < end ? s.items[i] : make_uint2(none, 0);
-        if (it.x == key) continue;
-        const bool tail = i >= end && long_out;
-        if (head || tail) write_part<E, C>(a, head ? part : part + a.width, c0, lanes, acc);
+    };
+    float *part = s.part + unit * 2 * a.width;
+    bool head = long_in;  // the current run is the long one that came in
+    // a run is complete, with its last position before the end or not
+    auto flush = [&](uint32_t key, bool at_end) {
+        if (head || (at_end && long_out)) write_part<E, C>(a, head ? part : part + a.width, c0, lanes, acc);
         else write_row<TO, E, C>(a, key, c0, lanes, acc);
         head = false;
 #pragma unroll
         for (int c = 0; c < C; ++c) acc[c] = 0.0f;
+    };
+    const int m = end - i;  // positions, fewer than two units
+    if constexpr (BIG) {
+        // the positions (at most 63) are held by the warp's lanes, and where a run
+        // ends in a mask
+        uint2 it[2];
+        uint64_t ends = 0;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int j = i + 32 * h + lane;
+            it[h] = j < end ? s.items[j] : make_uint2(none, 0);
+            const uint32_t after = j + 1 < end ? s.items[j + 1].x : none;
+            ends |= (uint64_t)__ballot_sync(0xffffffffu, it[h].x != after) << (32 * h);
+        }
+        auto y_of = [&](int j) {
+            const uint32_t y0 = __shfl_sync(0xffffffffu, it[0].y, j & 31), y1 = __shfl_sync(0xffffffffu, it[1].y, j & 31);
+            return j < 32 ? y0 : y1;
+        };
+        for (int k = 0; k < A - 1; ++k) {
+            if (k < m) copy(y_of(k), k);
+            cp_async_commit();
+        }
+        for (int j = 0; j < m; ++j) {
+            cp_async_wait<A - 2>();
+            // raw: the row was copied by the whole warp, and the row before it has been
+            // read by the whole warp before its place in the ring is filled again
+            if (RAW) __syncwarp();
+            if (j + A - 1 < m) copy(y_of(j + A - 1), (j + A - 1) & (A - 1));
+            cp_async_commit();
+            add(RAW ? y_of(j) : 0u, j & (A - 1));
+            if (ends >> j & 1) {
+                const uint32_t x0 = __shfl_sync(0xffffffffu, it[0].x, j & 31), x1 = __shfl_sync(0xffffffffu, it[1].x, j & 31);
+                flush(j < 32 ? x0 : x1, j + 1 == m);
+            }
+        }
+    } else {
+        const uint32_t mask = lanes == 32 ? 0xffffffffu : ((1u << lanes) - 1u) << (threadIdx.x & 31 & ~(lanes - 1));
+        for (int k = 0; k < A - 1; ++k) {
+            if (k < m) copy(s.items[i + k].y, k);
+            cp_async_commit();
+        }
+        uint2 it = s.items[i];
+        for (int j = 0; j < m; ++j) {
+            cp_async_wait<A - 2>();
+            if (RAW) __syncwarp(mask);
+            if (j + A - 1 < m) copy(s.items[i + j + A - 1].y, (j + A - 1) & (A - 1));
+            cp_async_commit();
+            add(it.y, j & (A - 1));
+            const uint32_t key = it.x;
+            it = j + 1 < m ? s.items[i + j + 1] : make_uint2(none, 0);
+            if (it.x != key) flush(key, j + 1 == m);
+        }
     }
     let_next_start();
 }
