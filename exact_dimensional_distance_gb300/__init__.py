@@ -8,6 +8,10 @@ join runs in the library's CUDA kernels.  PyTorch supplies device memory and
 streams.  There is no CPU fallback: importing this module fails if
 libhiss.so has not been built (``python exact_dimensional_distance_gb300/build.py``).
 
+Operators that take a model's parameters to the points and a gradient back
+(embedding lookup, layer norm, their gradients, clipping by the global gradient
+norm) are methods of ``Join`` too; they are asynchronous on its stream.
+
 Functions with the names of the C ABI (``hiss_create``, ``hiss_build``, ...)
 are the raw entry points; ``Join`` wraps a context for convenience.
 """

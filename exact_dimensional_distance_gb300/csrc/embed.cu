@@ -46,7 +46,7 @@ __device__ __forceinline__ int64_t row_of(const EmbedArgs &a, int64_t i)
 // lanes (a power of two up to 32) take one tile of lanes * E * NV columns of
 // one position.
 template <typename TI, typename TO, int E, int NV>
-__global__ void __launch_bounds__(kThreads) k_embed(EmbedArgs a, int lanes, int tiles)
+__global__ void __launch_bounds__(kThreads, 4) k_embed(EmbedArgs a, int lanes, int tiles)
 {
     const int per_block = kThreads / lanes;
     const int lane = threadIdx.x & (lanes - 1);
