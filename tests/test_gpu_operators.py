@@ -586,6 +586,13 @@ def test_clip_extremes(edd, lib):
                 assert math.isnan(n) if math.isnan(bad) else n == float("inf")
             for t, s in zip([a, b] + out, [a0, b0] * 2):
                 assert torch.equal(t.view(torch.uint8), s.view(torch.uint8))
+    # mostly zeros, as the gradient of a table, and values at the edges of the float32 sums
+    for v in (1.0, 2.0 ** -55, 2.0 ** -56, 2.0 ** -60, 2.0 ** -70, 2.0 ** 50, 2.0 ** 51, 2.0 ** 64):
+        for dt in (F32, BF16):
+            z = torch.zeros(200003, device="cuda")
+            z[::997] = v
+            z[5000:5100] = -1.5 * v
+            _check_clip(lib, edd, [z.to(dt)], 3.0 * float(np.float32(v)), False)
     # limits: zero, infinite, exactly the norm
     t = torch.tensor([3.0, 4.0], device="cuda")
     assert float(lib.clip_grads([t], 5.0)) == 5.0 and t.tolist() == [3.0, 4.0]
