@@ -680,8 +680,9 @@ class Join:
         if self._scalar is None:
             self._scalar = self._torch.empty((), dtype=self._torch.float32, device=self._device)
         norm = self._torch.empty_like(self._scalar)
+        here = self._current(self._index) == self._raw  # then no list of the tensors is needed
         self._enqueue(hiss_clip_grads, (g.array, len(g.grads), max_norm, norm.data_ptr()), "hiss_clip_grads",
-                      g.all + [norm])
+                      () if here else g.all + [norm])
         return norm
 
     def finish(self):

@@ -25,11 +25,11 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kBlocksPerSM = 5;
+constexpr int kBlocksPerSM = 4;
 constexpr int kMaxBlocks = kSMs * kBlocksPerSM;
 constexpr int kUnroll = 4;         // accesses in flight per thread
 constexpr int kMaxTensors = 1000;  // 29 KB of parameters per launch (the limit is 32,764 bytes)
-constexpr int kFewTensors = 64;
+constexpr int kFewTensors = 64, kSomeTensors = 384;  // shorter lists for fewer: a launch copies its parameters
 
 template <int CAP>
 struct TensorList {
@@ -361,6 +361,7 @@ cudaError_t clip_grads(const hiss_tensor *t, int64_t count, float max_norm, floa
     double *part = static_cast<double *>(tmp);
     ClipState *c = static_cast<ClipState *>(state);
     if (p.used <= kFewTensors) return run<kFewTensors>(t, count, p, max_norm, norm, c, part, s, launches);
+    if (p.used <= kSomeTensors) return run<kSomeTensors>(t, count, p, max_norm, norm, c, part, s, launches);
     return run<kMaxTensors>(t, count, p, max_norm, norm, c, part, s, launches);
 }
 
