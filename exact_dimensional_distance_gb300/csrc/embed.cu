@@ -29,6 +29,7 @@ namespace hiss {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kRawThreads = 128;  // of k_embed_raw
 
 // The table row of position i; kPadRow for padding and kBadRow for a token
 // outside the table, both rows of zeros.  The caller raises *a.bad once it has
@@ -86,89 +87,108 @@ __global__ void __launch_bounds__(kThreads, 4) k_embed(EmbedArgs a, int lanes, i
     if (bad) *a.bad = 1;
 }
 
-// E elements from any address: the 16-byte lines that hold them, shifted into
-// place.  The lines are inside the matrix.
+// The 16-byte lines that hold E elements of any address, and those elements shifted
+// into place.  Lanes of two rows sit in one warp, so nothing here branches.
 template <typename T, int E>
-__device__ __forceinline__ void load_shifted(const T *p, Pack<T, E> &v)
-{
-    constexpr int W = E * sizeof(T) / 4, L = E * sizeof(T) / 16 + 1;  // words; lines they can lie in
-    const uintptr_t at = reinterpret_cast<uintptr_t>(p);
-    const uint4 *line = reinterpret_cast<const uint4 *>(at & ~(uintptr_t)15);
-    const uint32_t off = (uint32_t)at & 15;
-    uint32_t w[4 * L + 1];
-    w[4 * L] = 0;
+struct Lines {
+    static constexpr int W = E * sizeof(T) / 4, L = E * sizeof(T) / 16 + 1;  // words; lines they can lie in
+    uint4 q[L];
+
+    __device__ __forceinline__ void load(const T *p, bool wanted)
+    {
+        const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+        const uint4 *line = reinterpret_cast<const uint4 *>(at & ~(uintptr_t)15);
 #pragma unroll
-    for (int i = 0; i < L; ++i) {
-        uint4 q = make_uint4(0, 0, 0, 0);
-        if (i + 1 < L || off) q = line[i];
-        w[4 * i] = q.x, w[4 * i + 1] = q.y, w[4 * i + 2] = q.z, w[4 * i + 3] = q.w;
+        for (int i = 0; i < L; ++i) {
+            q[i] = make_uint4(0, 0, 0, 0);
+            if (wanted && (i + 1 < L || (at & 15))) q[i] = line[i];
+        }
     }
-    // the offset is the same for all lanes of a row, so these do not diverge
-    if (off & 8)
+    __device__ __forceinline__ void shifted(const T *p, Pack<T, E> &v) const
+    {
+        const uint32_t off = (uint32_t)reinterpret_cast<uintptr_t>(p) & 15;
+        uint32_t w[4 * L];
 #pragma unroll
-        for (int i = 0; i + 2 <= 4 * L; ++i) w[i] = w[i + 2 <= 4 * L ? i + 2 : 4 * L];
-    if (off & 4)
+        for (int i = 0; i < L; ++i) w[4 * i] = q[i].x, w[4 * i + 1] = q[i].y, w[4 * i + 2] = q[i].z, w[4 * i + 3] = q[i].w;
 #pragma unroll
-        for (int i = 0; i < 4 * L; ++i) w[i] = w[i + 1];
-    if (sizeof(T) == 2 && (off & 2))
+        for (int i = 0; i < W + 2; ++i) w[i] = off & 8 ? w[i + 2] : w[i];
 #pragma unroll
-        for (int i = 0; i < W; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
-    uint32_t *o = reinterpret_cast<uint32_t *>(&v);
+        for (int i = 0; i < W + 1; ++i) w[i] = off & 4 ? w[i + 1] : w[i];
+        uint32_t *o = reinterpret_cast<uint32_t *>(&v);
 #pragma unroll
-    for (int i = 0; i < W; ++i) o[i] = w[i];
+        for (int i = 0; i < W; ++i) o[i] = sizeof(T) == 2 ? __funnelshift_r(w[i], w[i + 1], 8 * (off & 2)) : w[i];
+    }
+};
+
+template <typename T, int E>
+__device__ __forceinline__ void store_sector(T *p, const Pack<T, E> &v)
+{
+    static_assert(sizeof(v) == 32, "one sector, one store");
+    const uint32_t *w = reinterpret_cast<const uint32_t *>(&v);
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
 }
 
-// Rows that are not aligned to 16 bytes, in or out: a lane writes the E
-// elements of an aligned 16-byte line (two for float32 from 16-bit rows) of the output,
-// at column E k - s for line k of a row that begins s elements into its first line.
-// A row's first and last line, and elements whose input lines reach outside
-// the table, go one by one.  44,985 x 1853 bfloat16: 72 us (112 with 2-byte
-// accesses, of which each costs as much as one of 16 bytes).
+// Rows that are not aligned to 16 bytes, in or out: a thread writes the E elements
+// of one 32-byte sector of the output, at column E k - s for sector k of a row that
+// begins s elements into its first.  The sectors of all rows are dealt out in
+// turn (sectors per row; magic divides by it), so that a row's length need not fit a
+// warp; a row's first and last sector go word by word, and packs whose
+// input lines reach outside the table are loaded element by element.
+//
+// Bound by instructions (3.1 per cycle) and, almost as much, by writes: 214,863 x 526
+// float16 60 us (3.8 TB/s written); 92 with 16 bytes per thread, whose
+// indexing costs the same, and 171 with a warp per 512 columns of one row.
+// Two sectors per thread 75, blocks of 256 threads 64.  44,985 x 1853 bfloat16 44 us.
 template <typename TI, typename TO, int E>
-__global__ void __launch_bounds__(kThreads) k_embed_raw(EmbedArgs a, int lanes, int tiles)
+__global__ void __launch_bounds__(kRawThreads) k_embed_raw(EmbedArgs a, int sectors, uint32_t magic)
 {
-    constexpr int NV = 2;  // lines per lane
-    const int per_block = kThreads / lanes;
-    const int lane = threadIdx.x & (lanes - 1);
-    const int64_t items = a.n * tiles, step = (int64_t)gridDim.x * per_block;
     const uintptr_t lo = reinterpret_cast<uintptr_t>(a.rows), hi = lo + ((a.vocab - 1) * a.rows_stride + a.width) * sizeof(TI);
-    int64_t it = (int64_t)blockIdx.x * per_block + threadIdx.x / lanes;
-    auto position = [&](int64_t item) { return tiles == 1 ? item : item / tiles; };
-    int64_t next = it < items ? row_of(a, position(it)) : kPadRow;
-    bool bad = false;
-    for (; it < items; it += step) {
-        const int64_t i = position(it), r = next;
-        const TI *p = static_cast<const TI *>(a.rows) + r * a.rows_stride;
-        TO *q = static_cast<TO *>(a.out) + i * a.out_stride;
-        const int s = (int)((reinterpret_cast<uintptr_t>(q) & 15) / sizeof(TO));
-        const int c0 = ((int)(it - i * tiles) * lanes * NV + lane) * E - s;
-        Pack<TI, E> v[NV];
-        bool whole[NV];
+    const int64_t first = (int64_t)blockIdx.x * kRawThreads;
+    const int64_t i0 = first <= 0xffffffffll ? (int64_t)((uint32_t)first / (uint32_t)sectors) : first / sectors;
+    const uint32_t x = (uint32_t)(first - i0 * sectors) + threadIdx.x, d = sectors > 1 ? __umulhi(x, magic) : x;
+    const int64_t i = i0 + d;
+    if (i >= a.n) return;
+    const int64_t r = row_of(a, i);
+    TO *q = static_cast<TO *>(a.out) + i * a.out_stride;
+    const int c = (int)(x - d * sectors) * E - (int)((reinterpret_cast<uintptr_t>(q) & 31) / sizeof(TO));
+    q += c;
+    const TI *p = static_cast<const TI *>(a.rows) + r * a.rows_stride + c;
+    const uintptr_t from = reinterpret_cast<uintptr_t>(p) & ~(uintptr_t)15;
+    const uintptr_t to = (reinterpret_cast<uintptr_t>(p + E) + 15) & ~(uintptr_t)15;
+    const bool inside = from >= lo && to <= hi;
+    Lines<TI, E> in;
+    in.load(p, r >= 0 && inside);
+    if (r == kBadRow) *a.bad = 1;
+    Pack<TI, E> v;
+    in.shifted(p, v);
+    const int e0 = max(-c, 0), e1 = min(a.width - c, E);  // its elements e0 .. e1 are the row's
+    if (r >= 0 && !inside)
 #pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            const int c = c0 + k * lanes * E;
-            const uintptr_t from = reinterpret_cast<uintptr_t>(p + c) & ~(uintptr_t)15;
-            const uintptr_t to = (reinterpret_cast<uintptr_t>(p + c + E) + 15) & ~(uintptr_t)15;
-            whole[k] = c >= 0 && c + E <= a.width && (r < 0 || (from >= lo && to <= hi));
-            if (whole[k] && r >= 0) load_shifted<TI, E>(p + c, v[k]);
-        }
-        if (it + step < items) next = row_of(a, position(it + step));
-        bad = bad || r == kBadRow;
+        for (int e = 0; e < E; ++e)
+            if (e >= e0 && e < e1) v.v[e] = p[e];
+    // a row that is not there: +0 times the zeros that were not loaded
+    const float2 scale = both(r >= 0 ? a.scale : 0.0f);
+    Pack<TO, E> o;
 #pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            const int c = c0 + k * lanes * E;
-            if (whole[k]) {
-                Pack<TO, E> o;
-#pragma unroll
-                for (int e = 0; e < E; ++e) o.v[e] = from_f32<TO>(r >= 0 ? a.scale * to_f32(v[k].v[e]) : 0.0f);
-                store_pack<TO, E>(q + c, o);
-            } else {
-                for (int e = max(c, 0); e < min(c + E, a.width); ++e)
-                    q[e] = from_f32<TO>(r >= 0 ? a.scale * to_f32(p[e]) : 0.0f);
-            }
-        }
+    for (int e = 0; e < E; e += 2) set_pair(o.v + e, __fmul2_rn(scale, pair_of(v.v + e)));
+    if (e1 - e0 == E) {
+        store_sector(q, o);
+        return;
     }
-    if (bad) *a.bad = 1;
+    // its whole 4-byte words, and the elements of 2 bytes beside them
+    constexpr int PER = 4 / sizeof(TO);
+    const int w0 = (e0 + PER - 1) / PER, w1 = e1 / PER;
+    const uint32_t here = w1 > w0 ? (1u << w1) - (1u << w0) : 0;
+    const uint32_t *w = reinterpret_cast<const uint32_t *>(&o);
+#pragma unroll
+    for (int j = 0; j < E / PER; ++j)
+        if (here >> j & 1) reinterpret_cast<uint32_t *>(q)[j] = w[j];
+    if constexpr (PER == 2) {
+        if (e0 < e1 && (e0 & 1)) q[e0] = from_f32<TO>(r >= 0 ? a.scale * to_f32(p[e0]) : 0.0f);
+        if (e0 < e1 && (e1 & 1)) q[e1 - 1] = from_f32<TO>(r >= 0 ? a.scale * to_f32(p[e1 - 1]) : 0.0f);
+    }
 }
 
 // ---- the sort ---------------------------------------------------------------------
@@ -1019,16 +1039,22 @@ cudaError_t embed(const EmbedArgs &a, cudaStream_t s, int64_t *launches)
             using TI = decltype(ti);
             using TO = decltype(to);
             constexpr int E = kWide<TI, TO>;
-            const bool raw = pack_of(a, E) != E;
-            const int packs = raw ? 2 : 4;  // per lane
-            const int cols = a.width + (raw ? E - 1 : 0);  // a raw row begins inside its first line
-            int lanes = 1;
-            while (lanes < 32 && lanes * E * packs < cols) lanes <<= 1;
-            const int tiles = (cols + lanes * E * packs - 1) / (lanes * E * packs);
-            const int64_t want = (a.n * tiles * lanes + kThreads - 1) / kThreads;
-            const unsigned grid = (unsigned)std::min<int64_t>(want, 16 * kSMs);
-            if (raw) k_embed_raw<TI, TO, E><<<grid, kThreads, 0, s>>>(a, lanes, tiles);
-            else k_embed<TI, TO, E, 4><<<grid, kThreads, 0, s>>>(a, lanes, tiles);
+            if (pack_of(a, E) != E) {
+                constexpr int E = 32 / sizeof(TO);
+                const int sectors = (a.width + E - 1 + E - 1) / E;  // a row begins anywhere inside its first one
+                const int64_t blocks = (a.n * sectors + kRawThreads - 1) / kRawThreads;
+                if (blocks > 0x7fffffff) return cudaErrorInvalidValue;  // an output of 8 TB
+                // exact for the numbers below sectors + kRawThreads that it divides
+                const uint32_t magic = sectors > 1 ? 0xffffffffu / sectors + 1 : 0;
+                k_embed_raw<TI, TO, E><<<(unsigned)blocks, kRawThreads, 0, s>>>(a, sectors, magic);
+            } else {
+                constexpr int NV = 4;  // packs per lane
+                int lanes = 1;
+                while (lanes < 32 && lanes * E * NV < a.width) lanes <<= 1;
+                const int tiles = (a.width + lanes * E * NV - 1) / (lanes * E * NV);
+                const int64_t want = (a.n * tiles * lanes + kThreads - 1) / kThreads;
+                k_embed<TI, TO, E, NV><<<(unsigned)std::min<int64_t>(want, 16 * kSMs), kThreads, 0, s>>>(a, lanes, tiles);
+            }
             return cudaGetLastError();
         });
     });
