@@ -228,43 +228,55 @@ __device__ __forceinline__ uint2 entry(const EmbedArgs &a, const SortArgs &s, in
     return make_uint2((uint32_t)(r < 0 ? a.vocab : r), (uint32_t)i);
 }
 
-template <typename T>
-__device__ __forceinline__ void zero_row(char *p, int64_t bytes, int lane)
+// Zeros (all bits 0 in every type) for bytes at p, a multiple of 2, by a warp.
+__device__ __forceinline__ void zero_bytes(char *p, int64_t bytes, int lane)
 {
-    for (int64_t i = lane * sizeof(T); i < bytes; i += 32 * sizeof(T)) *reinterpret_cast<T *>(p + i) = T{};
+    const int head = (int)min((int64_t)(-reinterpret_cast<uintptr_t>(p) & 15), bytes);
+    const int64_t lines = (bytes - head) / 16;
+    const int tail = (int)(bytes - head) & 15;
+    if (2 * lane < head) reinterpret_cast<uint16_t *>(p)[lane] = 0;
+    p += head;
+    for (int64_t i = lane; i < lines; i += 32) reinterpret_cast<uint4 *>(p)[i] = uint4{};
+    if (2 * lane < tail) reinterpret_cast<uint16_t *>(p + 16 * lines)[lane] = 0;
 }
 
-// Zeros (all bits 0 in every type) for the rows that no position holds, in
-// this kernel's share [f0, f1) of kShares of the vocabulary.  warp of warps.
+// Zeros for the rows base + i, i < count, of the gradient whose bit i is not
+// set; warp of warps.  A run of such rows without gaps between them is one stretch of
+// bytes, so that narrow and unaligned rows are written in whole lines too: 1,000
+// positions over 131,072 x 16 bfloat16 24 -> 17 us, 5,000 over 58,391 x 1333 73 -> 56.
+__device__ void fill_rows(const EmbedArgs &a, const uint32_t *held, int64_t base, int64_t count, int64_t warp, int64_t warps)
+{
+    const int lane = threadIdx.x & 31;
+    const int size = a.out_dtype == HISS_F32 ? 4 : 2;
+    const int64_t bytes = (int64_t)a.width * size, stride = a.out_stride * size;
+    int rows = 32;  // per warp and turn: a power of two, so that they share a word
+    while (rows > 1 && count < warps * rows) rows >>= 1;
+    for (int64_t v = warp * rows; v < count; v += warps * rows) {
+        uint32_t empty = ~(held[v >> 5] >> (v & 31));
+        const int n = (int)min((int64_t)rows, count - v);
+        if (n < 32) empty &= (1u << n) - 1u;
+        while (empty) {
+            const int first = __ffs(empty) - 1;
+            const uint32_t rest = ~(empty >> first);  // its lowest bit: the run's end
+            const int run = stride != bytes ? 1 : rest ? __ffs(rest) - 1 : 32;
+            empty &= ~((run < 32 ? (1u << run) - 1u : ~0u) << first);
+            zero_bytes(static_cast<char *>(a.out) + (base + v + first) * stride, run * bytes, lane);
+        }
+    }
+}
+
+// The rows that no position holds, in this kernel's share [f0, f1) of kShares of the vocabulary.
 constexpr int kShares = 8, kScatterShare = 2;
 struct Fill {
     const uint32_t *present;
     int f0, f1;
-    int store;           // bytes per store that the gradient's rows allow
     int blocks;          // blocks of the kernel that do this, behind the others
 };
 __device__ void fill_empty(const EmbedArgs &a, const Fill &f, int64_t warp, int64_t warps)
 {
-    const int lane = threadIdx.x & 31;
     const int64_t words = (a.vocab + 31) / 32;
-    const int64_t v0 = words * f.f0 / kShares * 32, v1 = min(words * f.f1 / kShares * 32, a.vocab);
-    const int size = a.out_dtype == HISS_F32 ? 4 : 2;
-    const int64_t bytes = (int64_t)a.width * size, stride = a.out_stride * size;
-    int rows = 32;  // per warp and turn: a power of two, so that they share a word
-    while (rows > 1 && (v1 - v0) < warps * rows) rows >>= 1;
-    for (int64_t v = v0 + warp * rows; v < v1; v += warps * rows) {
-        uint32_t empty = ~(f.present[v >> 5] >> (v & 31));
-        if (rows < 32) empty &= (1u << rows) - 1u;
-        while (empty) {
-            const int64_t r = v + __ffs(empty) - 1;
-            empty &= empty - 1;
-            if (r >= v1) break;
-            char *p = static_cast<char *>(a.out) + r * stride;
-            if (f.store == 16) zero_row<uint4>(p, bytes, lane);
-            else if (f.store == 4) zero_row<uint32_t>(p, bytes, lane);
-            else zero_row<uint16_t>(p, bytes, lane);
-        }
-    }
+    const int64_t w0 = words * f.f0 / kShares, v1 = min(words * f.f1 / kShares * 32, a.vocab);
+    fill_rows(a, f.present + w0, 32 * w0, v1 - 32 * w0, warp, warps);
 }
 
 // First digit's counts of each tile, and which tokens occur.  Latency: 65,536
@@ -815,7 +827,6 @@ struct FewArgs {
     int lanes, tiles;    // lanes (a power of two) per row and tile; tiles of a row
     int sums;            // blocks that sum: one per position and tile
     int rows;            // rows of a fill block (the blocks behind those)
-    int store;           // bytes per store that the gradient's rows allow
 };
 
 // One kernel without a sort.  A block per position (and tile of columns): the
@@ -849,14 +860,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_grad_few(EmbedArgs a, FewArgs f
         for (int k = 0; k < kFewRound; ++k)
             if (r[k] >= v0 && r[k] < v1) atomicOr(&sh.held[(r[k] - v0) >> 5], 1u << ((r[k] - v0) & 31));
         __syncthreads();
-        const int size = sizeof(TO);
-        for (int64_t v = v0 + warp; v < v1; v += kThreads / 32) {
-            if (sh.held[(v - v0) >> 5] >> ((v - v0) & 31) & 1u) continue;
-            char *p = static_cast<char *>(a.out) + v * a.out_stride * size;
-            if (f.store == 16) zero_row<uint4>(p, (int64_t)a.width * size, lane);
-            else if (f.store == 4) zero_row<uint32_t>(p, (int64_t)a.width * size, lane);
-            else zero_row<uint16_t>(p, (int64_t)a.width * size, lane);
-        }
+        fill_rows(a, sh.held, v0, v1 - v0, warp, kThreads / 32);
         return;
     }
     const int pos = blockIdx.x / f.tiles, tile = blockIdx.x - pos * f.tiles;
@@ -982,16 +986,6 @@ cudaError_t with_types(const EmbedArgs &a, F &&f)
     });
 }
 
-// Bytes per store (16, 4 or 2) that the gradient's rows allow.
-int store_bytes(const EmbedArgs &a)
-{
-    for (int b : {16, 4}) {
-        const int e = b / (int)dtype_bytes(a.out_dtype);
-        if (a.width % e == 0 && rows_aligned(a.out, a.out_stride, a.out_dtype, e)) return b;
-    }
-    return 2;
-}
-
 struct GradLayout {
     int passes = 0, items = 1, tiles = 0, bins = 0;
     int unit = 0;
@@ -1075,7 +1069,6 @@ cudaError_t embed_grad(const EmbedArgs &a, void *tmp, uint32_t *present, cudaStr
             const int packs = f.lanes < kThreads ? 1 : kFewPacks;
             f.tiles = (a.width + f.lanes * E * packs - 1) / (f.lanes * E * packs);
             f.sums = (int)a.n * f.tiles;
-            f.store = store_bytes(a);
             // at least 4 fill blocks per SM
             f.rows = (int)std::min<int64_t>(kFewRows, std::max<int64_t>(1, a.vocab / (4 * kSMs)));
             const int64_t fills = a.accumulate ? 0 : (a.vocab + f.rows - 1) / f.rows;
@@ -1100,7 +1093,6 @@ cudaError_t embed_grad(const EmbedArgs &a, void *tmp, uint32_t *present, cudaStr
     // memory idle, and the rest beside the sums
     Fill f{};
     f.present = s.present;
-    f.store = store_bytes(a);
     auto fill_blocks = [&](int warps) {  // for the share f0 .. f1
         return (int)std::min<int64_t>(2 * kSMs, (a.vocab * (f.f1 - f.f0) / kShares + warps - 1) / warps);
     };
