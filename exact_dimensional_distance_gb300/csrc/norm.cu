@@ -14,8 +14,9 @@
 // into a shared-memory ring (cp.async), so the loads in flight cost no
 // registers: each thread copies its own packs where rows are aligned to 16
 // bytes, and no barrier guards the ring; a group copies the 16-byte lines that
-// hold a row of any other alignment.  Rows too wide for a group of kMaxLanes go through the looping
-// kernels at the end of the file.
+// hold a row of any other alignment.  Rows too wide for a group of kMaxLanes are
+// shared by two blocks, and those above 16,384 elements go through the looping kernels at
+// the end of the file.
 #include <algorithm>
 
 #include "hiss_internal.cuh"
@@ -100,6 +101,79 @@ __device__ __forceinline__ float inv_sqrt(float v)
 struct Exchange {
     float2 slot[2][kMaxWarps];
 };
+
+// ---- rows shared by two blocks -----------------------------------------------------
+// Rows too wide for a group of kMaxLanes are cut in two, a half for each block
+// of a cluster: the block's view of the operands is its half's columns, and
+// the warps' exchange of a row's sums reaches both blocks.  Backward, 3,825 x 12,032
+// float32: 128 us, against 262 in the looping kernels; 4,000 x 16,384 bfloat16 with
+// float32 dy 139 against 324; forward, 4,000 x 11,111 float32 121 against 128.  Bound
+// by the latency of a row, 2 us from one to the next: the sums, the barrier of the cluster,
+// and the sums over the warps.
+
+constexpr int kPair = 2;
+
+struct PairExchange {
+    float2 slot[2][kPair * kMaxWarps];
+};
+
+// The columns of the first half of a row, the longer one: every pack stays whole and aligned.
+__host__ __device__ __forceinline__ int first_half(int width) { return ((width + 1) / 2 + 15) & ~15; }
+
+template <typename T>
+__device__ __forceinline__ void advance(T *&p, int dtype, int64_t n)
+{
+    using C = std::conditional_t<std::is_const_v<T>, const char, char>;
+    if (p) p = static_cast<C *>(p) + n * (dtype == HISS_F32 ? 4 : 2);
+}
+
+// a's view of the columns of this block's half; returns its first column.
+__device__ __forceinline__ int take_half(NormArgs &a)
+{
+    const int half = first_half(a.width);
+    if (blockIdx.x % kPair == 0) {
+        a.width = half;
+        return 0;
+    }
+    a.width -= half;
+    advance(a.x, a.x_dtype, half);
+    advance(a.y, a.y_dtype, half);
+    advance(a.dy, a.y_dtype, half);
+    advance(a.dx, a.x_dtype, half);
+    advance(a.weight, a.p_dtype, half);
+    advance(a.bias, a.p_dtype, half);
+    advance(a.dweight, a.p_dtype, half);
+    advance(a.dbias, a.p_dtype, half);
+    return half;
+}
+
+// Barrier of the pair's threads; orders shared memory of both blocks.  Both
+// take the same rows, so that they meet equally often.
+__device__ __forceinline__ void pair_barrier()
+{
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+
+// v into *p of block `rank` of the pair (p: the same variable in this block).
+__device__ __forceinline__ void store_in_block(float2 *p, int rank, float2 v)
+{
+    asm volatile("{\n\t.reg .b32 q;\n\tmapa.shared::cluster.u32 q, %0, %1;\n\tst.shared::cluster.v2.f32 [q], {%2, %3};\n\t}" ::"r"(
+                     smem_u32(p)),
+                 "r"(rank), "f"(v.x), "f"(v.y)
+                 : "memory");
+}
+
+// Give every warp of the pair this warp's value; lane 16 r + w of a warp returns that
+// of warp w of block r (0 where there is none).
+__device__ __forceinline__ float2 pair_exchange(PairExchange &ex, const Group &g, int parity, float2 v)
+{
+    static_assert(kPair * kMaxWarps == 32, "a lane for every warp");
+    const int lane = threadIdx.x & 31;
+    float2 *slot = ex.slot[parity];
+    if (lane < kPair) store_in_block(slot + blockIdx.x % kPair * kMaxWarps + g.warp, lane, v);
+    pair_barrier();
+    return lane % kMaxWarps < g.warps ? slot[lane] : make_float2(0.0f, 0.0f);
+}
 
 // A lane's elements are handled as float32 pairs, in chunks: the pairs of a
 // pack, or two packs of one element.
@@ -212,12 +286,13 @@ struct Rows {
     int e = 0, nv = 0;     // elements per pack, packs per lane; e = 0: looping kernels
     int lanes = 0, groups = 0;
     bool narrow = false;
+    bool pair = false;     // a row per two blocks, lanes of each
     bool one_block = false;
 };
 
 // The widest pack that the width and every row's alignment allow; 16 elements
 // per lane, or 32 where that is too few and the caller has such a kernel for
-// the pack; as many groups per block as reach the given threads without leaving
+// the pack, or else two blocks per row; as many groups per block as reach the given threads without leaving
 // SMs idle.
 Rows plan_rows(const NormArgs &a, bool has32, bool has32_wide, int threads, bool one_block)
 {
@@ -237,8 +312,12 @@ Rows plan_rows(const NormArgs &a, bool has32, bool has32_wide, int threads, bool
     int per = 16;
     const bool can = e == wide ? has32_wide : has32;
     if (can && (a.width > per * kMaxLanes || (half && a.width > 512))) per = 32;
-    const int lanes = (a.width + per - 1) / per;
-    if (lanes > kMaxLanes) return r;
+    int lanes = (a.width + per - 1) / per;
+    if (lanes > kMaxLanes && !can) {
+        r.pair = true;
+        lanes = (first_half(a.width) + per - 1) / per;
+    }
+    if (lanes > kMaxLanes) return Rows{};
     r.e = e;
     r.nv = per / e;
     r.narrow = lanes <= 16;
@@ -385,14 +464,21 @@ struct Forward {
 // reads next.  Before float32 pairs, 32 elements per lane and products for divisions
 // it took 294 us and 25 instructions.  20,011 x 1021 float16 to float32: 31 us
 // (3.9 TB/s), bound by instructions, since the elements of odd 16-bit rows are read one by one.
-template <typename TX, typename TY, int E, int NV, bool NARROW>
+//
+// PAIR: two blocks per row.
+template <typename TX, typename TY, int E, int NV, bool NARROW, bool PAIR>
 __global__ void __launch_bounds__(kMaxLanes) k_norm(NormArgs a, int lanes, int groups)
 {
     using F = Forward<TX, E, NV, NARROW>;
     using PA = Params<NARROW, E, NV>;
     constexpr int S = F::kStages, C = NV * E, H = kPairs<E>, NC = kChunks<E, NV>;
     extern __shared__ __align__(16) char ring[];
-    __shared__ Exchange ex[kMaxWarps];
+    __shared__ std::conditional_t<PAIR, PairExchange, Exchange> ex[PAIR ? 1 : kMaxWarps];
+    const int row_width = a.width;
+    if constexpr (PAIR) {
+        take_half(a);
+        pair_barrier();  // both blocks are there
+    }
     const Group g = group_of<NARROW>(lanes);
     const int col = column_of<NARROW, E, NV>(g);
     const int vs = E * (NARROW ? lanes : 32);
@@ -403,8 +489,8 @@ __global__ void __launch_bounds__(kMaxLanes) k_norm(NormArgs a, int lanes, int g
     const int warp_col = NARROW ? 0 : g.warp * 32 * NV * E;
     auto any = [&](int c) { return warp_col + (E == 1 ? 2 * c : c) * vs < a.width; };
     const bool full = warp_col + NV * vs <= a.width;
-    const int64_t step = (int64_t)gridDim.x * groups;
-    int64_t row = (int64_t)blockIdx.x * groups + g.id;
+    const int64_t step = (int64_t)(gridDim.x / (PAIR ? kPair : 1)) * groups;
+    int64_t row = (int64_t)(blockIdx.x / (PAIR ? kPair : 1)) * groups + g.id;
     // the loop runs for whole warps: as long as the warp's first row exists
     int64_t first = row - (NARROW ? (threadIdx.x & 31) / lanes : 0);
     typename F::X xs;
@@ -421,11 +507,17 @@ __global__ void __launch_bounds__(kMaxLanes) k_norm(NormArgs a, int lanes, int g
     w.open(g, a.weight, a.p_dtype, 1.0f, col, vs, a.width, params);
     b.open(g, a.bias, a.p_dtype, 0.0f, col, vs, a.width, params + PA::kLaneBytes * lanes);
     if constexpr (PA::kShared) __syncthreads();
-    const float inv_width = 1.0f / (float)a.width;
+    const float inv_width = 1.0f / (float)row_width;
     // columns of this thread's warp, and of warp (lane id) of the group
-    auto columns = [&](int i) { return (float)min(max(a.width - i * 32 * C, 0), 32 * C); };
-    const float my_n = NARROW ? (float)a.width : columns(g.warp), inv_my_n = my_n > 0.0f ? 1.0f / my_n : 0.0f;
-    const float lane_n = NARROW ? 0.0f : columns(threadIdx.x & 31);
+    auto columns = [&](int width, int i) { return (float)min(max(width - i * 32 * C, 0), 32 * C); };
+    const float my_n = NARROW ? (float)a.width : columns(a.width, g.warp), inv_my_n = my_n > 0.0f ? 1.0f / my_n : 0.0f;
+    float lane_n = 0.0f;
+    if constexpr (PAIR) {
+        const int half = first_half(row_width), l = threadIdx.x & 31;
+        lane_n = columns(l < kMaxWarps ? half : row_width - half, l % kMaxWarps);
+    } else if (!NARROW) {
+        lane_n = columns(a.width, threadIdx.x & 31);
+    }
     int st = 0;
     int parity = 0;
     // one row; FULL: no column to be left out
@@ -468,7 +560,12 @@ __global__ void __launch_bounds__(kMaxLanes) k_norm(NormArgs a, int lanes, int g
                 }
         }
         float q = warp_sum<NARROW>(g, q2.x + q2.y);
-        if (!NARROW && g.warps > 1) {
+        if constexpr (PAIR) {
+            const float2 mine = pair_exchange(ex[0], g, parity, make_float2(mean, q));
+            mean = warp_sum<false>(g, lane_n * mine.x) * inv_width;
+            const float d = mine.x - mean;
+            q = warp_sum<false>(g, lane_n > 0.0f ? fmaf(lane_n * d, d, mine.y) : 0.0f);
+        } else if (!NARROW && g.warps > 1) {
             float2 *slot = ex[g.id].slot[parity];
             if ((threadIdx.x & 31) == 0) slot[g.warp] = make_float2(mean, q);
             group_barrier(g);
@@ -492,7 +589,7 @@ __global__ void __launch_bounds__(kMaxLanes) k_norm(NormArgs a, int lanes, int g
                     r[h] = __ffma2_rn(__fmul2_rn(__fadd2_rn(x[c][h], both(-mean)), both(rstd)), tw[h], tb[h]);
                 store_chunk<TY, E>(y, c, vs, FULL || has_second(c), r);
             }
-            if (g.lane == 0) {
+            if (g.lane == 0 && (!PAIR || blockIdx.x % kPair == 0)) {
                 if (a.mean) a.mean[row] = mean;
                 if (a.rstd) a.rstd[row] = rstd;
             }
@@ -534,15 +631,22 @@ struct Backward {
 //
 // Each block leaves its column sums in part[block][0 .. width) (dw) and
 // [width .. 2 width) (db): k_norm_param adds the blocks up.  direct: the only block
-// writes dweight and dbias itself.  x_bytes: of x's ring.
-template <typename TX, typename TY, int E, int NV, bool NARROW>
+// writes dweight and dbias itself.  x_bytes: of x's ring.  PAIR: two blocks per row.
+template <typename TX, typename TY, int E, int NV, bool NARROW, bool PAIR>
 __global__ void __launch_bounds__(kMaxLanes) k_norm_grad(NormArgs a, int lanes, int groups, int x_bytes, float *part, bool direct)
 {
     using B = Backward<TX, TY, E, NV, NARROW>;
     using PA = Params<NARROW, E, NV>;
     constexpr int S = B::kStages, H = kPairs<E>, NC = kChunks<E, NV>;
     extern __shared__ __align__(16) char ring[];
-    __shared__ Exchange ex[kMaxWarps];
+    __shared__ std::conditional_t<PAIR, PairExchange, Exchange> ex[PAIR ? 1 : kMaxWarps];
+    const int row_width = a.width;
+    const int block = blockIdx.x / (PAIR ? kPair : 1), blocks = gridDim.x / (PAIR ? kPair : 1);
+    if constexpr (PAIR) {
+        const int first_col = take_half(a);
+        if (part) part += first_col;
+        pair_barrier();  // both blocks are there
+    }
     const Group g = group_of<NARROW>(lanes);
     const int col = column_of<NARROW, E, NV>(g);
     const int vs = E * (NARROW ? lanes : 32);
@@ -553,8 +657,8 @@ __global__ void __launch_bounds__(kMaxLanes) k_norm_grad(NormArgs a, int lanes, 
     const int warp_col = NARROW ? 0 : g.warp * 32 * NV * E;
     auto any = [&](int c) { return warp_col + (E == 1 ? 2 * c : c) * vs < a.width; };
     const bool full = warp_col + NV * vs <= a.width;
-    const int64_t step = (int64_t)gridDim.x * groups;
-    int64_t row = (int64_t)blockIdx.x * groups + g.id;
+    const int64_t step = (int64_t)blocks * groups;
+    int64_t row = (int64_t)block * groups + g.id;
     int64_t first = row - (NARROW ? (threadIdx.x & 31) / lanes : 0);
     typename B::X xs;
     typename B::Y ys;
@@ -579,7 +683,7 @@ __global__ void __launch_bounds__(kMaxLanes) k_norm_grad(NormArgs a, int lanes, 
     for (int c = 0; c < NC; ++c)
 #pragma unroll
         for (int h = 0; h < H; ++h) dw[c][h] = db[c][h] = both(0.0f);
-    const float inv_width = 1.0f / (float)a.width;
+    const float inv_width = 1.0f / (float)row_width;
     float mean_n = row < a.n ? a.mean[row] : 0.0f, rstd_n = row < a.n ? a.rstd[row] : 0.0f;
     int st = 0;
     int parity = 0;
@@ -625,7 +729,11 @@ __global__ void __launch_bounds__(kMaxLanes) k_norm_grad(NormArgs a, int lanes, 
         }
         if (a.dx) {
             float sg = warp_sum<NARROW>(g, sg2.x + sg2.y), sgh = warp_sum<NARROW>(g, sgh2.x + sgh2.y);
-            if (!NARROW && g.warps > 1) {
+            if constexpr (PAIR) {
+                const float2 mine = pair_exchange(ex[0], g, parity, make_float2(sg, sgh));
+                sg = warp_sum<false>(g, mine.x);
+                sgh = warp_sum<false>(g, mine.y);
+            } else if (!NARROW && g.warps > 1) {
                 float2 *slot = ex[g.id].slot[parity];
                 if ((threadIdx.x & 31) == 0) slot[g.warp] = make_float2(sg, sgh);
                 group_barrier(g);
@@ -711,12 +819,12 @@ __global__ void __launch_bounds__(kMaxLanes) k_norm_grad(NormArgs a, int lanes, 
                 if (c1 < a.width && a.dbias) store_any(a.dbias, a.p_dtype, c1, db[c][h].y);
             }
     } else if (unit == 0 && lane < lanes) {
-        float *p = part + (int64_t)blockIdx.x * 2 * a.width + col;
+        float *p = part + (int64_t)block * 2 * row_width + col;
 #pragma unroll
         for (int c = 0; c < NC; ++c)
             if (has(c)) {
                 store_chunk<float, E>(p, c, vs, has_second(c), dw[c]);
-                store_chunk<float, E>(p + a.width, c, vs, has_second(c), db[c]);
+                store_chunk<float, E>(p + row_width, c, vs, has_second(c), db[c]);
             }
     }
     let_next_start();
@@ -749,10 +857,8 @@ __global__ void __launch_bounds__(1024) k_norm_param(NormArgs a, const float *pa
 }
 
 // ---- rows of any width and alignment, read again for each pass ---------------------
-// For rows too wide for a group: above 16,384 elements (8,192 with a float32
-// operand in the backward pass or unaligned float32 rows).  A block per row, the
-// second and third reading from L2; 5,437 x 9594 bfloat16 took 98 us here and
-// takes 73 in k_norm.
+// For rows above 16,384 elements.  A block per row, the second and third reading
+// from L2; 5,437 x 9594 bfloat16 took 98 us here and takes 73 in k_norm.
 
 constexpr int kLoopThreads = 512;
 constexpr int kLoopSplits = 64;  // row ranges of the column sums
@@ -852,17 +958,20 @@ cudaError_t with_xy(const NormArgs &a, F &&f)
 template <int V>
 using Int = std::integral_constant<int, V>;
 
-// f(E, NV, NARROW) for the packs of r.
+// f(E, NV, NARROW, PAIR) for the packs of r.
 template <typename TX, bool HAS32, bool HAS32_WIDE, typename F>
 cudaError_t with_packs(const Rows &r, F &&f)
 {
     constexpr int W = 16 / (int)sizeof(TX);
     auto with_width = [&](auto e) {
         constexpr int E = decltype(e)::value;
-        if constexpr (E == W ? HAS32_WIDE : HAS32)
-            if (r.e * r.nv == 32) return f(e, Int<32 / E>{}, std::false_type{});
-        if (r.narrow) return f(e, Int<16 / E>{}, std::true_type{});
-        return f(e, Int<16 / E>{}, std::false_type{});
+        if constexpr (E == W ? HAS32_WIDE : HAS32) {
+            if (r.e * r.nv == 32) return f(e, Int<32 / E>{}, std::false_type{}, std::false_type{});
+        } else {
+            if (r.pair) return f(e, Int<16 / E>{}, std::false_type{}, std::true_type{});
+        }
+        if (r.narrow) return f(e, Int<16 / E>{}, std::true_type{}, std::false_type{});
+        return f(e, Int<16 / E>{}, std::false_type{}, std::false_type{});
     };
     if (r.e == W) return with_width(Int<W>{});
     if constexpr (W == 8)
@@ -870,10 +979,34 @@ cudaError_t with_packs(const Rows &r, F &&f)
     return with_width(Int<1>{});
 }
 
+// Blocks, or pairs of blocks (an even number of SMs share a cluster's place,
+// so that all of them find room).
 unsigned grid_for(const NormArgs &a, const Rows &r, int per_sm)
 {
-    const int64_t want = (a.n + r.groups - 1) / r.groups;
-    return (unsigned)(want < (int64_t)kSMs * per_sm ? want : (int64_t)kSMs * per_sm);
+    const int64_t want = (a.n + r.groups - 1) / r.groups, room = (int64_t)kSMs * per_sm / (r.pair ? kPair : 1);
+    return (unsigned)(want < room ? want : room);
+}
+
+template <typename... P, typename... A>
+cudaError_t launch_rows(void (*kernel)(P...), const Rows &r, unsigned grid, size_t smem, cudaStream_t s, const A &...args)
+{
+    const unsigned threads = r.lanes * r.groups;
+    if (!r.pair) {
+        kernel<<<grid, threads, smem, s>>>(static_cast<P>(args)...);
+        return cudaGetLastError();
+    }
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(kPair * grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = kPair;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
 }
 
 Rows plan_forward(const NormArgs &a) { return plan_rows(a, a.x_dtype != HISS_F32, true, 256, false); }
@@ -903,18 +1036,16 @@ cudaError_t layer_norm(const NormArgs &a, cudaStream_t s, int64_t *launches)
             k_norm_loop<TX, TY><<<(unsigned)a.n, kLoopThreads, 0, s>>>(a);
             return cudaGetLastError();
         }
-        return with_packs<TX, sizeof(TX) == 2, true>(r, [&](auto e, auto nv, auto narrow) {
+        return with_packs<TX, sizeof(TX) == 2, true>(r, [&](auto e, auto nv, auto narrow, auto pair) {
             constexpr int E = decltype(e)::value, NV = decltype(nv)::value;
             constexpr bool NARROW = decltype(narrow)::value;
             static Residency cache;
-            auto kernel = k_norm<TX, TY, E, NV, NARROW>;
+            auto kernel = k_norm<TX, TY, E, NV, NARROW, decltype(pair)::value>;
             const int threads = r.lanes * r.groups;
-            const size_t smem = Forward<TX, E, NV, NARROW>::smem(threads, r.lanes, a.width);
+            const size_t smem = Forward<TX, E, NV, NARROW>::smem(threads, r.lanes, r.pair ? first_half(a.width) : a.width);
             int per_sm = 1;
             HISS_TRY(resident(kernel, threads, smem, cache, &per_sm));
-            const unsigned grid = grid_for(a, r, per_sm);
-            kernel<<<grid, threads, smem, s>>>(a, r.lanes, r.groups);
-            return cudaGetLastError();
+            return launch_rows(kernel, r, grid_for(a, r, per_sm), smem, s, a, r.lanes, r.groups);
         });
     });
 }
@@ -949,21 +1080,21 @@ cudaError_t layer_norm_grad(const NormArgs &a, void *tmp, cudaStream_t s, int64_
                 }
                 return cudaGetLastError();
             }
-            return with_packs<TX, sizeof(TY) == 2, sizeof(TY) == 2>(r, [&](auto e, auto nv, auto narrow) {
+            return with_packs<TX, sizeof(TY) == 2, sizeof(TY) == 2>(r, [&](auto e, auto nv, auto narrow, auto pair) {
                 constexpr int E = decltype(e)::value, NV = decltype(nv)::value;
                 static std::atomic<uint64_t> allowed{0};
-                auto kernel = k_norm_grad<TX, TY, E, NV, decltype(narrow)::value>;
+                auto kernel = k_norm_grad<TX, TY, E, NV, decltype(narrow)::value, decltype(pair)::value>;
                 const int threads = r.lanes * r.groups;
                 const bool many = threads > (r.narrow ? 32 : r.lanes);  // sums of several warps or groups to add up
                 using B = Backward<TX, TY, E, NV, decltype(narrow)::value>;
-                const size_t smem = B::smem(threads, r.lanes, a.width, many);
+                const int width = r.pair ? first_half(a.width) : a.width;  // of a block
+                const size_t smem = B::smem(threads, r.lanes, width, many);
                 HISS_TRY(allow_shared(kernel, kSharedBytes, allowed));
                 parts = grad_grid(a, r);
                 direct = r.one_block;
-                kernel<<<parts, threads, smem, s>>>(a, r.lanes, r.groups, (int)B::X::bytes(threads, r.lanes, a.width),
-                                                  r.one_block ? nullptr : part, r.one_block);
                 ++*launches;
-                return cudaGetLastError();
+                return launch_rows(kernel, r, parts, smem, s, a, r.lanes, r.groups, (int)B::X::bytes(threads, r.lanes, width),
+                                   r.one_block ? nullptr : part, r.one_block);
             });
         }));
     }

@@ -433,6 +433,32 @@ def test_layer_norm_grad(lib, shape, types):
         assert all(torch.equal(a, b) for a, b in zip(again, once)), "not repeatable"
 
 
+# rows cut in two, up to the widest and beyond; one, two, three, some and many rows; a
+# half that ends inside a pack, a warp or a group
+WIDE_SHAPES = [(1, 8193), (2, 8200), (3, 8704), (77, 9000), (200, 12345), (301, 8208), (153, 16384), (160, 16382),
+               (9, 16368), (5, 16385), (3, 16400)]
+
+
+@pytest.mark.parametrize("shape", WIDE_SHAPES)
+@pytest.mark.parametrize("types", [(F32, F32), (BF16, F32), (F16, F32), (BF16, BF16)])
+def test_layer_norm_wide_rows(lib, shape, types):
+    n, d = shape
+    g = _gen(n, d, str(types), 2)
+    x = _normal((n, d), types[0], g, 1.5, 0.7)
+    dy = _normal((n, d), types[1], g, 1.0, 0.2)
+    w, b = _normal((d,), F32, g, 0.3, 1.0), _normal((d,), F32, g)
+    for extra, off in [(0, 0), (3, 1), (16, 16)]:
+        xs, dys = _laid(x, extra, off), _laid(dy, extra, off)
+        y, mean, rstd = lib.layer_norm(xs, w, b, dtype=types[1])
+        for got, (wv, ev), what in zip((y, mean, rstd), _norm_ref(x, w, b, 1e-5), ("y", "mean", "rstd")):
+            _close(got, wv, ev, what)
+        got = lib.layer_norm_grad(dys, xs, mean, rstd, w)
+        for got1, (wv, ev), what in zip(got, _norm_grad_ref(dy, x, mean, rstd, w), ("dx", "dw", "db")):
+            _close(got1, wv, ev, what)
+        again = lib.layer_norm_grad(dys, xs, mean, rstd, w)
+        assert all(torch.equal(p, q) for p, q in zip(got, again)), "not repeatable"
+
+
 def test_layer_norm_grad_edges(edd, lib):
     g = _gen(4)
     d = 96
