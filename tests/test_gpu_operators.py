@@ -280,6 +280,10 @@ def test_offsets_beyond_32_bits(edd, lib):
     x += (torch.arange(width, device="cuda") % 2).to(BF16)
     last = torch.tensor([0, 1, rows - 1, rows - 2, (1 << 31) // width + 1], device="cuda")
     assert torch.equal(lib.embed(last, x), x[last])
+    odd = lib.embed(torch.arange(rows, device="cuda"), x[:, 1:1036])  # unaligned rows in and out
+    assert odd.numel() > 1 << 31
+    assert all(torch.equal(odd[i:i + step], x[i:i + step, 1:1036]) for i in range(0, rows, step))
+    del odd
     y, mean, rstd = lib.layer_norm(x)
     want = lib.layer_norm(x[last].contiguous())
     assert torch.equal(y[last], want[0]) and torch.equal(mean[last], want[1]) and torch.equal(rstd[last], want[2])
