@@ -538,8 +538,9 @@ constexpr int kManyUnits = 64;  // a run over more units is summed by a whole bl
 
 // The sums of the runs.  65,536 positions x 1024 bfloat16 over 50,001 float32 rows,
 // with half of the empty rows' zeros: 49 us at 4.7 TB/s, bound by memory.  262,144 x
-// 322 float16, rows aligned to 4 bytes: 56 us, bound by instructions (187 per
-// row).  Rows wait in a shared-memory ring, and there is one copy of the code that writes a
+// 322 float16, rows aligned to 4 bytes, bound by instructions: the call 66 us; 74
+// with every row's address computed by the whole warp when it comes up, not by one lane each
+// beforehand.  Rows wait in a shared-memory ring, and there is one copy of the code that writes a
 // finished row: inside a loop unrolled over the rows it made the kernel take 93 us.
 template <typename TI, typename TO, int E, bool BIG>
 __global__ void __launch_bounds__(kThreads) k_sum(EmbedArgs a, SumArgs s, Fill f)
@@ -599,15 +600,18 @@ __global__ void __launch_bounds__(kThreads) k_sum(EmbedArgs a, SumArgs s, Fill f
     // raw: lines that reach outside the matrix are copied by element: they belong
     // to the first and last rows
     const uint32_t edge = a.rows_stride > 0 ? (uint32_t)((15 + a.rows_stride) / a.rows_stride) : 0x7fffffffu;
-    const uint32_t rows_at = (uint32_t)reinterpret_cast<uintptr_t>(rows), rows_by = (uint32_t)a.rows_stride * (uint32_t)sizeof(TI);
-    // start copying row y into place st of the ring
-    auto copy = [&](uint32_t y, int st) {
-        const TI *p = rows + (int64_t)y * a.rows_stride;
+    // the address of row y, with bit 0 (raw) set for those
+    auto place = [&](uint32_t y) {
+        const uint64_t p = reinterpret_cast<uint64_t>(rows + (int64_t)y * a.rows_stride);
+        return RAW && !(y >= edge && y + edge < (uint32_t)n) ? p | 1 : p;
+    };
+    // start copying the row at a place into slot st of the ring
+    auto copy = [&](uint64_t at, int st) {
         char *d = group_ring + st * row_bytes;
         if constexpr (RAW) {
-            const int off = (int)((rows_at + y * rows_by) & 15), bytes = off + cols * (int)sizeof(TI);
-            const char *q = reinterpret_cast<const char *>(p) - off;
-            if (y >= edge && y + edge < (uint32_t)n) {
+            const int off = (int)at & 14, bytes = off + cols * (int)sizeof(TI);
+            const char *q = reinterpret_cast<const char *>(at & ~(uint64_t)15);
+            if (!(at & 1)) {
                 if constexpr (BIG) {
 #pragma unroll
                     for (int k = 0; k < (512 * (int)sizeof(TI) + 15 + 511) / 512; ++k) {
@@ -619,7 +623,7 @@ __global__ void __launch_bounds__(kThreads) k_sum(EmbedArgs a, SumArgs s, Fill f
                 }
             } else {
                 const uintptr_t lo = reinterpret_cast<uintptr_t>(a.rows), hi = lo + ((a.n - 1) * a.rows_stride + a.width) * sizeof(TI);
-                const uintptr_t b0 = reinterpret_cast<uintptr_t>(p), b1 = b0 + cols * sizeof(TI), line0 = b0 - off;
+                const uintptr_t line0 = at & ~(uint64_t)15, b0 = line0 + off, b1 = b0 + cols * sizeof(TI);
                 for (int b = 16 * lane; b < bytes; b += 16 * lanes) {
                     if (line0 + b >= lo && line0 + b + 16 <= hi) {
                         cp_async16(d + b, q + b);
@@ -630,6 +634,7 @@ __global__ void __launch_bounds__(kThreads) k_sum(EmbedArgs a, SumArgs s, Fill f
                 }
             }
         } else {
+            const TI *p = reinterpret_cast<const TI *>(at);
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
                 const int c = (k * lanes + lane) * E;
@@ -641,10 +646,10 @@ __global__ void __launch_bounds__(kThreads) k_sum(EmbedArgs a, SumArgs s, Fill f
     float acc[C];
 #pragma unroll
     for (int c = 0; c < C; ++c) acc[c] = 0.0f;
-    // add row y, which is in place st
-    auto add = [&](uint32_t y, int st) {
+    // add the row in slot st; at: the low bits of its place
+    auto add = [&](uint32_t at, int st) {
         const char *d = group_ring + st * row_bytes;
-        if constexpr (RAW) d += (rows_at + y * rows_by) & 15;
+        if constexpr (RAW) d += at & 14;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             if (k * lanes * E >= cols) break;
@@ -674,23 +679,24 @@ __global__ void __launch_bounds__(kThreads) k_sum(EmbedArgs a, SumArgs s, Fill f
     };
     const int m = end - i;  // positions, at most two units
     if constexpr (BIG) {
-        // the positions (at most 64) are held by the warp's lanes, and where a run
-        // ends in a mask
-        uint2 it[2];
+        // the rows' places (at most 64) wait in shared memory, the tokens in the
+        // warp's lanes, and where a run ends in a mask
+        __shared__ uint64_t where[kThreads / 32][64];
+        uint64_t *const place_of = where[threadIdx.x / 32];
+        uint32_t it[2];
         uint64_t ends = 0;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int j = i + 32 * h + lane;
-            it[h] = j < end ? s.items[j] : make_uint2(none, 0);
+            const uint2 item = j < end ? s.items[j] : make_uint2(none, 0);
+            it[h] = item.x;
+            if (j < end) place_of[32 * h + lane] = place(item.y);
             const uint32_t after = j + 1 < end ? s.items[j + 1].x : none;
-            ends |= (uint64_t)__ballot_sync(0xffffffffu, it[h].x != after) << (32 * h);
+            ends |= (uint64_t)__ballot_sync(0xffffffffu, item.x != after) << (32 * h);
         }
-        auto y_of = [&](int j) {
-            const uint32_t y0 = __shfl_sync(0xffffffffu, it[0].y, j & 31), y1 = __shfl_sync(0xffffffffu, it[1].y, j & 31);
-            return j < 32 ? y0 : y1;
-        };
+        __syncwarp();
         for (int k = 0; k < A - 1; ++k) {
-            if (k < m) copy(y_of(k), k);
+            if (k < m) copy(place_of[k], k);
             cp_async_commit();
         }
         for (int j = 0; j < m; ++j) {
@@ -698,27 +704,27 @@ __global__ void __launch_bounds__(kThreads) k_sum(EmbedArgs a, SumArgs s, Fill f
             // raw: the row was copied by the whole warp, and the row before it has been
             // read by the whole warp before its place in the ring is filled again
             if (RAW) __syncwarp();
-            if (j + A - 1 < m) copy(y_of(j + A - 1), (j + A - 1) & (A - 1));
+            if (j + A - 1 < m) copy(place_of[j + A - 1], (j + A - 1) & (A - 1));
             cp_async_commit();
-            add(RAW ? y_of(j) : 0u, j & (A - 1));
+            add(RAW ? (uint32_t)place_of[j] : 0u, j & (A - 1));
             if (ends >> j & 1) {
-                const uint32_t x0 = __shfl_sync(0xffffffffu, it[0].x, j & 31), x1 = __shfl_sync(0xffffffffu, it[1].x, j & 31);
+                const uint32_t x0 = __shfl_sync(0xffffffffu, it[0], j & 31), x1 = __shfl_sync(0xffffffffu, it[1], j & 31);
                 flush(j < 32 ? x0 : x1, j + 1 == m);
             }
         }
     } else {
         const uint32_t mask = lanes == 32 ? 0xffffffffu : ((1u << lanes) - 1u) << (threadIdx.x & 31 & ~(lanes - 1));
         for (int k = 0; k < A - 1; ++k) {
-            if (k < m) copy(s.items[i + k].y, k);
+            if (k < m) copy(place(s.items[i + k].y), k);
             cp_async_commit();
         }
         uint2 it = s.items[i];
         for (int j = 0; j < m; ++j) {
             cp_async_wait<A - 2>();
             if (RAW) __syncwarp(mask);
-            if (j + A - 1 < m) copy(s.items[i + j + A - 1].y, (j + A - 1) & (A - 1));
+            if (j + A - 1 < m) copy(place(s.items[i + j + A - 1].y), (j + A - 1) & (A - 1));
             cp_async_commit();
-            add(it.y, j & (A - 1));
+            add(RAW ? (uint32_t)place(it.y) : 0u, j & (A - 1));
             const uint32_t key = it.x;
             it = j + 1 < m ? s.items[i + j + 1] : make_uint2(none, 0);
             if (it.x != key) flush(key, j + 1 == m);
