@@ -1146,7 +1146,13 @@ cudaError_t embed_grad(const EmbedArgs &a, void *tmp, uint32_t *present, cudaStr
             using S = SumShape<TI, E, BIG>;
             auto kernel = k_sum<TI, TO, E, BIG>;
             for (m.lanes = BIG ? 32 : 1; m.lanes < 32 && m.lanes * S::C < a.width;) m.lanes <<= 1;
-            m.tiles = (a.width + m.lanes * S::C - 1) / (m.lanes * S::C);
+            // shorter tiles where fewer lanes of the last one are idle: 115,404 x 132 bfloat16
+            // 56 -> 49 us, 166,078 x 141 float32 97 -> 86 (91 with at least 16 lanes)
+            auto tiles = [&](int lanes) { return (a.width + lanes * S::C - 1) / (lanes * S::C); };
+            if (!BIG)
+                for (int l = m.lanes / 2; l >= 8; l /= 2)
+                    if (tiles(l) * l < tiles(m.lanes) * m.lanes) m.lanes = l;
+            m.tiles = tiles(m.lanes);
             m.blocks = (int)((l.units * m.tiles + kThreads / m.lanes - 1) / (kThreads / m.lanes));
             static std::atomic<uint64_t> allowed{0};
             HISS_TRY(allow_shared(kernel, 128 * 1024, allowed));
