@@ -540,7 +540,9 @@ class Join:
     # operators between a model's parameters and the points: asynchronous on
     # the context's stream (``finish`` waits).  Called with another current
     # stream, that stream's earlier work is waited for on the device first and
-    # its later work waits for the call.
+    # its later work waits for the call.  They can be captured in a graph after
+    # a call of the same sizes that was not; the graph is replayed on the context's
+    # stream, or ordered with it, while the Join is open.
 
     def _enqueue(self, fn, args, what, tensors):
         """fn(context, *args): tensors are those that it reads or writes."""

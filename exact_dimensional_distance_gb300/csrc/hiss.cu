@@ -22,6 +22,18 @@ struct DBuf {
     size_t cap = 0;
 };
 
+// A workspace of the operators.  Graphs replay the addresses that were captured, so
+// a buffer that a captured call uses is never freed before the context is.
+struct OpBuf : DBuf {
+    bool captured = false;
+};
+
+// Such a buffer after a later call needed a larger one.
+struct Kept {
+    DBuf buf;
+    Kept *next;
+};
+
 template <typename T>
 T *as(DBuf &b) { return static_cast<T *>(b.p); }
 
@@ -93,7 +105,8 @@ struct hiss_ctx {
     // operators on parameters and activations: workspace, counters of the
     // clipping and flags of the embedding gradient that every call leaves zero, and
     // a device int that records an out-of-range token until hiss_finish reads it
-    DBuf op_tmp, op_clip, op_present, op_bad;
+    OpBuf op_tmp, op_clip, op_present, op_bad;
+    Kept *op_kept = nullptr;
 
     hiss_stats st{};
     cudaEvent_t ev[8] = {};
@@ -1256,12 +1269,45 @@ int embed_args_ok(const EmbedArgs &a, int64_t rows_n, int64_t out_n)
     return HISS_OK;
 }
 
-// A buffer that is zero when it is new.
-int ensure_zeroed(hiss_ctx *ctx, DBuf &b, size_t bytes)
+// Whether the context's stream is being captured; HISS_E_STATE where nothing can be
+// put on it (an invalidated capture, the legacy stream beside another's capture).
+int is_capturing(hiss_ctx *ctx, bool *yes)
 {
-    if (b.cap >= bytes) return HISS_OK;
-    ST(ensure(ctx, b, bytes));
-    CK(cudaMemsetAsync(b.p, 0, b.cap, ctx->stream));
+    cudaStreamCaptureStatus st = cudaStreamCaptureStatusNone;
+    const cudaError_t e = cudaStreamIsCapturing(ctx->stream, &st);
+    if (e == cudaErrorStreamCaptureImplicit || st == cudaStreamCaptureStatusInvalidated) {
+        cudaGetLastError();
+        return HISS_E_STATE;
+    }
+    CK(e);
+    *yes = st == cudaStreamCaptureStatusActive;
+    return HISS_OK;
+}
+
+// An operator's workspace of at least the given bytes, all zero when it is new if
+// wanted.  An allocation cannot be captured (it would belong to the graph, not to the
+// context): HISS_E_STATE before anything is put on the stream.
+int ensure_op(hiss_ctx *ctx, OpBuf &b, size_t bytes, bool zeroed, bool capturing)
+{
+    if (bytes == 0) return HISS_OK;
+    if (b.cap < bytes) {
+        if (capturing) return HISS_E_STATE;
+        Kept *k = b.captured ? new (std::nothrow) Kept{b, ctx->op_kept} : nullptr;
+        if (b.captured && !k) return HISS_E_NOMEM;
+        DBuf fresh;
+        if (!k) fresh = b;
+        const int rc = ensure(ctx, fresh, bytes);
+        if (rc != HISS_OK) {
+            if (!k) static_cast<DBuf &>(b) = fresh;
+            delete k;
+            return rc;
+        }
+        if (k) ctx->op_kept = k;
+        static_cast<DBuf &>(b) = fresh;
+        b.captured = false;
+        if (zeroed) CK(cudaMemsetAsync(b.p, 0, b.cap, ctx->stream));
+    }
+    b.captured = b.captured || capturing;
     return HISS_OK;
 }
 
@@ -1318,6 +1364,11 @@ void hiss_destroy(hiss_ctx *ctx)
                    &ctx->query_ids2, &ctx->query_rows2, &ctx->op_tmp, &ctx->op_clip, &ctx->op_present, &ctx->op_bad};
     if (ctx->copy_stream) cudaStreamSynchronize(ctx->copy_stream);
     for (DBuf *b : all) release(ctx, *b);
+    while (Kept *k = ctx->op_kept) {
+        ctx->op_kept = k->next;
+        release(ctx, k->buf);
+        delete k;
+    }
     cudaStreamSynchronize(ctx->stream);
     if (ctx->h_pinned) cudaFreeHost(ctx->h_pinned);
     if (ctx->h_pinned2) cudaFreeHost(ctx->h_pinned2);
@@ -1583,7 +1634,9 @@ int hiss_embed(hiss_ctx *ctx, const void *d_table, int32_t table_dtype, int64_t 
                 d_out, out_dtype, out_stride, 0, nullptr};
     ST(embed_args_ok(a, vocab, n));
     if (n == 0) return HISS_OK;
-    ST(ensure_zeroed(ctx, ctx->op_bad, sizeof(int)));
+    bool capturing = false;
+    ST(is_capturing(ctx, &capturing));
+    ST(ensure_op(ctx, ctx->op_bad, sizeof(int), true, capturing));
     a.bad = as<int>(ctx->op_bad);
     CK(embed(a, ctx->stream, &ctx->launches));
     return HISS_OK;
@@ -1598,10 +1651,12 @@ int hiss_embed_grad(hiss_ctx *ctx, const void *d_dy, int32_t dy_dtype, int64_t d
                 d_grad, grad_dtype, grad_stride, accumulate, nullptr};
     if (accumulate != 0 && accumulate != 1) return HISS_E_ARG;
     ST(embed_args_ok(a, n, vocab));
-    ST(ensure_zeroed(ctx, ctx->op_bad, sizeof(int)));
-    ST(ensure(ctx, ctx->op_tmp, embed_grad_tmp_bytes(a)));
+    bool capturing = false;
+    ST(is_capturing(ctx, &capturing));
+    ST(ensure_op(ctx, ctx->op_bad, sizeof(int), true, capturing));
+    ST(ensure_op(ctx, ctx->op_tmp, embed_grad_tmp_bytes(a), false, capturing));
+    ST(ensure_op(ctx, ctx->op_present, embed_grad_present_bytes(a), true, capturing));
     a.bad = as<int>(ctx->op_bad);
-    ST(ensure_zeroed(ctx, ctx->op_present, embed_grad_present_bytes(a)));
     CK(embed_grad(a, ctx->op_tmp.p, as<uint32_t>(ctx->op_present), ctx->stream, &ctx->launches));
     return HISS_OK;
 }
@@ -1686,7 +1741,9 @@ int hiss_layer_norm_grad(hiss_ctx *ctx, const void *d_dy, int32_t dy_dtype, int6
     a.dx = d_dx;
     a.dweight = d_dweight;
     a.dbias = d_dbias;
-    ST(ensure(ctx, ctx->op_tmp, layer_norm_grad_tmp_bytes(a)));
+    bool capturing = false;
+    ST(is_capturing(ctx, &capturing));
+    ST(ensure_op(ctx, ctx->op_tmp, layer_norm_grad_tmp_bytes(a), false, capturing));
     CK(layer_norm_grad(a, ctx->op_tmp.p, ctx->stream, &ctx->launches));
     return HISS_OK;
 }
@@ -1708,8 +1765,10 @@ int hiss_clip_grads(hiss_ctx *ctx, const hiss_tensor *tensors, int64_t count, fl
         const Span in = span(t.in, es * (size_t)t.n), out = span(t.out, es * (size_t)t.n);
         if ((t.out && t.out != t.in && overlap(in, out)) || overlap(norm, in) || overlap(norm, out)) return HISS_E_ARG;
     }
-    ST(ensure(ctx, ctx->op_tmp, clip_tmp_bytes(tensors, count)));
-    ST(ensure_zeroed(ctx, ctx->op_clip, clip_state_bytes()));
+    bool capturing = false;
+    ST(is_capturing(ctx, &capturing));
+    ST(ensure_op(ctx, ctx->op_tmp, clip_tmp_bytes(tensors, count), false, capturing));
+    ST(ensure_op(ctx, ctx->op_clip, clip_state_bytes(), true, capturing));
     CK(clip_grads(tensors, count, max_norm, d_norm, ctx->op_clip.p, ctx->op_tmp.p, ctx->stream, &ctx->launches));
     return HISS_OK;
 }
@@ -1717,6 +1776,9 @@ int hiss_clip_grads(hiss_ctx *ctx, const hiss_tensor *tensors, int64_t count, fl
 int hiss_finish(hiss_ctx *ctx)
 {
     ST(enter(ctx));
+    bool capturing = false;
+    ST(is_capturing(ctx, &capturing));
+    if (capturing) return HISS_E_STATE;
     if (!ctx->op_bad.p) return sync(ctx);
     int bad = 0;
     CK(cudaMemcpyAsync(&bad, ctx->op_bad.p, sizeof(bad), cudaMemcpyDeviceToHost, ctx->stream));

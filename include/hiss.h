@@ -54,7 +54,8 @@ typedef enum {
     HISS_OK = 0,
     HISS_E_ARG = -1,             /* invalid argument (NULL, n < 1, d out of range, eps < 0 or NaN, non-finite input) */
     HISS_E_NOMEM = -2,           /* a device or pinned allocation failed (or exceeded the allocation limit) */
-    HISS_E_STATE = -3,           /* call out of order (join before build), or the context holds a sticky CUDA error */
+    HISS_E_STATE = -3,           /* call out of order (join before build; an allocation or a wait during a graph capture),
+                                    or the context holds a sticky CUDA error */
     HISS_E_BATCH_TOO_SMALL = -4, /* batch_bytes is smaller than the result mask of one query tile */
     HISS_E_OVERFLOW = -5,        /* a count exceeded the library's integer ranges */
     HISS_E_CUDA = -6,            /* a CUDA runtime call or kernel failed; see hiss_last_cuda_error */
@@ -345,8 +346,14 @@ int hiss_gram_tf32(hiss_ctx *ctx, const float *d_a, const float *d_b, int32_t k,
  *   - They are asynchronous: the work is ordered on the context's stream and
  *     the call returns without waiting for it.  hiss_finish waits.  Workspace
  *     belongs to the context, grows on the first call that needs more, and
- *     counts towards HISS_OPT_ALLOC_LIMIT; a call that allocates nothing new
- *     can be captured in a CUDA graph.
+ *     counts towards HISS_OPT_ALLOC_LIMIT.
+ *   - A call for which the workspace is large enough (after one of the same
+ *     sizes that was not captured) can be captured in a CUDA graph; one that would
+ *     have to allocate returns HISS_E_STATE instead, and so does hiss_finish.  The
+ *     graph uses the context's workspace, which is kept as long as the context
+ *     even when later calls need a larger one.  So a replay is ordered with the
+ *     context's other calls like a call (on its stream, or by events), and the graph's
+ *     use ends with hiss_destroy.
  *   - A matrix of n rows has unit column stride and a row stride given in
  *     elements, at most 2^30: at least the width for what is written, any value
  *     >= 0 for what is only read (0 repeats one row).  Pointers are aligned to
@@ -431,7 +438,8 @@ int hiss_clip_grads(hiss_ctx *ctx, const hiss_tensor *tensors, int64_t count, fl
 
 /* Wait for everything this context has put on its stream.  HISS_E_ARG if an
  * embedding call since the last hiss_finish met a token that was neither pad nor
- * in [0, vocab) (the context stays usable). */
+ * in [0, vocab) (the context stays usable).  HISS_E_STATE while the stream is
+ * being captured. */
 int hiss_finish(hiss_ctx *ctx);
 
 /* ---- allocation-free variant ---------------------------------------------

@@ -718,6 +718,86 @@ def test_captured_in_a_graph(edd):
     j.close()
 
 
+def test_workspace_growth_keeps_captured_graphs(edd):
+    # a graph holds the workspace it was captured with, whatever later calls need
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        j, other = edd.Join(), edd.Join()
+        t = _tokens(5000, 300, _gen(61), "zipf")
+        dy = _normal((5000, 64), F32, _gen(62))
+        x = _normal((5000, 64), F32, _gen(63))
+        _, m, r = j.layer_norm(x)
+
+        def step(lib):
+            grad = lib.embed_grad(t, dy, 300)
+            dx, dw, db = lib.layer_norm_grad(dy, x, m, r)
+            norm = lib.clip_grads([grad, dw, db], 0.1)
+            return grad, dx, dw, db, norm
+
+        def larger(lib, k):
+            n, vocab = 100000 * k, 40000 * k
+            grad = lib.embed_grad(_tokens(n, vocab, _gen(k, 64), "uniform"), torch.ones((n, 16), device="cuda"), vocab)
+            lib.layer_norm_grad(torch.ones((k, 40000), device="cuda"), torch.ones((k, 40000), device="cuda"),
+                                torch.zeros(k, device="cuda"), torch.ones(k, device="cuda"))
+            lib.clip_grads([torch.ones(5, device="cuda") for _ in range(1000 * k + 1)], 1.0)
+            assert float(grad.sum()) == 16.0 * n
+
+        step(j)
+        graphs = []
+        for k in range(1, 4):
+            s.synchronize()
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph, stream=s):
+                outs = step(j)
+            graphs.append((graph, outs))
+            larger(j, k)       # replaces what the graph uses
+            larger(other, k)   # takes what would have been freed
+            for graph, outs in graphs:
+                dy.copy_(_normal((5000, 64), F32, _gen(k, 65)))
+                graph.replay()
+                larger(other, k)
+                assert all(torch.equal(a, b) for a, b in zip(outs, step(other)))
+                assert all(torch.equal(a, b) for a, b in zip(outs, step(j)))
+        j.finish()
+        other.finish()
+        del graphs, graph
+        j.close()
+        other.close()
+
+
+def test_capture_without_workspace_is_refused(edd):
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        j = edd.Join()
+        t = torch.zeros(5000, dtype=torch.int64, device="cuda")
+        dy = torch.ones((5000, 8), device="cuda")
+        m, r = torch.zeros(5000, device="cuda"), torch.ones(5000, device="cuda")
+        hits = torch.zeros(3, device="cuda")
+        s.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            hits.add_(1)
+            for call in (lambda: j.embed(t, dy), lambda: j.embed_grad(t, dy, 5), lambda: j.layer_norm_grad(dy, dy, m, r),
+                         lambda: j.clip_grads([dy], 1.0), j.finish):
+                with pytest.raises(edd.HissError) as e:
+                    call()
+                assert e.value.status == edd.HISS_E_STATE
+            y = j.layer_norm(dy)[0]  # needs none
+        graph.replay()
+        s.synchronize()
+        assert hits.tolist() == [1.0] * 3 and not y.any()
+        # the context goes on, and the same calls can be captured once they have run
+        assert float(j.embed_grad(t, dy, 5)[0, 0]) == 5000.0
+        j.finish()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            grad = j.embed_grad(t, dy, 5)
+        graph.replay()
+        s.synchronize()
+        assert grad.sum(1).tolist() == [40000.0, 0, 0, 0, 0]
+        j.close()
+
+
 # ---- refusals ----------------------------------------------------------------------------------
 
 def test_refusals(edd, lib):
