@@ -243,16 +243,28 @@ class Gradients:
     tensors) and optionally the tensors of the same shapes and types that receive the
     clipped values (default: in place).  Keeps the list that
     ``Join.clip_grads`` hands to the library, so a step that reuses its gradient
-    tensors builds it once.  Tensors must be dense (contiguous in some
-    order of their dimensions) and must not overlap."""
+    tensors builds it once.  A tensor that has since got other memory (``t.data = ...``,
+    ``t.set_()``) is found by each call, which then builds the list again.  One whose
+    size, type or order changed within the memory it had needs a new list: until
+    then the old elements are clipped, whose memory the list keeps from being freed.
+    Tensors must be dense (contiguous in some order of their dimensions) and must not
+    overlap."""
 
     def __init__(self, grads, out=None):
         grads = list(grads)
         out = grads if out is None else list(out)
         if len(out) != len(grads):
             raise ValueError("as many outputs as gradients expected")
+        from torch import Tensor
+        self._address, self._storage = Tensor.data_ptr, Tensor.untyped_storage
+        self.grads, self.out = grads, out
+        self._tensors = grads if out is grads else grads + out
+        self._build()
+
+    def _build(self):
+        grads, out = self.grads, self.out
         spans = []
-        self.array = (hiss_tensor * max(1, len(grads)))()
+        array = (hiss_tensor * max(1, len(grads)))()
         for i, (g, o) in enumerate(zip(grads, out)):
             if not (g.is_cuda and o.is_cuda and g.device == o.device == grads[0].device):
                 raise ValueError("gradient %d: CUDA tensors of one device expected" % i)
@@ -261,7 +273,7 @@ class Gradients:
             if not self._dense(g):
                 raise ValueError("gradient %d is not dense" % i)
             n = g.numel()
-            self.array[i] = hiss_tensor(g.data_ptr(), o.data_ptr(), n, _dtype(g.dtype), 0)
+            array[i] = hiss_tensor(g.data_ptr(), o.data_ptr(), n, _dtype(g.dtype), 0)
             if n:
                 spans.append((g.data_ptr(), g.data_ptr() + n * g.element_size()))
                 if o.data_ptr() != g.data_ptr():
@@ -270,7 +282,16 @@ class Gradients:
         for a, b in zip(spans, spans[1:]):
             if b[0] < a[1]:
                 raise ValueError("the tensors overlap")
-        self.grads, self.out, self.all = grads, out, [t for t in grads + out if t.numel()]
+        self.array, self._seen = array, [*map(self._address, self._tensors)]
+        # as long as these are held, an address that is still a tensor's is the same memory
+        self._memory = [*map(self._storage, self._tensors)]
+        self.all = [t for t in self._tensors if t.numel()]
+
+    def current(self):
+        """The list for the tensors where they are now (60 tensors: 3 us)."""
+        if [*map(self._address, self._tensors)] != self._seen:
+            self._build()
+        return self.array
 
     @staticmethod
     def _dense(t):
@@ -678,12 +699,13 @@ class Join:
         or a sequence of tensors, clipped in place.  Returns the norm before
         clipping (float32 CUDA scalar)."""
         g = grads if isinstance(grads, Gradients) else Gradients(grads)
+        array = g.current() if g is grads else g.array
         self._here("hiss_clip_grads", *g.grads[:1])  # one device for all: checked by Gradients
         if self._scalar is None:
             self._scalar = self._torch.empty((), dtype=self._torch.float32, device=self._device)
         norm = self._torch.empty_like(self._scalar)
         here = self._current(self._index) == self._raw  # then no list of the tensors is needed
-        self._enqueue(hiss_clip_grads, (g.array, len(g.grads), max_norm, norm.data_ptr()), "hiss_clip_grads",
+        self._enqueue(hiss_clip_grads, (array, len(g.grads), max_norm, norm.data_ptr()), "hiss_clip_grads",
                       () if here else g.all + [norm])
         return norm
 

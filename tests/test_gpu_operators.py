@@ -631,6 +631,55 @@ def test_clip_extremes(edd, lib):
     assert float(lib.clip_grads([t], 0.0)) == 0.0
 
 
+def test_clip_lists_follow_their_tensors(edd, lib):
+    # a kept list meets tensors that have other memory than when it was made
+    g = _gen(41)
+    ts = [_normal((n,), dt, g) for n, dt in ((1000, F32), (333, BF16), (70, F32))]
+    out = [torch.empty_like(t) for t in ts]
+    kept, kept_out = edd.Gradients(ts), edd.Gradients(ts, out)
+
+    def check(limit_of):
+        norm, c = _clip_ref(ts, 1.0)
+        norm, c = _clip_ref(ts, limit_of * norm)
+        before = [t.clone() for t in ts]
+        assert abs(float(lib.clip_grads(kept_out, limit_of * norm)) - norm) <= NORM_REL * norm
+        for o, s in zip(out, before):
+            _close(o, s.double() * c, (NORM_REL + 4 * U) * (s.double() * c).abs())
+        assert abs(float(lib.clip_grads(kept, limit_of * norm)) - norm) <= NORM_REL * norm
+        assert all(torch.equal(t, o) for t, o in zip(ts, out))
+
+    check(0.5)
+    left = []  # the memory that tensors had before, and what it held then
+
+    def leave(k):
+        left.extend((t.data, t.clone()) for t in (ts[k], out[k]))
+
+    leave(0)
+    ts[0].data = _normal((1000,), F32, g)               # other memory
+    out[0].data = torch.empty(1000, device="cuda")
+    check(0.25)
+    leave(1)
+    ts[1].data = _normal((7, 11), F16, g)               # another type and shape
+    out[1].data = torch.empty((7, 11), dtype=F16, device="cuda")
+    check(0.25)
+    leave(2)
+    with torch.no_grad():
+        ts[2].set_(_normal((5000,), F32, g))            # more elements
+        out[2].set_(torch.empty(5000, device="cuda"))
+    check(2.0)
+    assert all(torch.equal(o, c) for o, c in left)
+    # what the list could not have been made from is refused
+    mine, theirs = ts[0].data, ts[1].data
+    for bad in (torch.zeros(10), ts[2].data[:10], torch.zeros((10, 2), device="cuda")[:, 0]):
+        ts[0].data = bad
+        with pytest.raises(ValueError):
+            lib.clip_grads(kept, 1.0)
+    ts[0].data = mine
+    check(0.5)
+    assert ts[1].data_ptr() == theirs.data_ptr()
+    lib.finish()
+
+
 # ---- streams, workspace, graphs ---------------------------------------------------------------
 
 def test_another_stream(edd, lib):
