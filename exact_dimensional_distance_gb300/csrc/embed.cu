@@ -272,11 +272,19 @@ struct Fill {
     int f0, f1;
     int blocks;          // blocks of the kernel that do this, behind the others
 };
+// The share in words of the bitmap, and the rows of the vocabulary that those hold.
+struct Share {
+    int64_t word, rows;
+};
+__host__ __device__ __forceinline__ Share share_of(int64_t vocab, const Fill &f)
+{
+    const int64_t words = (vocab + 31) / 32, w0 = words * f.f0 / kShares, end = 32 * (words * f.f1 / kShares);
+    return {w0, (end < vocab ? end : vocab) - 32 * w0};
+}
 __device__ void fill_empty(const EmbedArgs &a, const Fill &f, int64_t warp, int64_t warps)
 {
-    const int64_t words = (a.vocab + 31) / 32;
-    const int64_t w0 = words * f.f0 / kShares, v1 = min(words * f.f1 / kShares * 32, a.vocab);
-    fill_rows(a, f.present + w0, 32 * w0, v1 - 32 * w0, warp, warps);
+    const Share s = share_of(a.vocab, f);
+    fill_rows(a, f.present + s.word, 32 * s.word, s.rows, warp, warps);
 }
 
 // First digit's counts of each tile, and which tokens occur.  Latency: 65,536
@@ -1100,7 +1108,7 @@ cudaError_t embed_grad(const EmbedArgs &a, void *tmp, uint32_t *present, cudaStr
     Fill f{};
     f.present = s.present;
     auto fill_blocks = [&](int warps) {  // for the share f0 .. f1
-        return (int)std::min<int64_t>(2 * kSMs, (a.vocab * (f.f1 - f.f0) / kShares + warps - 1) / warps);
+        return (int)std::min<int64_t>(2 * kSMs, (share_of(a.vocab, f).rows + warps - 1) / warps);
     };
     auto sort = [&](auto per_thread) {
         constexpr int ITEMS = decltype(per_thread)::value;

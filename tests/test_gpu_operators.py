@@ -241,6 +241,22 @@ def test_embed_grad_all_padding(lib, n):
     lib.finish()
 
 
+@pytest.mark.parametrize("vocab", [1, 2, 3, 31, 32, 33])
+@pytest.mark.parametrize("n", [2048, 2049, 40000])
+def test_embed_grad_small_vocabularies_without_positions(edd, lib, vocab, n):
+    # every row is written, whichever share of the zeros it falls into
+    dy = torch.full((n, 24), float("nan"), device="cuda")
+    for token, pad in ((-7, -7), (vocab, None)):  # all padding; all out of range
+        t = torch.full((n,), token, dtype=torch.int32, device="cuda")
+        for dtype in (F32, BF16):
+            got = lib.embed_grad(t, dy, vocab, pad=pad, out=torch.full((vocab, 24), 9.0, dtype=dtype, device="cuda"))
+            assert not got.any()
+        if pad is None:
+            with pytest.raises(edd.HissError):
+                lib.finish()
+    lib.finish()
+
+
 @pytest.mark.parametrize("vocab", [511, 512, (1 << 18) - 1, 1 << 18, 300007, (1 << 20) + 3])
 def test_embed_grad_large_vocabularies(lib, vocab):
     # one, two and three sort passes; more tokens than a tile's bitmap holds
