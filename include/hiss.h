@@ -397,8 +397,9 @@ int hiss_embed_grad(hiss_ctx *ctx, const void *d_dy, int32_t dy_dtype, int64_t d
  * weight and bias (param_dtype, width entries) may be NULL: 1 and 0.  y has
  * x's type or float32.  d_mean and d_rstd (float32[n], either may be NULL)
  * receive the statistics that hiss_layer_norm_grad takes.  eps must be finite
- * and >= 0; a constant row with eps = 0 gives rstd = +inf and NaN, as the
- * formula does. */
+ * and >= 0.  The mean of a constant row is its value, y the bias; with eps = 0 such a
+ * row gives rstd = +inf and NaN, as the formula does.  The sums are float32: a row
+ * whose sum or sum of squared differences overflows it gives infinities or NaN. */
 int hiss_layer_norm(hiss_ctx *ctx, const void *d_x, int32_t x_dtype, int64_t x_stride, int64_t n, int32_t width,
                     const void *d_weight, const void *d_bias, int32_t param_dtype, float eps, void *d_y,
                     int32_t y_dtype, int64_t y_stride, float *d_mean, float *d_rstd);

@@ -419,6 +419,55 @@ def test_layer_norm_difficult_rows(lib):
     assert torch.equal(lib.layer_norm(r.expand(5, d))[0], lib.layer_norm(r)[0].expand(5, d))
 
 
+@pytest.mark.parametrize("types", XY)
+@pytest.mark.parametrize("d", [1, 3, 41, 47, 96, 100, 328, 512, 656, 1000, 1021, 1302, 2569, 4099, 5000, 8200, 9001, 12000, 16384,
+                               20001, 65535])
+def test_layer_norm_constant_rows(lib, d, types):
+    # a constant row's mean is its value and its differences are zero, whatever the
+    # width and however the row is laid out over lanes, warps and blocks
+    value = torch.tensor([1.0, 0.1, -3000.0, 1e-3, 6.1e4, 1e-30, 0.0], device="cuda").to(types[0])
+    other = _normal((d,), types[0], _gen(d, str(types)), 1.5, 0.7)
+    bias = _normal((d,), types[1], _gen(d, 1))
+    for extra, off in ((0, 0), (3, 1)):
+        x = torch.cat([value[:, None].expand(-1, d), other[None], value[:, None].expand(-1, d)])
+        x = _laid(x, extra, off)
+        row = lib.layer_norm(_laid(other[None], extra, off), bias=bias, dtype=types[1])
+        y, mean, rstd = lib.layer_norm(x, bias=bias, dtype=types[1])
+        # a row between them is not changed by its neighbours
+        assert torch.equal(y[7], row[0][0]) and torch.equal(mean[7], row[1][0]) and torch.equal(rstd[7], row[2][0])
+        y0, mean0, rstd0 = lib.layer_norm(x, bias=bias, eps=0.0, dtype=types[1])
+        for k in list(range(7)) + list(range(8, 15)):
+            v = value[k % 8]
+            assert float(mean[k]) == float(v) and float(mean0[k]) == float(v)
+            assert torch.equal(y[k], bias)
+            assert abs(float(rstd[k]) / float(np.float32(1e-5)) ** -0.5 - 1) <= 4 * U
+            assert math.isinf(float(rstd0[k])) and bool(torch.isnan(y0[k]).all())
+
+
+@pytest.mark.parametrize("d", [7, 41, 100, 300, 1000, 1021, 4099])
+def test_layer_norm_small_spread(lib, d):
+    # a spread far below the mean: the mean is the exact one rounded (U of it), up to the
+    # error of a mean of differences from a first mean that is (d + 1) U off at most
+    n = 37
+    x = 1000 + torch.randint(-8, 9, (n, d), generator=_gen(d, 5), device="cuda") * 2.0 ** -12
+    x = x.float()  # exact: multiples of 2^-14 below 1024
+    w = _normal((d,), F32, _gen(d, 6))
+    for extra, off in ((0, 0), (3, 1)):
+        y, mean, rstd = lib.layer_norm(_laid(x, extra, off), w, eps=1e-12)
+        (wy, _), (wm, _), (wr, _) = _norm_ref(x, w, None, 1e-12)
+        e = x.double() - wm[:, None]
+        var = (e * e).mean(1)
+        em = U * wm.abs() + (d + 2) * U * (e.abs().mean(1) + (d + 1) * U * wm.abs())
+        # the squares are taken about a mean that is em off, the rest as in _norm_ref
+        rel = 0.5 * ((d + 6) * U + em * em / var) + 4 * U
+        rel = rel * (1 + 2 * rel)
+        _close(mean, wm, em, "mean")
+        _close(rstd, wr, rel * wr, "rstd")
+        h = (e * wr[:, None]).abs()
+        ey = w.double().abs() * (h * (rel + 3 * U)[:, None] + (em * wr * (1 + 2 * rel))[:, None]) + 4 * U * wy.abs()
+        _close(y, wy, ey, "y")
+
+
 def _norm_grad_ref(dy, x, mean, rstd, w):
     dy, x, m, r = dy.double(), x.double(), mean.double()[:, None], rstd.double()[:, None]
     n, d = x.shape
