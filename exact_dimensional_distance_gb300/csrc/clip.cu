@@ -141,7 +141,8 @@ __device__ __forceinline__ int tensor_of(const TensorList<CAP> &l, int chunk)
 // The sums over the lists so far, and what k_clip reads.
 struct ClipState {
     unsigned done;   // blocks of the last list's kernel that have finished (0 between calls)
-    float factor;
+    float factor;    // 0 also where float32 cannot hold it as a normal number:
+    double fine;     // then this is it (0 otherwise)
 };
 
 // Sum over the block of a float64 per thread, in thread 0.
@@ -208,7 +209,9 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSM)
         if (threadIdx.x == 0) {
             const double total = sqrt(s);
             *norm = (float)total;
-            state->factor = isfinite(total) && total > (double)max_norm ? (float)((double)max_norm / total) : 1.0f;
+            const double factor = isfinite(total) && total > (double)max_norm ? (double)max_norm / total : 1.0;
+            state->factor = factor < 0x1p-126 ? 0.0f : (float)factor;
+            state->fine = factor < 0x1p-126 ? factor : 0.0;
             state->done = 0;
         }
     }
@@ -252,6 +255,15 @@ __device__ void chunk_scale(const T *x, T *y, int64_t n, float f)
     }
 }
 
+// A factor that float32 holds as a subnormal number or as zero (a norm around 1e38 and
+// above, clipped to 1 or less): products in float64, rounded to float32 and to the
+// type as the others are.
+template <typename T>
+__device__ __noinline__ void chunk_scale_fine(const T *x, T *y, int64_t n, double f)
+{
+    for (int64_t i = threadIdx.x; i < n; i += kThreads) y[i] = from_f32<T>((float)((double)to_f32(x[i]) * f));
+}
+
 // 2^30 elements: 683 us, 6.3 TB/s read and written, bound by memory.
 template <int CAP>
 __global__ void __launch_bounds__(kThreads, kBlocksPerSM)
@@ -259,18 +271,23 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSM)
 {
     wait_for_previous();
     const float f = state->factor;
+    const double fine = state->fine;
     const int chunks = l.first[l.count];
     for (int i = blockIdx.x; i < chunks; i += gridDim.x) {
         const int c = chunks - 1 - i;
         const int t = tensor_of(l, c);
         if (f == 1.0f && l.in[t] == l.out[t]) continue;
         const int64_t at = (int64_t)(c - l.first[t]) * l.chunk, n = min((int64_t)l.chunk, l.n[t] - at);
-        if (l.dtype[t] == HISS_F32)
-            chunk_scale(static_cast<const float *>(l.in[t]) + at, static_cast<float *>(l.out[t]) + at, n, f);
-        else if (l.dtype[t] == HISS_F16)
-            chunk_scale(static_cast<const __half *>(l.in[t]) + at, static_cast<__half *>(l.out[t]) + at, n, f);
-        else
-            chunk_scale(static_cast<const __nv_bfloat16 *>(l.in[t]) + at, static_cast<__nv_bfloat16 *>(l.out[t]) + at, n, f);
+        auto scale = [&](auto type) {
+            using T = decltype(type);
+            const T *x = static_cast<const T *>(l.in[t]) + at;
+            T *y = static_cast<T *>(l.out[t]) + at;
+            if (fine != 0.0) chunk_scale_fine(x, y, n, fine);
+            else chunk_scale(x, y, n, f);
+        };
+        if (l.dtype[t] == HISS_F32) scale(float{});
+        else if (l.dtype[t] == HISS_F16) scale(__half{});
+        else scale(__nv_bfloat16{});
     }
 }
 

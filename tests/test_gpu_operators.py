@@ -696,6 +696,32 @@ def test_clip_extremes(edd, lib):
     assert float(lib.clip_grads([t], 0.0)) == 0.0
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_clip_factors_below_float32(edd, lib, dtype):
+    # max_norm / N is subnormal or zero in float32, the clipped values are not
+    g = _gen(str(dtype), 31)
+    for top, n, max_norm in [(3e38, 1000, 1e-3), (3e38, 1000, 1e-6), (1e38, 2, 1e-6), (1e38, 5000, 1e-6), (1e20, 30, 1e-30),
+                             (2.0 ** 100, 40001, 2.0 ** -40), (3e38, 9, 2e-38), (1e38, 10, 1.17)]:
+        x = (torch.rand(n, generator=g, device="cuda") * 2 - 1) * top
+        x[0], x[-1] = top, -top
+        x[n // 2] = x[n // 2] * 1e-20
+        x = x.to(dtype)
+        limit = float(np.float32(max_norm))
+        norm, c = _clip_ref([x], limit)
+        assert c < 2.0 ** -125
+        buf, dst = torch.zeros(n + 9, dtype=dtype, device="cuda"), torch.zeros(n + 9, dtype=dtype, device="cuda")
+        for a, b in ((0, 0), (1, 1), (3, 2), (0, None)):  # None: in place
+            src = buf[a:a + n]
+            src.copy_(x)
+            out = src if b is None else dst[b:b + n]
+            got = float(lib.clip_grads(edd.Gradients([src], [out]), limit))
+            assert math.isinf(got) if norm > 3.4028236e38 else abs(got - norm) <= NORM_REL * norm
+            _close(out, x.double() * c, (NORM_REL + 3 * U) * (x.double() * c).abs())
+    z = torch.full((10,), 1e38, device="cuda")
+    lib.clip_grads([z], 0.0)
+    assert not z.any()
+
+
 def test_clip_lists_follow_their_tensors(edd, lib):
     # a kept list meets tensors that have other memory than when it was made
     g = _gen(41)
