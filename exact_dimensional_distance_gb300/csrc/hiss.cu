@@ -1240,7 +1240,11 @@ Span span_rows(const void *p, int64_t n, int64_t width, int64_t stride, int dtyp
     return span(p, n > 0 ? dtype_size(dtype) * (size_t)((n - 1) * stride + width) : 0);
 }
 
-bool overlap(const Span &a, const Span &b) { return a.lo < b.hi && b.lo < a.hi; }
+// An empty range overlaps nothing, wherever it lies.
+bool overlap(const Span &a, const Span &b)
+{
+    return a.lo < b.hi && b.lo < a.hi && a.lo < a.hi && b.lo < b.hi;
+}
 
 bool aligned(const void *p, size_t bytes) { return (uintptr_t)p % bytes == 0; }
 

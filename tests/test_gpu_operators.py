@@ -1035,6 +1035,23 @@ def test_c_refusals(edd, lib):
     assert not f.any()
 
 
+def test_empty_operands_overlap_nothing(edd, lib):
+    # a matrix of no rows has no elements, wherever its pointer lies
+    f = torch.full((8, 16), 9.0, device="cuda")
+    s = torch.zeros((2, 8), device="cuda")
+    h, F, p, z = lib.handle, edd.HISS_F32, f.data_ptr(), edd.HISS_NO_PAD
+    assert edd.hiss_embed(h, p, F, 8, 16, 16, None, 64, 0, z, 1.0, p + 64, F, 16) == 0
+    assert edd.hiss_layer_norm(h, p + 64, F, 16, 0, 16, p, None, F, 1e-5, p + 128, F, 16, s.data_ptr(), s.data_ptr()) == 0
+    torch.cuda.synchronize()
+    assert bool((f == 9.0).all())
+    assert edd.hiss_embed_grad(h, p + 64, F, 16, None, 64, 0, z, 1.0, 8, 16, 0, p, F, 16) == 0
+    dw = torch.full((16,), 9.0, device="cuda")
+    assert edd.hiss_layer_norm_grad(h, dw.data_ptr() + 4, F, 16, dw.data_ptr() + 4, F, 16, None, None, None, F, 0, 16, None, 16,
+                                    dw.data_ptr(), None) == 0
+    lib.finish()
+    assert not f.any() and not dw.any()
+
+
 # ---- together: a table is learned, and its rows are joined --------------------------------------
 
 def test_operators_leave_the_join_alone(edd):
