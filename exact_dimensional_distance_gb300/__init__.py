@@ -210,6 +210,15 @@ def _matrix(t, name):
     return t, n, d, row if n > 1 else d
 
 
+def _pad(pad):
+    """The library's pad argument (ctypes would wrap a larger number around to a token)."""
+    if pad is None:
+        return HISS_NO_PAD
+    if not -1 << 63 <= pad < 1 << 63:
+        raise ValueError("pad does not fit 64 bits")
+    return pad
+
+
 def _vector(t, width):
     """The address of a contiguous vector of width entries."""
     if t.shape != (width,) or not t.is_contiguous():
@@ -620,7 +629,7 @@ class Join:
         self._here("hiss_embed", t, w)
         out, o, o_stride, o_code = self._out(out, (*t.shape, width), dtype, kind, width, "hiss_embed")
         self._enqueue(hiss_embed, (w.data_ptr(), code, vocab, width, stride, t.data_ptr(), bits, t.numel(),
-                                   HISS_NO_PAD if pad is None else pad, scale, o.data_ptr(), o_code, o_stride),
+                                   _pad(pad), scale, o.data_ptr(), o_code, o_stride),
                       "hiss_embed", (t, w, o))
         return out
 
@@ -639,7 +648,7 @@ class Join:
         self._here("hiss_embed_grad", t, g)
         out, o, o_stride, o_code = self._out(out, (max(vocab, 0), width), dtype, kind, width, "hiss_embed_grad")
         self._enqueue(hiss_embed_grad, (g.data_ptr(), code, stride, t.data_ptr(), bits, n,
-                                        HISS_NO_PAD if pad is None else pad, scale, vocab, width,
+                                        _pad(pad), scale, vocab, width,
                                         1 if accumulate else 0, o.data_ptr(), o_code, o_stride),
                       "hiss_embed_grad", (t, g, o))
         return out

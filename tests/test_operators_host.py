@@ -69,3 +69,13 @@ def test_rows_and_density():
     dense = edd.Gradients._dense
     assert dense(x) and dense(x.permute(2, 0, 1)) and dense(torch.zeros(())) and dense(torch.zeros((0, 3)))
     assert dense(x[:1]) and not dense(x[:, :3]) and not dense(x[0, :1].expand(5, 8)) and not dense(x[..., ::2])
+
+
+def test_padding_tokens_fit_64_bits():
+    edd = _edd()
+    assert edd._pad(None) == edd.HISS_NO_PAD
+    for pad in (0, -1, 1 << 40, (1 << 63) - 1, -(1 << 63)):
+        assert edd._pad(pad) == pad
+    for pad in (1 << 63, (1 << 64) - 1, -(1 << 63) - 1):  # c_int64 takes the second for -1
+        with pytest.raises(ValueError):
+            edd._pad(pad)
