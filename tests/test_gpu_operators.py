@@ -771,6 +771,29 @@ def test_clip_lists_follow_their_tensors(edd, lib):
     lib.finish()
 
 
+def test_embed_grad_unaligned_rows_in_big_tiles(lib):
+    # enough units of wide unaligned rows for tiles of 512 columns: pairs and single elements
+    for n, vocab, width, types in [(90000, 259, 322, (F16, F16)), (90000, 70, 323, (BF16, F32)), (50000, 20000, 530, (BF16, F32)),
+                                   (90001, 5, 258, (F32, F32))]:
+        g = _gen(n, vocab, width)
+        t = _tokens(n, vocab, g, "zipf", 32, -1)
+        dy = _normal((n, width), types[0], g, 1.0, 0.1)
+        got = lib.embed_grad(t, dy, vocab, scale=0.75, pad=-1, dtype=types[1])
+        want, mag, count = _embed_grad_ref(t, dy, vocab, 0.75, -1)
+        _close(got, want, (count[:, None] + 1) * U * mag, "width %d" % width)
+    lib.finish()
+
+
+@pytest.mark.parametrize("count", [64, 65, 290, 384, 385, 1000, 1001])
+def test_clip_list_lengths(edd, lib, count):
+    # on both sides of each length of the tensor list that the launches carry
+    g = _gen(count, 17)
+    ts = [_normal((1 + 37 * i % 301,), (F32, BF16, F16)[i % 3], g, 0.5) for i in range(count)]
+    norm = _clip_ref(ts, 1.0)[0]
+    for in_place in (False, True):
+        _check_clip(lib, edd, [t.clone() for t in ts], norm * 0.25, in_place)
+
+
 # ---- streams, workspace, graphs ---------------------------------------------------------------
 
 def test_another_stream(edd, lib):
