@@ -44,8 +44,8 @@ struct TensorList {
     int32_t chunk;           // elements per chunk, a multiple of 2048
 };
 
-// Whether a sum of squares lost nothing that matters: no square overflowed, and
-// those that float32 rounds to multiples of 2^-149 are below 2^-37 of the sum.
+// Whether a sum of squares lost nothing that matters: no square overflowed, and what
+// float32 loses of small squares, half of 2^-149 each, is below 2^-37 of the sum.
 __device__ __forceinline__ bool in_range(float s) { return s >= 0x1p-110f && s <= 0x1p100f; }
 
 // Adds the squares of U packs to *narrow in float32; a pack whose sum is not in

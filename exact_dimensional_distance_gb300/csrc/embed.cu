@@ -48,7 +48,8 @@ __device__ __forceinline__ int64_t row_of(const EmbedArgs &a, int64_t i)
 // one position.  Bound by writes, which this memory takes at 4.0 TB/s alone: 131,072
 // positions x 1024, float32 to bfloat16, 72 us (3.7 TB/s written, 1.8 read).
 // Four blocks per SM (64 registers) against three: 60,000 x 768 bfloat16 31 -> 27 us;
-// two packs per lane instead of four: 38.
+// two packs per lane instead of four: 38.  The limit of 64 spills 8 to 24 bytes per thread
+// in five of the aligned builds (float32 or bfloat16 to bfloat16 among them).
 template <typename TI, typename TO, int E, int NV>
 __global__ void __launch_bounds__(kThreads, 4) k_embed(EmbedArgs a, int lanes, int tiles)
 {
@@ -830,8 +831,9 @@ __global__ void __launch_bounds__(kJoinThreads) k_join(EmbedArgs a, SumArgs s)
 
 // ---- few positions -------------------------------------------------------------------
 
-// Up to here one kernel is faster than the sort: 1,500 positions over 5,000 x 1024
-// rows 15 us against 26, 2,000 over 32,000 x 1024 38 against 34.
+// Up to here one kernel replaces the sort: about where the two meet (1,500 positions over
+// 5,000 x 1024 rows 15 us against 26, 2,000 over 32,000 x 1024 38 against 34, where the
+// zeros count for more than the positions).
 constexpr int kFew = 2048;
 constexpr int kFewRound = kFew / kThreads;  // tokens per thread
 constexpr int kFewPacks = 4;                // packs per lane
@@ -848,7 +850,8 @@ struct FewArgs {
 // and writes the row; the others leave.  Further blocks write zeros to the rows of
 // their range that no position holds.  384 positions x 256 over 5,003 rows: 5 us, a
 // token load, a dy load and a store one after the other; with a large vocabulary the
-// zeros bound it (94 x 2968 over 27,183 rows: 48 us, 3.4 TB/s written).
+// zeros bound it (94 x 2968 over 27,183 rows: 48 us, 3.4 TB/s written).  Four blocks per SM
+// cost the build of four float32 columns 16 bytes of spills.
 template <typename TI, typename TO, int E>
 __global__ void __launch_bounds__(kThreads, 4) k_grad_few(EmbedArgs a, FewArgs f)
 {
@@ -1103,7 +1106,7 @@ cudaError_t embed_grad(const EmbedArgs &a, void *tmp, uint32_t *present, cudaStr
     s.present = a.accumulate ? nullptr : present;
     s.clear = (uint32_t *)(p + l.counts_later);
     s.clear_n = (int64_t)l.later_n;
-    // the empty rows: an eighth with each scatter, whose latencies leave the
+    // the empty rows: a quarter with each scatter, whose latencies leave the
     // memory idle, and the rest beside the sums
     Fill f{};
     f.present = s.present;

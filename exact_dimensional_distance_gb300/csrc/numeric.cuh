@@ -80,20 +80,14 @@ __device__ __forceinline__ void set_pair(__nv_bfloat16 *p, float2 v)
 }
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
-// Asynchronous copy of a pack of at least 4 bytes to shared memory.
+// Asynchronous copy of a pack of whole 16-byte lines to shared memory.
 template <typename T, int E>
 __device__ __forceinline__ void copy_pack_async(Pack<T, E> *d, const T *p)
 {
     constexpr int B = sizeof(T) * E;
-    static_assert(B >= 4, "cp.async copies 4, 8 or 16 bytes");
-    if constexpr (B >= 16) {
+    static_assert(B % 16 == 0, "whole lines");
 #pragma unroll
-        for (int i = 0; i < B; i += 16) cp_async16(reinterpret_cast<char *>(d) + i, reinterpret_cast<const char *>(p) + i);
-    } else if constexpr (B == 8) {
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(d)), "l"(p) : "memory");
-    } else {
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(d)), "l"(p) : "memory");
-    }
+    for (int i = 0; i < B; i += 16) cp_async16(reinterpret_cast<char *>(d) + i, reinterpret_cast<const char *>(p) + i);
 }
 
 // E consecutive parameters of a type known at run time (read once per block).
