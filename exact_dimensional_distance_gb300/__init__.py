@@ -10,7 +10,9 @@ libhiss.so has not been built (``python exact_dimensional_distance_gb300/build.p
 
 Operators that take a model's parameters to the points and a gradient back
 (embedding lookup, layer norm, their gradients, clipping by the global gradient
-norm) are methods of ``Join`` too; they are asynchronous on its stream.
+norm) are methods of ``Join`` too; they are asynchronous on its stream.  They
+work outside torch's differentiation: a result never requires a gradient, whatever
+its inputs do, and the way back is called as such (``layer_norm_grad``, ``embed_grad``).
 
 Functions with the names of the C ABI (``hiss_create``, ``hiss_build``, ...)
 are the raw entry points; ``Join`` wraps a context for convenience.

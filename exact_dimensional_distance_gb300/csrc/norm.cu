@@ -122,7 +122,7 @@ struct Exchange {
 // of a cluster: the block's view of the operands is its half's columns, and
 // the warps' exchange of a row's sums reaches both blocks.  Backward, 3,825 x 12,032
 // float32: 128 us, against 262 in the looping kernels; 4,000 x 16,384 bfloat16 with
-// float32 dy 139 against 324; forward, 4,000 x 11,111 float32 121 against 128.  Bound
+// float32 dy 144 against 324; forward, 4,000 x 11,111 float32 126 against 128.  Bound
 // by the latency of a row, 2 us from one to the next: the sums, the barrier of the cluster,
 // and the sums over the warps.
 
@@ -919,7 +919,9 @@ __global__ void __launch_bounds__(1024) k_norm_param(NormArgs a, const float *pa
 
 // ---- rows of any width and alignment, read again for each pass ---------------------
 // For rows above 16,384 elements.  A block per row, the second and third reading
-// from L2; 5,437 x 9594 bfloat16 took 98 us here and takes 73 in k_norm.
+// from L2; 5,437 x 9594 bfloat16 took 98 us here and takes 72 in k_norm.  Bound by the latency of
+// loads of single elements: 2,000 x 32,768 bfloat16 forward 212 us, backward 369, 1,000 x
+// 65,536 float32 351 and 496, a fifth of what the copy rate would give.
 
 constexpr int kLoopThreads = 512;
 constexpr int kLoopSplits = 64;  // row ranges of the column sums
