@@ -444,6 +444,23 @@ def test_layer_norm_constant_rows(lib, d, types):
             assert math.isinf(float(rstd0[k])) and bool(torch.isnan(y0[k]).all())
 
 
+@pytest.mark.parametrize("types", [(F32, F32), (BF16, BF16), (F16, F32)])
+@pytest.mark.parametrize("n,d", [(30011, 40), (9000, 300), (5001, 700), (4003, 1021), (3001, 3000), (2000, 5000), (1001, 8200),
+                                 (700, 9001), (601, 12000), (500, 16384), (201, 20001)])
+def test_layer_norm_constant_rows_among_others(lib, n, d, types):
+    # blocks that take rows of both kinds one after the other: each row is what it is alone
+    g = _gen(n, d, str(types), 3)
+    x = _normal((n, d), types[0], g, 1.5, 0.7)
+    flat = torch.rand(n, generator=g, device="cuda") < 0.4
+    x[flat] = torch.randint(1, 99, (int(flat.sum()), 1), generator=g, device="cuda").to(types[0])
+    for extra, off in ((0, 0), (3, 1)):
+        got = lib.layer_norm(_laid(x, extra, off), dtype=types[1])
+        for rows in (flat, ~flat):
+            want = lib.layer_norm(_laid(x[rows], extra, off), dtype=types[1])
+            assert all(torch.equal(a[rows], b) for a, b in zip(got, want))
+        assert not got[0][flat].any() and torch.equal(got[1][flat], x[flat, 0].float())
+
+
 @pytest.mark.parametrize("d", [7, 41, 100, 300, 1000, 1021, 4099])
 def test_layer_norm_small_spread(lib, d):
     # a spread far below the mean: the mean is the exact one rounded (U of it), up to the
