@@ -210,6 +210,13 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&v)[32])
 }
 __device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
+// A group of four warps gives registers back to its block, or takes some of them (waits until they are
+// there): N a thread from here on.
+template <int N>
+__device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+
 // ---- pairs of CTAs: clusters, tensor copies, tcgen05 with cta_group::2 ----------------
 __device__ __forceinline__ uint32_t cluster_rank()
 {

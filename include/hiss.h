@@ -493,7 +493,8 @@ typedef struct {
 /* y = the block's value at n rows x (0 <= n < 2^30).  kept: NULL, or two hiss_packed of
  * n rows of hidden columns that receive a and b in 8 bits (of float32 sums, by the
  * rule of float32 rows), for hiss_feed_forward_grad.  Sums are float32, on the tensor
- * cores, which cut at most 2^-23 of a sum for every 16 columns; h may be rounded to
+ * cores, which cut at most 2^-23 of what an accumulator holds for every 16 columns; a and b
+ * leave it after at most 512 columns (float32: 128) for additions to nearest.  h may be rounded to
  * dtype before the second product (float32: it is held to 24 bits), so in float16 a value
  * beyond 65504 may be an infinity there.  A row with an infinity or a NaN gives values
  * that are not finite, in float32 NaN where an infinity would be exact. */

@@ -1,0 +1,143 @@
+"""Long sums of the feed-forward block.  The tensor cores cut a sum towards zero at each step of 16
+columns, so no accumulator may take in many: what it lost shows in means of terms of one sign, in the
+codes of kept projections and in the signs that relu's derivative takes."""
+import zlib
+
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+F32, F16, BF16 = torch.float32, torch.float16, torch.bfloat16
+HALF = {F32: 2.0 ** -24, F16: 2.0 ** -11, BF16: 2.0 ** -8}  # half a step, relative
+# A rounding's error relative to the value, in the 2-norm: uniform within half a step of 2^e, over values
+# whose logarithms are: sqrt(1 / 3 * 3 / (8 ln 2)) half steps.
+ROUNDING = 0.43
+
+
+def _error(width, few=False):
+    """The mean error of a projection of 16-bit rows over its size, the 2-norm of its terms.  A step loses half of
+    2^-23 of its range's sum so far on average, which after j steps is sqrt(16 j / width) of the size.  Ranges have signs of
+    their own: the large products' first two, of 32 steps (the sum of sqrt(j) is 123), and the others, of 16 (44.5).
+    The ranges' additions in float32 are each off by a quarter of 2^-23 on average of a sum that is sqrt(1/2) of the
+    whole on average."""
+    long = 0 if few else 2
+    lost = ((long * (4 * 123) ** 2 + (width - 512 * long) / 256 * (4 * 44.5) ** 2) / width) ** 0.5
+    return lost * 2.0 ** -24 + 2.0 ** -25 * (width / 512) ** 0.5
+
+
+@pytest.fixture(scope="module")
+def lib():
+    import __graft_entry__
+    __graft_entry__.build()
+    import exact_dimensional_distance_gb300 as edd
+    j = edd.Join()
+    yield j
+    j.finish()
+    j.close()
+
+
+def _gen(*seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(zlib.crc32(repr(seed).encode()))
+    return g
+
+
+def _normal(shape, dtype, gen, scale=1.0):
+    return (scale * torch.randn(shape, generator=gen, device="cuda")).to(dtype)
+
+
+def _positive(shape, dtype, gen, scale=1.0):
+    return (scale * torch.randn(shape, generator=gen, device="cuda").abs()).to(dtype)
+
+
+def _kept(v):
+    """(codes, scales, scale bytes) of float64 rows by the definition."""
+    n, f = v.shape
+    m = torch.nn.functional.pad(v.abs(), (0, -f % 32)).view(n, -1, 32).amax(2)
+    e = torch.ceil(torch.log2(m.clamp_min(2.0 ** -140) / 127))
+    e = torch.where(127 * torch.exp2(e) < m, e + 1, e)
+    e = torch.where(127 * torch.exp2(e - 1) >= m, e - 1, e).clamp_min(-126)
+    s = torch.exp2(e).repeat_interleave(32, 1)[:, :f]
+    return (v / s).round(), s, (e + 127).to(torch.uint8)
+
+
+# ---- codes of what was kept --------------------------------------------------------
+
+def _count_codes(lib, dtype, n, d, f, inputs, few=False):
+    """A code differs from the definition's where an error carries a value across the middle of two: by chance
+    (error / scale).  A block's scale differs where its largest value crosses 127 scales, 1 / 64 as often."""
+    count, blocks, expected, expected_blocks = 0, 0, 0.0, 0.0
+    for i in range(inputs):
+        g = _gen(n, d, f, str(dtype), i)
+        x, gate, up = _normal((n, d), dtype, g), _normal((f, d), dtype, g, d ** -0.5), _normal((f, d), dtype, g, d ** -0.5)
+        _, kept = lib.feed_forward(x, gate, up, _normal((8, f), dtype, g), act="relu", keep=True)
+        for k, w in zip(kept, (gate, up)):
+            codes, s, byte = _kept(x.double() @ w.double().t())
+            size = (x.double().square() @ w.double().square().t()).sqrt()
+            same = (k.scales == byte).repeat_interleave(32, 1)[:, :f]
+            count += int(((k.codes[:, :f] != codes) & same).sum())
+            blocks += int((k.scales != byte).sum())
+            expected += _error(d, few) * float((size / s).sum())
+            expected_blocks += _error(d, few) * float((size / s).sum()) / 64 / 32
+    # five times the spread of a count
+    assert count <= expected + 5 * expected ** 0.5 + 5
+    assert blocks <= expected_blocks + 5 * expected_blocks ** 0.5 + 5
+
+
+#                                    rows, width, hidden, inputs
+@pytest.mark.parametrize("n,d,f,inputs", [(1024, 4096, 2048, 1), (300, 8200, 1000, 3), (100, 16384, 520, 6), (70, 65536, 136, 16)])
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_codes_of_kept_projections(lib, dtype, n, d, f, inputs):
+    _count_codes(lib, dtype, n, d, f, inputs)
+
+
+# ---- signs that relu's derivative takes -----------------------------------------------
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_signs_of_projections_computed_again(lib, dtype):
+    """Projections near zero whose sums go far from it and back.  Each row of x has a column of its own, in
+    which gate and up are 0: there the gate's gradient is da itself.  Eight times the
+    mean error settles the sign."""
+    n, half, near, f, o = 256, 8192, 32, 512, 64
+    d = 2 * half + near + n
+    g = _gen(str(dtype))
+    x, gate = torch.zeros((n, d), dtype=dtype, device="cuda"), torch.zeros((f, d), dtype=dtype, device="cuda")
+    x[:, :half], gate[:, :half] = _normal((n, half), dtype, g), _normal((f, half), dtype, g, half ** -0.5)
+    x[:, half:2 * half], gate[:, half:2 * half] = -x[:, :half], gate[:, :half]
+    x[:, 2 * half:2 * half + near] = _normal((n, near), dtype, g, 2.0 ** -9)
+    gate[:, 2 * half:2 * half + near] = _normal((f, near), dtype, g, half ** -0.5)
+    up = torch.zeros_like(gate)
+    up[:, :half] = _normal((f, half), dtype, g, half ** -0.5)
+    x[:, d - n:] = torch.eye(n, dtype=dtype, device="cuda")
+    down, dy = _normal((o, f), dtype, g), _normal((n, o), dtype, g)
+    dgate = lib.feed_forward_grad(dy, x, gate, up, down, act="relu")[1]
+    a = x.double() @ gate.double().t()
+    size = (x.double().square() @ gate.double().square().t()).sqrt()
+    db = (dy.double() @ down.double()) * (x.double() @ up.double().t())
+    settled = (a.abs() >= 8 * _error(d) * size) & (db.abs() > 2.0 ** -8)
+    assert float(settled.double().mean()) > 0.5
+    wrong = ((dgate[:, d - n:].t() != 0) != (a > 0)) & settled
+    assert int(wrong.sum()) == 0
+
+
+@pytest.mark.parametrize("keep", [False, True])
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_gradients_of_wide_blocks_with_relu(lib, dtype, keep):
+    """Each gradient in norm, within 1.5 times its two roundings: of da, db or h, and its own."""
+    n, d, f, o = 600, 4096, 520, 264
+    g = _gen(str(dtype), keep)
+    x, dy = _normal((n, d), dtype, g), _normal((n, o), dtype, g, 0.5)
+    gate, up, down = _normal((f, d), dtype, g, d ** -0.5), _normal((f, d), dtype, g, d ** -0.5), _normal((o, f), dtype, g, f ** -0.5)
+    kept = lib.feed_forward(x, gate, up, down, act="relu", keep=True)[1] if keep else None
+    got = lib.feed_forward_grad(dy, x, gate, up, down, act="relu", kept=kept)
+    xd, gd, ud, dd, v = (t.double() for t in (x, gate, up, down, dy))
+    a, b = xd @ gd.t(), xd @ ud.t()
+    if keep:
+        a, b = (c * s for c, s, _ in map(_kept, (a, b)))
+    dh = v @ dd
+    da, db = dh * b * (a > 0), dh * a.clamp_min(0)
+    want = (da @ gd + db @ ud, da.t() @ xd, db.t() @ xd, v.t() @ (a.clamp_min(0) * b))
+    for name, t, w in zip(("dx", "dgate", "dup", "ddown"), got, want):
+        off = float((t.double() - w).norm() / w.norm())
+        assert off <= 1.5 * 2 ** 0.5 * ROUNDING * HALF[dtype], name
