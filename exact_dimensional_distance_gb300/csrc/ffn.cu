@@ -35,13 +35,10 @@ constexpr int kMaxProblems = 3;
 constexpr int kBarrierBytes = 1024;
 constexpr int kGroupM = 8;         // tiles run down a group of this many tile rows before the next column
 
-// K blocks of 16-bit operands that one accumulator takes in, but of a and b.
-constexpr int kLongest(bool bf16) { return bf16 ? 1024 : 256; }
-
-// What an epilogue does with a tile.
-enum { kOut = 0, kGated = 1, kGrad = 2 };
+// What an epilogue does with a tile; kGradLong: kGrad over a long K.
+enum { kOut = 0, kGated = 1, kGrad = 2, kGradLong = 3 };
 template <int EP>
-constexpr bool kMiddle = EP == kGrad;
+constexpr bool kMiddle = EP == kGrad || EP == kGradLong;
 
 // K blocks that a tile's accumulator i takes in before it is added to float32 registers.  The tensor cores
 // cut a sum towards zero at every step of 16 columns, up to 2^-23 of it: one accumulator for all of K is
@@ -53,11 +50,13 @@ constexpr bool kMiddle = EP == kGrad;
 //   bfloat16 are 3.3e-7 of the terms' 2-norm off so, 3.5e-6 with one accumulator (4.0e-7 in a library's float32
 //   product).  8192 x 2048 by 2 x 5632, kept in 8 bits: 253 us, 246 with one accumulator, 306 with 4 from the
 //   start, 248 with 8 throughout.
-//   Others: all.
+//   Others round what they add up, or their terms, to 16 bits: 16 blocks lose up to 2^-18 of a sum of one sign, a
+//   128th of float16's half step.  dh up to 4096 columns: all, 2^-16, since registers for its sums
+//   cost its epilogue (54 us for 70 on 16,384 x 1024).
 template <int EP, int P>
 __host__ __device__ constexpr int fold_blocks(int i)
 {
-    return P == 3 ? 2 : EP == kGated ? (i < 2 ? 8 : 4) : 1 << 30;
+    return P == 3 ? 2 : EP == kGated ? (i < 2 ? 8 : 4) : EP == kGrad ? 64 : 16;
 }
 
 // Registers: an epilogue thread has 128 sums, the issuing warps need few (more with three problems).  Of
@@ -714,7 +713,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_produ
             };
             // The last sums leave as they come from tensor memory (kDirect).  The gated ones, whose accumulators are
             // short, are taken first: the products go on in both accumulators then.
-            constexpr bool kDirect = P == 1 && EP != kGated, kSums = P == 3 || EP == kGated;
+            constexpr bool kDirect = P == 1 && EP != kGated, kSums = P == 3 || EP != kGrad;
             float sum[G][32];
             if constexpr (kSums) {
 #pragma unroll
@@ -757,9 +756,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_produ
                     float v[32];
                     load(g, v);
                     if (g + 1 == kGroups) done();
+                    if constexpr (kSums) add(v, sum[EP == kOut ? g : 0]);
                     if constexpr (EP == kOut) {
                         if (there) emit<EP, P>(slots, a, p, w.split, row, col, v, v);
                     } else {
+                        if constexpr (kSums) {  // the groups that are left, from the first place on
+#pragma unroll
+                            for (int i = 0; i + 1 < G; ++i)
+#pragma unroll
+                                for (int j = 0; j < 32; ++j) sum[i][j] = sum[i + 1][j];
+                        }
                         Kept next;
                         if (a.keeps && g + 1 < kGroups) next.load(a, p, row + lane, col + 32);
                         if (there) emit_grad<P>(slots, a, p, row, col, v, kept);
@@ -1426,9 +1432,6 @@ struct Plan {
         a.splits = 1;
         // few tiles over a long K: ranges of at least 8 blocks that fill the pairs
         if (EP == kOut && 2 * a.tiles <= kPairs) a.splits = std::max(1, std::min(kPairs / a.tiles, blocks / 8));
-        // the tensor cores cut what a sum loses at each step instead of rounding it, 2^-23 of the sum
-        // and always towards zero: after kLongest blocks that is half of a rounding to the result's type
-        if (EP == kOut && planes == 1) a.splits = std::max(a.splits, (blocks + kLongest(bf16) - 1) / kLongest(bf16));
         a.per_split = (blocks + a.splits - 1) / a.splits;
         a.splits = (blocks + a.per_split - 1) / a.per_split;
         const float *part[kMaxProblems] = {};
@@ -1445,8 +1448,8 @@ struct Plan {
             }
         }
         if (!ws) return cudaSuccess;
-        if (planes == 3) HISS_TRY((launch<EP, 3>(a, after, s, launches)));
-        else HISS_TRY((launch<EP, 1>(a, after, s, launches)));
+        if (planes == 1) HISS_TRY((launch<EP, 1>(a, after, s, launches)));
+        else if constexpr (EP != kGradLong) HISS_TRY((launch<EP, 3>(a, after, s, launches)));
         after = true;
         for (int i = 0; a.splits > 1 && i < a.problems; ++i) {
             const Problem &p = a.p[i];
@@ -1558,7 +1561,10 @@ struct Plan {
             HISS_TRY(store_map(&a.da, da, planes, false, bf16, planes, cols));
             HISS_TRY(store_map(&a.db, db, planes, false, bf16, planes, cols));
         }
-        HISS_TRY((run<kGrad>(a, {{{dy}, {down}, n, f, nullptr, 0}}, {o}, false, true)));
+        if (planes == 1 && o > fold_blocks<kGrad, 1>(0) * kBlockK)
+            HISS_TRY((run<kGradLong>(a, {{{dy}, {down}, n, f, nullptr, 0}}, {o}, false, true)));
+        else
+            HISS_TRY((run<kGrad>(a, {{{dy}, {down}, n, f, nullptr, 0}}, {o}, false, true)));
         Args b{};
         HISS_TRY((run<kOut>(b, {{{da, db}, {gate, up}, n, d, g.dx, g.dx_stride}}, {f, f}, false, true)));
         Args c{};

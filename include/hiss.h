@@ -493,8 +493,8 @@ typedef struct {
 /* y = the block's value at n rows x (0 <= n < 2^30).  kept: NULL, or two hiss_packed of
  * n rows of hidden columns that receive a and b in 8 bits (of float32 sums, by the
  * rule of float32 rows), for hiss_feed_forward_grad.  Sums are float32, on the tensor
- * cores, which cut at most 2^-23 of what an accumulator holds for every 16 columns; a and b
- * leave it after at most 512 columns (float32: 128) for additions to nearest.  h may be rounded to
+ * cores, which cut at most 2^-23 of what an accumulator holds for every 16 columns; sums
+ * leave it after at most 512 columns of x or 1024 of h (float32: 128) for additions to nearest.  h may be rounded to
  * dtype before the second product (float32: it is held to 24 bits), so in float16 a value
  * beyond 65504 may be an infinity there.  A row with an infinity or a NaN gives values
  * that are not finite, in float32 NaN where an infinity would be exact. */
@@ -516,8 +516,8 @@ typedef struct {
 /* Gradient of hiss_feed_forward:
  *   dh = dy down,  da = dh * b * act'(a),  db = dh * act(a),
  *   dx = da gate + db up,  dgate = da^T x,  dup = db^T x,  ddown = dy^T h.
- * Sums are float32; da, db and h are rounded to dtype between the products (float32:
- * held to 24 bits).  n = 0 gives weight gradients of 0.  The workspace holds da, db and h (float32:
+ * Sums are float32, as there (dh: up to 4096 columns, then 1024; of others 1024); da, db and h are
+ * rounded to dtype between the products (float32: held to 24 bits).  n = 0 gives weight gradients of 0.  The workspace holds da, db and h (float32:
  * 6 bytes per element each), without kept a and b in float32, copies of operands that are float32,
  * in 8 bits or not aligned to 16 bytes, and partial sums of products that are cut into ranges. */
 int hiss_feed_forward_grad(hiss_ctx *ctx, const hiss_ffn *w, const hiss_ffn_grad *g, int64_t n);

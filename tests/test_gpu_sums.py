@@ -141,3 +141,50 @@ def test_gradients_of_wide_blocks_with_relu(lib, dtype, keep):
     for name, t, w in zip(("dx", "dgate", "dup", "ddown"), got, want):
         off = float((t.double() - w).norm() / w.norm())
         assert off <= 1.5 * 2 ** 0.5 * ROUNDING * HALF[dtype], name
+
+
+# ---- terms of one sign --------------------------------------------------------------
+
+# Ranges of 1024 columns, of 64 steps: a step loses at most 2^-23 of the range's sum so far, which is half of it
+# on average: 2^-18 of the whole.
+LOST = 2.0 ** -18
+
+
+def _biased(got, want, lost, values):
+    """The mean relative error is within lost and five times the spread of that many roundings' mean."""
+    off = float((got.double() / want - 1).mean())
+    assert abs(off) <= lost + 5 * ROUNDING * HALF[got.dtype] / values ** 0.5, off
+
+
+@pytest.mark.parametrize("n", [16384, 65536, 1 << 20])
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_weight_gradients_over_many_rows(lib, dtype, n):
+    d, f, o = 32, 256, 256
+    g = _gen(n, str(dtype))
+    x, dy = _positive((n, d), dtype, g), _positive((n, o), dtype, g, 2.0 ** -12)
+    gate, up, down = (_positive(s, dtype, g, 0.2) for s in ((f, d), (f, d), (o, f)))
+    ddown = lib.feed_forward_grad(dy, x, gate, up, down, act="relu")[3]
+    h = ((x.double() @ gate.double().t()) * (x.double() @ up.double().t())).to(dtype)
+    # The elements of a column are sums of n products of one mean, whose spread relative to it is sqrt(0.6) (the
+    # squares' mean of dy is pi / 2 times its mean's square, that of h 1.03 times): the sums' is sqrt(0.6 / n).
+    # Where that is below a quarter of half a step (bfloat16, 2^20 rows), a column is rounded as one: f values.
+    values = f * o if (0.6 / n) ** 0.5 > HALF[dtype] / 4 else f
+    _biased(ddown, dy.double().t() @ h.double(), LOST + 2.0 ** -20, values)  # some of h round to the other side
+
+
+@pytest.mark.parametrize("n,d,f,o", [(128, 65536, 64, 128), (128, 32, 65536, 128), (128, 128, 64, 65536), (128, 128, 64, 20000)])
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_wide_blocks(lib, dtype, n, d, f, o):
+    """Width, hidden or out width up to the largest: the value, and dx where the out width is long.  Ranges of a and
+    b are shorter: at most 17 * 2^-23 lost in each.  Roundings: of what goes into the last product, and the result's."""
+    g = _gen(n, d, f, o, str(dtype))
+    x, gate, up = _positive((n, d), dtype, g), _positive((f, d), dtype, g, 1 / d), _positive((f, d), dtype, g, 1 / d)
+    down, dy = _positive((o, f), dtype, g, 2.0 ** -6), _positive((n, o), dtype, g, 2.0 ** -10)
+    xd, gd, ud, dd, v = (t.double() for t in (x, gate, up, down, dy))
+    a, b = xd @ gd.t(), xd @ ud.t()
+    if o > max(d, f):
+        dh = v @ dd
+        got, want, inner = lib.feed_forward_grad(dy, x, gate, up, down, act="relu")[0], (dh * b) @ gd + (dh * a) @ ud, 2 * n * f
+    else:
+        got, want, inner = lib.feed_forward(x, gate, up, down, act="relu"), (a * b) @ dd.t(), n * f
+    _biased(got, want, LOST + 34 * 2.0 ** -23, 1 / (1 / want.numel() + 1 / inner))
