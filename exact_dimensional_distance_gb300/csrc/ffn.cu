@@ -1130,6 +1130,12 @@ constexpr int kPieces = (GATED ? 2 : 1) * (int)sizeof(T) / 2 + kParts<T, MT, GAT
 template <typename T, int MT>
 constexpr int kDepth = sizeof(T) == 4 && MT > 1 ? 3 : 4;
 
+// Blocks of 32 columns between two additions to the sums: these instructions cut as the large products' do.
+// 16 float32 rows through 4096 x 11008 are 6.5e-6 off with one accumulator a warp (295 us), 5e-7 so (299;
+// 32 rows 441 and 463).
+template <typename T>
+constexpr int kFoldBlocks = sizeof(T) == 4 ? 4 : 8;
+
 // MT: 16-row tiles of x.
 // 16 rows of bfloat16 through 512 x 2048 9 us, 48 rows 17 (20 in the large products); bound by the
 // latency of a ring's blocks.
@@ -1194,7 +1200,20 @@ __global__ void __launch_bounds__(kWarps * 32) k_tile_rows(FewArgs a)
         if (b < blocks) fetch_x(b);
         cp_async_commit();
     }
-    float acc[G][MT][4] = {}, cross[WIDE ? G : 1][WIDE ? MT : 1][4] = {};
+    float sum[G][MT][4] = {}, acc[G][MT][4] = {}, cross[WIDE ? G : 1][WIDE ? MT : 1][4] = {};
+    auto fold = [&]() {
+#pragma unroll
+        for (int e = 0; e < S; ++e) {
+            float &to = sum[e / (MT * 4)][e / 4 % MT][e % 4], &from = acc[e / (MT * 4)][e / 4 % MT][e % 4];
+            to += from;
+            from = 0.0f;
+            if constexpr (WIDE) {
+                float &rest = cross[e / (MT * 4)][e / 4 % MT][e % 4];
+                to += rest;
+                rest = 0.0f;
+            }
+        }
+    };
     for (int b = 0; b < blocks; ++b) {
         if (b + D - 1 < blocks) {
             fetch_weights(b + D - 1);
@@ -1237,18 +1256,16 @@ __global__ void __launch_bounds__(kWarps * 32) k_tile_rows(FewArgs a)
                     }
                 }
             }
+        if (b % kFoldBlocks<T> == kFoldBlocks<T> - 1) fold();
     }
-    if constexpr (WIDE) {
-#pragma unroll
-        for (int e = 0; e < S; ++e) acc[e / (MT * 4)][e / 4 % MT][e % 4] += cross[e / (MT * 4)][e / 4 % MT][e % 4];
-    }
+    fold();
     if (GATED) let_next_start();
     if (a.ks > 1) {
         float *sums = reinterpret_cast<float *>(ring);
         cp_async_wait<0>();
         __syncthreads();
 #pragma unroll
-        for (int e = 0; e < S; ++e) sums[(warp * S + e) * 32 + lane] = acc[e / (MT * 4)][e / 4 % MT][e % 4];
+        for (int e = 0; e < S; ++e) sums[(warp * S + e) * 32 + lane] = sum[e / (MT * 4)][e / 4 % MT][e % 4];
         __syncthreads();
         // each of the row's warps joins its part of the sums
         const int per = (S + a.ks - 1) / a.ks;
@@ -1261,7 +1278,7 @@ __global__ void __launch_bounds__(kWarps * 32) k_tile_rows(FewArgs a)
         __syncthreads();
         if (share != 0) return;
 #pragma unroll
-        for (int e = 0; e < S; ++e) acc[e / (MT * 4)][e / 4 % MT][e % 4] = mine[e * 32];
+        for (int e = 0; e < S; ++e) sum[e / (MT * 4)][e / 4 % MT][e % 4] = mine[e * 32];
     }
 #pragma unroll
     for (int m = 0; m < MT; ++m)
@@ -1270,9 +1287,9 @@ __global__ void __launch_bounds__(kWarps * 32) k_tile_rows(FewArgs a)
             const int i = 16 * m + g8 + (e & 2) * 4, row = row0 + 2 * t + (e & 1);
             if (i >= a.n || row >= a.m) continue;
             const int64_t at = i * a.out_stride + row;
-            float v = acc[0][m][e];
+            float v = sum[0][m][e];
             if constexpr (GATED) {
-                const float u = acc[1][m][e];
+                const float u = sum[1][m][e];
                 if (a.sums[0]) a.sums[0][at] = v, a.sums[1][at] = u;
                 float h = 0.0f;
                 with_activation(a.act, [&](auto act) { h = activate<!WIDE, decltype(act)::value>(both(v)).value.x * u; });

@@ -188,3 +188,35 @@ def test_wide_blocks(lib, dtype, n, d, f, o):
     else:
         got, want, inner = lib.feed_forward(x, gate, up, down, act="relu"), (a * b) @ dd.t(), n * f
     _biased(got, want, LOST + 34 * 2.0 ** -23, 1 / (1 / want.numel() + 1 / inner))
+
+
+# ---- few rows -----------------------------------------------------------------------
+
+@pytest.mark.parametrize("n,d,f,inputs", [(5, 2048, 16384, 64), (16, 1000, 15000, 32), (33, 2000, 2960, 32)])
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_codes_of_few_rows(lib, dtype, n, d, f, inputs):
+    _count_codes(lib, dtype, n, d, f, inputs, few=True)
+
+
+@pytest.mark.parametrize("n,d,f,o", [(16, 4096, 11008, 4096), (9, 64, 22016, 8192), (32, 64, 22016, 8192), (20, 20000, 1000, 64)])
+def test_few_float32_rows(lib, n, d, f, o):
+    """Ranges of 128 columns, 8 steps: as in _error, the sum of sqrt(j) is 16.3, so 16.3 * 4 / sqrt(128) = 5.8 halves of
+    2^-23 in each product; two additions per range, a quarter of 2^-23 each of sqrt(1/2) of the sum; and what three
+    parts leave out, 2^-23.  The value's error has those of a and b in it.  Half as much again for the inputs' spread."""
+    def product(width):
+        return 5.8 * 2.0 ** -24 + 2.0 ** -25 * (width / 128) ** 0.5 + 2.0 ** -23
+    g = _gen(n, d, f, o)
+    x = _normal((n, d), F32, g)
+    gate, up, down = _normal((f, d), F32, g, d ** -0.5), _normal((f, d), F32, g, d ** -0.5), _normal((o, f), F32, g, f ** -0.5)
+    y = lib.feed_forward(x, gate, up, down, act="relu").double()
+    xd, dd = x.double(), down.double()
+    want = ((xd @ gate.double().t()).clamp_min(0) * (xd @ up.double().t())) @ dd.t()
+    off = float((y - want).norm() / want.norm())
+    assert off <= 1.5 * (product(f) ** 2 + 2 * product(d) ** 2) ** 0.5, off
+    # terms of one sign: 8 steps that lose at most 2^-23 of a half of their range's sum on average
+    x, gate, up, down = (t.abs() for t in (x, gate, up, down))
+    y = lib.feed_forward(x, gate, up, down, act="relu").double()
+    xd, dd = x.double(), down.double()
+    want = ((xd @ gate.double().t()) * (xd @ up.double().t())) @ dd.t()
+    off = float((y / want - 1).mean())
+    assert abs(off) <= 3 * (4.5 + 1) * 2.0 ** -23, off
