@@ -182,10 +182,11 @@ __device__ __forceinline__ Activated activate(float2 a)
         const float2 o = __ffma2_rn(q, both(-1.0f), both(1.0f)), p = make_float2(a.x > 0.0f ? o.x : q.x, a.y > 0.0f ? o.y : q.y);
         return {__fmul2_rn(a, p), __ffma2_rn(__fmul2_rn(a, both(0.39894228f)), e, p)};
     }
-    float2 s;
-    if (FAST) s = inverse_fast(__fadd2_rn(exp2_fast(__fmul2_rn(a, both(-kLog2E))), both(1.0f)));
-    else s = make_float2(1.0f / (1.0f + expf(-a.x)), 1.0f / (1.0f + expf(-a.y)));
-    const float2 o = __ffma2_rn(s, both(-1.0f), both(1.0f));
+    const float2 e = FAST ? exp2_fast(__fmul2_rn(a, both(-kLog2E))) : make_float2(expf(-a.x), expf(-a.y));
+    const float2 s = FAST ? inverse_fast(__fadd2_rn(e, both(1.0f))) : make_float2(1.0f / (1.0f + e.x), 1.0f / (1.0f + e.y));
+    // 1 - s: above 0 the difference cancels (6% off at 16), e s does not
+    const float2 left = __ffma2_rn(s, both(-1.0f), both(1.0f)), es = __fmul2_rn(e, s);
+    const float2 o = make_float2(a.x > 0.0f ? es.x : left.x, a.y > 0.0f ? es.y : left.y);
     if (ACT == HISS_SIGMOID) return {s, __fmul2_rn(s, o)};
     return {__fmul2_rn(a, s), __fmul2_rn(s, __ffma2_rn(a, o, both(1.0f)))};
 }
