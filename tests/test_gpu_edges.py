@@ -69,3 +69,51 @@ def test_derivatives_over_the_range(lib, dtype, act):
     rel, sub = ROUND[dtype]  # of da, and of the result
     bad = ~((got - want).abs() <= _relative(a, act, dtype) * size * (1 + 2 * rel) + 2 * (rel * want.abs() + sub))
     assert not bool(bad.any()), [(float(a[i]), float(got[i]), float(want[i])) for i in torch.nonzero(bad).flatten()[:5]]
+
+
+@pytest.mark.parametrize("width", [64, 128, 520, 2048, 12288])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_norm_gradient_of_constant_rows_kept_in_8_bits(lib, dtype, width):
+    """Rows whose value 8 bits hold exactly: x - mean is 0 there, so dweight is 0 and dx = rstd (g - mean(g)), the
+    same from rows that the kernel reads in 8 bits (dy and dx aligned) and from rows that are unpacked first."""
+    values = [1000.0, -3.0, 0.0, 127.0, 2.0 ** -10, 100.0] + ([] if dtype == F16 else [2.0 ** 120, -2.0 ** 119])
+    x = torch.tensor(values, device="cuda").to(dtype)[:, None].expand(len(values), width).contiguous()
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(width)
+    dy = torch.randn((len(values), width), generator=gen, device="cuda").to(dtype)
+    w = 1 + 0.3 * torch.randn(width, generator=gen, device="cuda")
+    # by the definition: layer_norm's float32 sum of 520 times 2^120 overflows
+    mean, rstd = x[:, 0].float(), torch.full((len(values),), 1e-5 ** -0.5, device="cuda")
+    p = lib.pack(x)
+    assert torch.equal(lib.unpack(p), x)
+    buf = torch.zeros((len(values), width + 1), dtype=dtype, device="cuda")
+    apart = buf[:, 1:]  # rows that are not aligned
+    apart.copy_(dy)
+    g = dy.double() * w.double()
+    want = rstd.double()[:, None] * (g - g.mean(1, keepdim=True))
+    # float32 sums of width terms, four steps of each element, the result's rounding
+    err = rstd.double()[:, None] * U * (4 * g.abs() + (width + 8) * g.abs().mean(1, keepdim=True))
+    for v in (dy, apart):
+        dx, dw, db = lib.layer_norm_grad(v, p, mean, rstd, w)
+        assert not bool(dw.any())
+        assert bool(((dx.double() - want).abs() <= err + 2 * ROUND[dtype][0] * want.abs() + ROUND[dtype][1]).all())
+        assert bool(((db.double() - dy.double().sum(0)).abs() <= len(values) * U * dy.double().abs().sum(0)).all())
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_norm_gradient_far_from_zero(lib, dtype):
+    """Rows whose mean is far above their spread, of values that 8 bits hold exactly: h = (x - mean) rstd is off by
+    the mean's and its own three roundings alone, wherever the rows lie."""
+    n, width = 64, 256
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(7)
+    x = (120 + torch.randint(0, 8, (n, width), generator=gen, device="cuda")).to(dtype) * 8
+    dy = torch.randn((n, width), generator=gen, device="cuda").to(dtype)
+    _, mean, rstd = lib.layer_norm(x)
+    p = lib.pack(x)
+    assert torch.equal(lib.unpack(p), x)
+    d, r = dy.double(), rstd.double()[:, None]
+    h = (x.double() - mean.double()[:, None]) * r
+    dw = lib.layer_norm_grad(dy, p, mean, rstd, torch.ones(width, device="cuda"))[1]
+    err = (n + 4) * U * (d * h).abs().sum(0)
+    assert bool(((dw.double() - (d * h).sum(0)).abs() <= err).all())
