@@ -495,7 +495,7 @@ typedef struct {
  * rule of float32 rows), for hiss_feed_forward_grad.  Sums are float32, on the tensor
  * cores, which cut at most 2^-23 of what an accumulator holds for every 16 columns; sums
  * leave it after at most 512 columns of x or 1024 of h (float32: 128) for additions to nearest.  h may be rounded to
- * dtype before the second product (float32: it is held to 24 bits), so in float16 a value
+ * dtype before the second product (float32: operands are held to 24 bits and to 2^-133), so in float16 a value
  * beyond 65504 may be an infinity there.  A row with an infinity or a NaN gives values
  * that are not finite, in float32 NaN where an infinity would be exact. */
 int hiss_feed_forward(hiss_ctx *ctx, const hiss_ffn *w, const void *d_x, int64_t x_stride, int64_t n, void *d_y,

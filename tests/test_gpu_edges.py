@@ -117,3 +117,20 @@ def test_norm_gradient_far_from_zero(lib, dtype):
     dw = lib.layer_norm_grad(dy, p, mean, rstd, torch.ones(width, device="cuda"))[1]
     err = (n + 4) * U * (d * h).abs().sum(0)
     assert bool(((dw.double() - (d * h).sum(0)).abs() <= err).all())
+
+
+@pytest.mark.parametrize("n", [1, 7, 16, 50, 600])
+@pytest.mark.parametrize("act", ["silu", "gelu", "sigmoid"])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_values_over_the_range(lib, dtype, act, n):
+    """y = act(a), from each of the block's kernels."""
+    largest = min(LARGEST[dtype], 12.0) if act == "gelu" else LARGEST[dtype]
+    e = torch.eye(2, dtype=dtype, device="cuda")
+    for part in _range(dtype, 600, largest).split(n)[::max(1, 600 // n // 40)]:
+        x = torch.stack((part, torch.ones_like(part)), 1)
+        y = lib.feed_forward(x, e[:1], e[1:], e[:1, :1], act=act)[:, 0].double()
+        a = part.double()
+        want = _terms(a, act)[0]
+        rel, sub = ROUND[dtype]  # of h, and of the result
+        bad = ~((y - want).abs() <= _relative(a, act, dtype) * want.abs() * (1 + 2 * rel) + 2 * (rel * want.abs() + sub))
+        assert not bool(bad.any()), [(float(a[i]), float(y[i]), float(want[i])) for i in torch.nonzero(bad).flatten()[:5]]
