@@ -85,6 +85,8 @@ __host__ __device__ constexpr int stages(int bn)
 {
     return (227 * 1024 - kBarrierBytes - 1024 - kEpilogueWarps * kRoomBytes<EP, P>) / stage_bytes<P>(bn);
 }
+static_assert(stages<kOut, 1>(256) == 6 && stages<kGated, 1>(256) == 6 && stages<kGrad, 1>(256) == 4, "16-bit");
+static_assert(stages<kOut, 3>(128) == 2 && stages<kGated, 3>(128) == 2 && stages<kGrad, 3>(128) == 2, "three planes");
 
 // One product D[m][n] = sum over its segments of A B^T, cut into tiles.
 struct Problem {
@@ -513,8 +515,8 @@ struct Unit {
 // Products on 256 x 256 tiles (256 x 128 of float32's planes) by pairs of CTAs, which share B: each
 // copies 128 rows of A and half of B's, so a stage of 64 columns is 32 KB a CTA for 512 cycles of
 // matrix instructions.  One CTA per SM and 128 x 256 would copy 48 KB for them, above the 64 bytes a
-// cycle that L2 gives an SM.  A CTA's warps: eight of the epilogue, one that copies (6 stages ahead; 5 and
-// 4 where the epilogue needs the room; 2 of three planes), one that issues.  Two accumulators of
+// cycle that L2 gives an SM.  A CTA's warps: eight of the epilogue, one that copies (6 stages; 4 where
+// da, db and h leave; 2 of three planes), one that issues.  Two accumulators of
 // 256 columns fill tensor memory, so a tile's epilogue runs beside the next one's products.
 // Persistent: 76 pairs take the tiles in groups of 8 tile rows (4, 16 and 32: within 1%).
 //
@@ -640,19 +642,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_produ
                             if constexpr (P == 1) {
                                 mma_f16_pair(d, ad + j * a_step, bd + j * b_step, idesc, in_fold + j > 0);
                             } else {
-                                // the planes of A in turn, so that each is read for its products once
                                 const uint32_t cross = d + 128;
-                                auto product = [&](auto keep, uint32_t to, int pa, int pb, bool add) {
-                                    mma_f16_pair<decltype(keep)::value>(to, ad + j * a_step + pa * a_plane, bd + j * b_step + pb * b_plane,
-                                                                        idesc, add);
+                                auto product = [&](uint32_t to, int pa, int pb, bool add) {
+                                    mma_f16_pair(to, ad + j * a_step + pa * a_plane, bd + j * b_step + pb * b_plane, idesc, add);
                                 };
                                 const bool more = in_fold + j > 0;
-                                product(std::integral_constant<int, kAFill>{}, d, 0, 0, more);
-                                product(std::integral_constant<int, kAUse>{}, cross, 0, 1, more);
-                                product(std::integral_constant<int, kALast>{}, cross, 0, 2, true);
-                                product(std::integral_constant<int, kAFill>{}, cross, 1, 0, true);
-                                product(std::integral_constant<int, kALast>{}, cross, 1, 1, true);
-                                product(std::integral_constant<int, kAOnce>{}, cross, 2, 0, true);
+                                product(d, 0, 0, more);
+                                product(cross, 0, 1, more);
+                                product(cross, 0, 2, true);
+                                product(cross, 1, 0, true);
+                                product(cross, 1, 1, true);
+                                product(cross, 2, 0, true);
                             }
                         }
                         mma_commit_pair(&empty[s]);

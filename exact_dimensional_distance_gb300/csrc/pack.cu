@@ -12,9 +12,9 @@ namespace hiss {
 namespace {
 
 constexpr int kThreads = 256;
-// Pieces that a thread loads before it uses the first: 65,536 x 4096 bfloat16 are packed in 148 us
-// with 4 and 156 with 2 or 8, unpacked in 124 with 8 and 131 with 4.
-constexpr int kPackAhead = 4, kUnpackAhead = 8, kLinesAhead = 1;
+// Pieces that a thread loads before it uses the first: 4 are 8 us faster than 2 or 8 for packing 65,536 x 4096
+// bfloat16, 8 are 7 us faster than 4 for unpacking it.
+constexpr int kPackAhead = 4, kUnpackAhead = 8;
 
 // A thread handles 8 columns, four neighbouring lanes a block: its columns are one
 // access of 16 bytes (two of float32), its codes one of 8 bytes.  65,536 x 4096 bfloat16: 137 us
@@ -93,48 +93,34 @@ __global__ void __launch_bounds__(kThreads) k_unpack_lines(const int8_t *codes, 
 {
     constexpr int E = 16 / sizeof(T);
     const int64_t total = n * per_row.d, step = (int64_t)gridDim.x * kThreads;
-    for (int64_t i0 = (int64_t)blockIdx.x * kThreads + threadIdx.x; i0 < total; i0 += kLinesAhead * step) {
-        T *row[kLinesAhead];
-        int col[kLinesAhead];  // the line's first column: -E + 1 .. and, in the last lines, behind the row
-        uint2 a[kLinesAhead], b[kLinesAhead];
-        uint32_t s0[kLinesAhead], s1[kLinesAhead];
+    for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < total; i += step) {
+        const int64_t r = per_row.quotient(i);
+        T *row = x + r * stride;
+        // the line's first column: -E + 1 .. and, in the last lines, behind the row
+        const int c = (int)(i - r * per_row.d) * E - (int)((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(T));
+        if (c >= width) continue;
+        const int8_t *q = codes + r * blocks * kPackBlock;
+        const int at = c & ~7, first = max(c, 0) / kPackBlock, last = min(c + E, width) - 1;
+        const uint2 a = at >= 0 ? *reinterpret_cast<const uint2 *>(q + at) : make_uint2(0, 0);
+        const uint2 b = at + 8 < blocks * kPackBlock ? *reinterpret_cast<const uint2 *>(q + at + 8) : make_uint2(0, 0);
+        const uint8_t *s = scales + r * blocks + first;
+        const float f0 = scale_of(s[0]), f1 = last / kPackBlock > first ? scale_of(s[1]) : f0;
+        const int sh = (c & 7) * 8, edge = (first + 1) * kPackBlock;
+        const uint64_t lo = a.x | (uint64_t)a.y << 32, hi = b.x | (uint64_t)b.y << 32;
+        const uint64_t w = sh ? lo >> sh | hi << (64 - sh) : lo;
+        float v[8];
+        values8(make_uint2((uint32_t)w, (uint32_t)(w >> 32)), 1.0f, v);
 #pragma unroll
-        for (int k = 0; k < kLinesAhead; ++k) {
-            const int64_t i = i0 + k * step, r = per_row.quotient(i < total ? i : 0);
-            row[k] = x + r * stride;
-            const int c = (int)(i - r * per_row.d) * E - (int)((reinterpret_cast<uintptr_t>(row[k]) & 15) / sizeof(T));
-            col[k] = i < total && c < width ? c : INT_MAX / 2;
-            if (col[k] >= width) continue;
-            const int8_t *q = codes + r * blocks * kPackBlock;
-            const int at = c & ~7, first = max(c, 0) / kPackBlock, last = min(c + E, width) - 1;
-            a[k] = at >= 0 ? *reinterpret_cast<const uint2 *>(q + at) : make_uint2(0, 0);
-            b[k] = at + 8 < blocks * kPackBlock ? *reinterpret_cast<const uint2 *>(q + at + 8) : make_uint2(0, 0);
-            const uint8_t *s = scales + r * blocks + first;
-            s0[k] = s[0];
-            s1[k] = last / kPackBlock > first ? s[1] : s0[k];
-        }
+        for (int e = 0; e < E; ++e) v[e] = __fmul_rn(v[e], c + e < edge ? f0 : f1);
+        if (c >= 0 && c <= width - E) {
+            Pack<T, E> p;
 #pragma unroll
-        for (int k = 0; k < kLinesAhead; ++k) {
-            const int c = col[k];
-            if (c >= width) continue;
-            const int sh = (c & 7) * 8, edge = (max(c, 0) / kPackBlock + 1) * kPackBlock;
-            const uint64_t lo = a[k].x | (uint64_t)a[k].y << 32, hi = b[k].x | (uint64_t)b[k].y << 32;
-            const uint64_t w = sh ? lo >> sh | hi << (64 - sh) : lo;
-            float v[8];
-            values8(make_uint2((uint32_t)w, (uint32_t)(w >> 32)), 1.0f, v);
-            const float f0 = scale_of(s0[k]), f1 = scale_of(s1[k]);
+            for (int e = 0; e < E; e += 2) set_pair(p.v + e, make_float2(v[e], v[e + 1]));
+            store_pack<T, E>(row + c, p);
+        } else {
 #pragma unroll
-            for (int e = 0; e < E; ++e) v[e] = __fmul_rn(v[e], c + e < edge ? f0 : f1);
-            if (c >= 0 && c <= width - E) {
-                Pack<T, E> p;
-#pragma unroll
-                for (int e = 0; e < E; e += 2) set_pair(p.v + e, make_float2(v[e], v[e + 1]));
-                store_pack<T, E>(row[k] + c, p);
-            } else {
-#pragma unroll
-                for (int e = 0; e < E; ++e)
-                    if (c + e >= 0 && c + e < width) row[k][c + e] = from_f32<T>(v[e]);
-            }
+            for (int e = 0; e < E; ++e)
+                if (c + e >= 0 && c + e < width) row[c + e] = from_f32<T>(v[e]);
         }
     }
 }
@@ -176,7 +162,7 @@ cudaError_t unpack(const hiss_packed &p, int64_t n, int width, void *x, int dtyp
                                                                                static_cast<T *>(x), stride);
         } else {
             const Divider per_row((width * (int)sizeof(T) + 14) / 16 + 1);
-            const unsigned grid = std::min(grid_for(n * per_row.d, kLinesAhead), 16u * kSMs);
+            const unsigned grid = std::min(grid_for(n * per_row.d, 1), 16u * kSMs);
             k_unpack_lines<T><<<grid, kThreads, 0, s>>>(p.codes, p.scales, n, width, blocks, per_row,
                                                                                 static_cast<T *>(x), stride);
         }

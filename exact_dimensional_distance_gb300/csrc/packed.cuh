@@ -166,14 +166,15 @@ struct Eight {
 #pragma unroll
             for (int j = 0; j < 8; ++j) m = max(m, w[j] & 0x7FFFFFFFu);
             return m;
-        }
+        } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) m = __vmaxu2(m, w[j] & 0x7FFF7FFFu);
-        m = max(m & 0xFFFFu, m >> 16);
-        const uint16_t h = (uint16_t)m;
-        T e;
-        memcpy(&e, &h, 2);
-        return __float_as_uint(to_f32(e));
+            for (int j = 0; j < 4; ++j) m = __vmaxu2(m, w[j] & 0x7FFF7FFFu);
+            m = max(m & 0xFFFFu, m >> 16);
+            const uint16_t h = (uint16_t)m;
+            T e;
+            memcpy(&e, &h, 2);
+            return __float_as_uint(to_f32(e));
+        }
     }
     __device__ __forceinline__ void get(const T *row, int col, int width, float (&v)[8]) const
     {

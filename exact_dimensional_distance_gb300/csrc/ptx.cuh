@@ -319,23 +319,13 @@ __host__ __device__ constexpr uint32_t idesc_f16(bool bf16, bool a_m_major, bool
 }
 
 // D[tmem of both CTAs] (+)= A B^T for one K step of 16 elements, issued by one thread of the
-// pair's first CTA: each CTA holds half of A's rows, half of B's, and its rows of D.  KEEP: what
-// becomes of A in the tensor core's buffer: products of the same A one after the other read it from
-// shared memory once.
-enum { kAOnce = 0, kAFill = 1, kAUse = 2, kALast = 3 };
-template <int KEEP = kAOnce>
+// pair's first CTA: each CTA holds half of A's rows, half of B's, and its rows of D.
 __device__ __forceinline__ void mma_f16_pair(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate)
 {
-#define HISS_MMA_PAIR(collector)                                                                            \
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"                                        \
-                 "tcgen05.mma.cta_group::2.kind::f16" collector " [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d), \
-                 "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)                                        \
-                 : "memory")
-    if constexpr (KEEP == kAFill) HISS_MMA_PAIR(".collector::a::fill");
-    else if constexpr (KEEP == kAUse) HISS_MMA_PAIR(".collector::a::use");
-    else if constexpr (KEEP == kALast) HISS_MMA_PAIR(".collector::a::lastuse");
-    else HISS_MMA_PAIR("");
-#undef HISS_MMA_PAIR
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),
+                 "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+                 : "memory");
 }
 // Arrive on the barrier at this address of both CTAs once every tcgen05 operation this
 // thread issued so far has completed.
