@@ -44,15 +44,15 @@ constexpr bool kMiddle = EP == kGrad || EP == kGradLong;
 // cut a sum towards zero at every step of 16 columns, up to 2^-23 of it: one accumulator for all of K is
 // off by 9e-10 per column in a and b, always to the same side of a sum that grows, so that codes that are
 // kept and signs that relu's derivative takes come out wrong.
-//   Three planes: 2.  8192 x 256 through 1024 is 8.8e-7 off the exact value with 4 (69 us), 5.4e-7 with 2 (70),
-//   3.7e-7 with 1 (79); float32 sums of plain products are 7.1e-7 off.
+//   Three planes: 2.  8192 x 256 through 1024 is 8.7e-7 off the exact value with 4 (61 us), 5.2e-7 with 2 (62),
+//   3.6e-7 with 1 (63); float32 sums of plain products are 7.2e-7 off.
 //   a and b: 4, but 8 in the two accumulators that the next tile fills beside this tile's epilogue.  4096 columns:
 //   bfloat16 are 3.3e-7 of the terms' 2-norm off so, 3.5e-6 with one accumulator (4.0e-7 in a library's float32
 //   product).  8192 x 2048 by 2 x 5632, kept in 8 bits: 253 us, 246 with one accumulator, 306 with 4 from the
 //   start, 248 with 8 throughout.
 //   Others round what they add up, or their terms, to 16 bits: 16 blocks lose up to 2^-18 of a sum of one sign, a
-//   128th of float16's half step.  dh up to 4096 columns: all, 2^-16, since registers for its sums
-//   cost its epilogue (54 us for 70 on 16,384 x 1024).
+//   128th of float16's half step.  dh up to 4096 columns: all, 2^-16, since sums in registers cost its
+//   epilogue (4104 columns of 8192 x 2048: 145 us, 129 in one accumulator).
 template <int EP, int P>
 __host__ __device__ constexpr int fold_blocks(int i)
 {
@@ -520,11 +520,11 @@ struct Unit {
 // 256 columns fill tensor memory, so a tile's epilogue runs beside the next one's products.
 // Persistent: 76 pairs take the tiles in groups of 8 tile rows (4, 16 and 32: within 1%).
 //
-// 32,768 x 2048 bfloat16 through 5632: gate and up 0.92 ms (1.65 PFLOP/s), down 0.45 ms (1.67);
-// tensor pipe 71% busy, and the library's best on this GPU is 1.9.  What bounds it: matrix
+// 32,768 x 2048 bfloat16 through 5632: gate and up 0.94 ms (1.61 PFLOP/s), down 0.46 ms (1.64);
+// tensor pipe 68 and 72% busy, and the library's best on this GPU is 1.9.  What bounds it: matrix
 // instructions and, next to them, the copies (45 bytes a cycle and SM).  Float32, 8192 x 256 by 2 x
-// 1024: 44 us, 70% of the six products' time; its backward middle (three results of three planes
-// for each sum) 73 us, bound by the epilogue.
+// 1024: 41 us, 27 of them the six products' at the library's rate; its backward middle (three results of three planes
+// for each sum) 66 to 70 us, bound by the epilogue.
 template <int EP, int P>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_product(const __grid_constant__ Args a)
 {
@@ -740,7 +740,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) k_produ
                 give_up();
                 break;
             }
-            // kGrad's long code once: unrolled, 54 us become 70 on 16,384 x 1024
+            // kGrad's long code once: for four groups, with sums, it took 70 us for 54 on 16,384 x 1024
 #pragma unroll(P == 1 && kMiddle<EP> ? 1 : kGroups)
             for (int g = 0; g < kGroups; ++g) {
                 const int64_t col = col0 + 32 * g;
@@ -1525,9 +1525,9 @@ struct Plan {
         const hiss_ffn &w = q.w;
         const int64_t n = q.n, f = w.hidden, d = w.width, o = w.out_width;
         // the tiles' time grows with rows and weights, that of the large products (20 us and up) hardly
-        // with the rows: 16 rows of bfloat16 through 1024 x 4096 take 19 and 24 us, 64 rows 35 and 25,
-        // 16 through 4096 x 11008 105 and 79
-        // (float32: 32 rows through 1024 x 4096 55 and 61, through 4096 x 11008 430 and 534, 48 rows 91 and 61)
+        // with the rows: 16 rows of bfloat16 through 1024 x 4096 take 19 and 23 us, 64 rows 37 and 23,
+        // 16 through 4096 x 11008 105 and 81
+        // (float32: 16 rows through 1024 x 4096 39 and 56, 32 rows 56 and 56, through 4096 x 11008 455 and 523)
         const bool tiles = planes == 3 ? n <= 32 : n <= kTileRows && n * f * (2 * d + o) <= int64_t(3) << 27;
         if (tiles || n <= kFewRows<__half>) return with_dtype(dtype, [&](auto t) { return few<decltype(t)>(); });
         const Operand x = matrix(q.g.x, q.g.x_stride, n, d), gate = matrix(w.gate, w.gate_stride, f, d);
