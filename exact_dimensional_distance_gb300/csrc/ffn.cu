@@ -948,11 +948,13 @@ cudaError_t launch(const Args &a, bool after, cudaStream_t s, int64_t *launches)
     constexpr size_t smem = 227 * 1024;
     HISS_TRY(allow_shared(k_product<EP, P>, smem, done));
     // a block of fewer would wait for registers that it does not have
-    static const int registers = [] {
+    static std::atomic<int> registers{0};
+    if (registers.load(std::memory_order_relaxed) == 0) {
         cudaFuncAttributes at{};
-        return cudaFuncGetAttributes(&at, k_product<EP, P>) == cudaSuccess ? at.numRegs : 0;
-    }();
-    if (registers != kLaunchRegs) return cudaErrorLaunchOutOfResources;
+        HISS_TRY(cudaFuncGetAttributes(&at, k_product<EP, P>));
+        registers.store(at.numRegs, std::memory_order_relaxed);
+    }
+    if (registers.load(std::memory_order_relaxed) != kLaunchRegs) return cudaErrorLaunchOutOfResources;
     const int units = a.tiles * a.splits;
     const unsigned grid = 2 * std::min(units, kPairs);
     ++*launches;

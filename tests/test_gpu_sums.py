@@ -143,6 +143,34 @@ def test_gradients_of_wide_blocks_with_relu(lib, dtype, keep):
         assert off <= 1.5 * 2 ** 0.5 * ROUNDING * HALF[dtype], name
 
 
+# ---- where accumulators change -----------------------------------------------------
+
+#                                   whole accumulators, one block or one column more or less; ranges of K and none
+@pytest.mark.parametrize("n,d,f,o", [(300, 512, 1024, 5200), (300, 513, 1025, 5200), (300, 1024, 2048, 5200), (300, 1025, 2049, 5200),
+                                     (300, 1279, 3000, 200), (300, 1280, 1088, 200), (300, 1281, 960, 5200), (100, 1600, 130, 4096),
+                                     (100, 65, 130, 4097), (70, 64, 200, 6145)])
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_sums_of_every_length(lib, dtype, n, d, f, o):
+    """The value and all gradients, computed again and from kept rows, in norm: within 1.5 times their two roundings."""
+    g = _gen(n, d, f, o, str(dtype))
+    x, dy = _normal((n, d), dtype, g), _normal((n, o), dtype, g, 0.5)
+    gate, up, down = _normal((f, d), dtype, g, d ** -0.5), _normal((f, d), dtype, g, d ** -0.5), _normal((o, f), dtype, g, f ** -0.5)
+    y, kept = lib.feed_forward(x, gate, up, down, act="silu", keep=True)
+    xd, gd, ud, dd, v = (t.double() for t in (x, gate, up, down, dy))
+    for keep in (None, kept):
+        a, b = (xd @ gd.t(), xd @ ud.t()) if keep is None else (lib.unpack(k).double() for k in keep)
+        s = torch.sigmoid(a)
+        if keep is None:
+            off = float((y.double() - (a * s * b) @ dd.t()).norm() / ((a * s * b) @ dd.t()).norm())
+            assert off <= 1.5 * 2 ** 0.5 * ROUNDING * HALF[dtype], "y"
+        dh = v @ dd
+        da, db = dh * b * s * (1 + a * (1 - s)), dh * a * s
+        want = (da @ gd + db @ ud, da.t() @ xd, db.t() @ xd, v.t() @ (a * s * b))
+        for name, t, w in zip(("dx", "dgate", "dup", "ddown"), lib.feed_forward_grad(dy, x, gate, up, down, act="silu", kept=keep), want):
+            off = float((t.double() - w).norm() / w.norm())
+            assert off <= 1.5 * 2 ** 0.5 * ROUNDING * HALF[dtype], name
+
+
 # ---- terms of one sign --------------------------------------------------------------
 
 # Ranges of 1024 columns, of 64 steps: a step loses at most 2^-23 of the range's sum so far, which is half of it
